@@ -4,7 +4,7 @@ read-back, and attention over it.
 The cache holds 8-bit codes with one fp32 scale for each (block of tokens, KV head).  Codes are stored in tiles of
 16 tokens, in the order a wave's matrix operands want them; for a token t of a tile and a channel d
     K: byte  (d / 64) * 1024 + (d / 16 % 4) * 256 + t * 16 + d % 16
-    V: byte  (d / 64) * 1024 + (t / 4) * 256 + (d % 16) * 16 + (d / 16 % 4) * 4 + t % 4
+    V: byte  (d / 64) * 1024 + (t / 4) * 256 + (d / 4 % 16) * 16 + d % 4 * 4 + t % 4
 `own` false computes every operator in elementary torch operations in 32 bits, `own` true calls the library.
 """
 import numpy as np
@@ -353,8 +353,8 @@ def _k_rows(x, case, back=False):
 def _v_rows(x, case, back=False):
     bs, d = case["bs"], case["d"]
     if back:
-        return x.unflatten(-1, (d // 64, 4, 16)).unflatten(-4, (bs // 16, 4, 4)).permute(0, 1, 2, 5, 3, 7, 6, 4).flatten(2)
-    return x.unflatten(-1, (bs // 16, d // 64, 4, 16, 4, 4)).permute(0, 1, 2, 4, 7, 3, 6, 5).flatten(5).flatten(2, 4)
+        return x.unflatten(-1, (d // 64, 16, 4)).unflatten(-4, (bs // 16, 4, 4)).permute(0, 1, 2, 5, 3, 6, 7, 4).flatten(2)
+    return x.unflatten(-1, (bs // 16, d // 64, 4, 16, 4, 4)).permute(0, 1, 2, 4, 7, 3, 5, 6).flatten(5).flatten(2, 4)
 
 
 def _k_at(case, t):
@@ -367,7 +367,7 @@ def _k_at(case, t):
 def _v_at(case, t):
     c = torch.arange(case["d"], device=DEV)
     t = t[:, None]
-    return t // 16 * (16 * case["d"]) + c // 64 * 1024 + t % 16 // 4 * 256 + c % 16 * 16 + c // 16 % 4 * 4 + t % 4
+    return t // 16 * (16 * case["d"]) + c // 64 * 1024 + t % 16 // 4 * 256 + c // 4 % 16 * 16 + c % 4 * 4 + t % 4
 
 
 def _values(codes, fmt):
