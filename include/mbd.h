@@ -320,6 +320,148 @@ mbd_status mbd_encode_cassandra(const uint16_t* w, const float* act_norm, int64_
                                 int32_t keep_num, int32_t keep_den, const mbd_encode_plan_t* plan,
                                 void* const* sec, void* ws, uint64_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ KV cache
+ * The other half of what a decode step reads: a paged cache of 8-bit keys and values.
+ * A pool of n_blocks blocks holds block_size tokens each; a request's block table
+ * names its blocks in order.  Each (block, KV head) has one fp32 scale for its keys
+ * and one for its values; a value is code * scale.
+ *
+ * Formats, x the value to store, s the scale, amax the largest finite |x| among the
+ * tokens that one call brings to a (block, head):
+ *   MBD_KV_INT8  code = clamp(rne(x / s), -127, 127); wanted s = amax * (1/127), the
+ *                constant rounded to fp32, quotient and product rounded to fp32.
+ *   MBD_KV_E4M3  code = e4m3fn(x / s), nearest even, saturating at 448; wanted s =
+ *                the smallest power of two, at least 2^-126, with amax <= 448 s.
+ * amax = 0 wants s = 0 (codes 0).  NaN is stored as 0; an infinity as the largest code.
+ * A slot is block * block_size + place in the block.  A block's tokens are appended
+ * in order, so a token at place o finds o live tokens before it: the first call that
+ * reaches a block at place 0 sets the wanted scale; later calls take
+ * s' = max(s, wanted), and where that is larger than s the live codes become
+ * rne(code * fl32(s / s')) (for E4M3 a power of two, so exact above its subnormals).
+ *
+ * Codes: uint8 [n_blocks][n_heads][block_size/16] tiles of 16 tokens x head_dim, in the
+ * order in which a wave's 64 lanes feed them to the matrix cores 16 bytes each.  Byte
+ * of (token t of the tile, channel d):
+ *   keys    (d/64)*1024 + (d/16%4)*256 + t*16 + d%16
+ *   values  (d/64)*1024 + (t/4)*256 + (d/4%16)*16 + d%4*4 + t%4
+ * Scales: fp32 [n_blocks][n_heads].  None of it needs to be cleared before use.  */
+typedef enum { MBD_KV_INT8 = 1, MBD_KV_E4M3 = 2 } mbd_kv_format;
+typedef enum { MBD_BF16 = 1, MBD_F32 = 2 } mbd_dtype;
+
+typedef struct {
+    int32_t fmt;          /* mbd_kv_format                              */
+    int32_t block_size;   /* tokens a block: 16, 32, 64, 128 or 256     */
+    int32_t n_heads;      /* KV heads, 1..65535                         */
+    int32_t head_dim;     /* 64, 128, 192 or 256                        */
+    int64_t n_blocks;     /* n_blocks * block_size < 2^31               */
+    void* k_codes;        /* device, 16-byte aligned; offsets may pass  */
+    void* v_codes;        /*   32 bits                                  */
+    float* k_scale;       /* device, 4-byte aligned                     */
+    float* v_scale;
+} mbd_kv_cache;
+
+/* Block tables of n_seqs requests over one pool, and its free blocks as a stack:
+ * free_blocks[0 .. n_free) are free, the last is taken first. */
+typedef struct {
+    int32_t n_seqs;       /* 1..4096                                    */
+    int32_t block_size;   /* 16, 32, 64, 128 or 256                     */
+    int32_t max_blocks;   /* columns of the block table                 */
+    int32_t n_blocks;     /* length of free_blocks; ids are below it    */
+    int32_t* block_table; /* device [n_seqs][max_blocks]                */
+    int32_t* free_blocks; /* device [n_blocks]                          */
+} mbd_kv_pool;
+
+/* One step's bookkeeping, from request lengths, in one call: which blocks each request
+ * gets, and where each of its new tokens goes.  All arrays are device int32.
+ *   in   new_tokens [n_seqs]  tokens that the request brings; negative: it has ended,
+ *                             and its blocks go back to the pool
+ *        lens [n_seqs]        tokens it has cached; held [n_seqs] blocks it holds
+ *        n_free [1]
+ *   out  seq_start [n_seqs+1] exclusive prefix sum of max(new_tokens, 0), at most T:
+ *                             the rows of the step's packed [T] token batch
+ *        slots [T]            slot of each new token; -1 for tokens of a request that
+ *                             is not served and for rows past seq_start[n_seqs]
+ *        positions [T]        its place in its request (lens + j), or -1; may be NULL
+ *        lens_out, held_out [n_seqs], n_free_out [1]: after the step (may be the
+ *                             same buffers as lens, held, n_free)
+ *        status [n_seqs]      0 served, or nothing to do; 1 the pool has too few
+ *                             blocks; 2 more than max_blocks columns; 3 its tokens end
+ *                             past T; 4 lens or held cannot be (negative, held above
+ *                             max_blocks, lens above held blocks' tokens)
+ * Ended requests' blocks are pushed in request order, each in table order, before any
+ * is taken.  Requests take blocks in order, all that they need or none: one is served
+ * if it needs none, or if what it and the requests before it need (those of status 1
+ * among them) is there.  A request not served keeps lens, held and its table row.
+ * Rows of ended requests stay as they were, with lens_out = held_out = 0.  A request
+ * whose lens was lowered (rejected drafts) keeps its blocks and fills them again.
+ * Errors: EINVAL (NULL), ESHAPE (n_seqs, block_size, max_blocks or n_blocks < 1,
+ * either times block_size 2^31 or more, T < 0), EALIGN (4 bytes), EHIP. */
+mbd_status mbd_kv_slots(const mbd_kv_pool* pool, const int32_t* new_tokens, const int32_t* lens,
+                        const int32_t* held, const int32_t* n_free, int32_t T, int32_t* seq_start,
+                        int32_t* slots, int32_t* positions, int32_t* lens_out, int32_t* held_out,
+                        int32_t* n_free_out, int32_t* status, void* stream);
+
+/* Quantise T tokens' keys and values into the cache (rules above).  k, v: device
+ * [T][n_heads][head_dim] of dtype (MBD_BF16 or MBD_F32, e.g. rows of mbd_gemv's y),
+ * 16-byte aligned; k_stride, v_stride: elements from one token to the next, multiples
+ * of 8, at least n_heads * head_dim (so both may be slices of one projection).  slots
+ * [T] device int32: the slot of each token; a slot outside the cache skips its token.
+ * The tokens that a call brings to one block stand next to each other in rising slots
+ * (as mbd_kv_slots writes them); otherwise that block's codes and scale are unspecified.
+ * T = 0 does nothing; T is at most 2^24.  Errors: EINVAL, ESHAPE, EALIGN, EHIP. */
+mbd_status mbd_kv_append(const mbd_kv_cache* cache, const void* k, const void* v, int32_t dtype,
+                         int64_t k_stride, int64_t v_stride, const int32_t* slots, int32_t T,
+                         void* stream);
+
+/* Dense keys and values of cached tokens: k_out, v_out [T][n_heads][head_dim] of dtype,
+ * 16-byte aligned: code * scale in fp32, then rounded to dtype.  Any slots in any order;
+ * rows of slots outside the cache stay as they were.  Errors as mbd_kv_append. */
+mbd_status mbd_kv_gather(const mbd_kv_cache* cache, const int32_t* slots, int32_t T, int32_t dtype,
+                         void* k_out, void* v_out, void* stream);
+
+/* Attention of each request's newest tokens over its cache, causal:
+ *   u_ij = cap(scale * q_i . k_j) + slope_h * (j - i),  cap(x) = softcap * tanh(x / softcap)
+ *   o_i  = sum_j softmax_j(u_ij) v_j   over j <= i, i - j < window, j in a block with an id
+ * i, j positions in the request.  softcap = 0: no cap; window = 0: no window; slopes
+ * NULL: no distance bias. */
+typedef struct {
+    int32_t n_heads;      /* query heads, a multiple of the cache's; query head h reads
+                             KV head h / (n_heads / cache n_heads)                      */
+    int32_t n_seqs;       /* 1..4096                                                    */
+    int32_t max_blocks;   /* columns of the block table                                 */
+    int32_t T;            /* rows of q, out and lse                                     */
+    int32_t max_new;      /* most new tokens of one request, >= 1: 1 for decode, N+1 to
+                             verify N drafts, more for prompts                          */
+    int32_t window;       /* >= 0                                                       */
+    float scale, softcap; /* finite; softcap >= 0                                       */
+    const float* slopes;  /* device fp32 [n_heads], or NULL                             */
+    int64_t q_stride;     /* elements from one token's row to the next, a multiple of 8 */
+    int64_t out_stride;   /*   and at least n_heads * head_dim                          */
+} mbd_kv_attn_args;
+
+/* seq_start [n_seqs+1], lens [n_seqs], block_table [n_seqs][max_blocks]: device int32.
+ * Request i's queries are rows seq_start[i] .. seq_start[i+1] of q [T][n_heads][head_dim]
+ * (bf16, 16-byte aligned); they are its last tokens: row j of n_i stands at position
+ * lens[i] - n_i + j, its own key and value already appended.  lens is taken as at most
+ * max_blocks * block_size, seq_start as within [0, T].  Block ids outside the cache
+ * are left out, as if masked.  A query that sees nothing (position below 0, all
+ * blocks left out) gets o = 0, lse = -inf.  out bf16 [T][n_heads][head_dim], 16-byte
+ * aligned: as the x of mbd_gemv where out_stride = n_heads * head_dim.  lse fp32
+ * [T][n_heads], natural logarithm of the softmax's sum, or NULL.  Rows of no request,
+ * and a request's rows past its first max_new, stay as they were.  Sums and
+ * statistics are fp32; softmax weights times value scales enter the second product
+ * as bf16.  The order of every sum depends on the arguments alone.
+ * ws: device workspace of mbd_kv_attn_workspace_bytes, 16-byte aligned, contents
+ * overwritten; may be NULL where that is 0.  Calls that share a workspace must not
+ * overlap.  Errors: EINVAL, ESHAPE (T above 2^24, max_blocks * block_size above 2^30,
+ * n_seqs * max_blocks * block_size / 16 of 2^31 or more, KV heads times tiles of query
+ * rows above 65535), EALIGN, EHIP. */
+mbd_status mbd_kv_attn_workspace_bytes(const mbd_kv_cache* cache, int32_t n_heads, int32_t n_seqs,
+                                       int32_t max_new, int32_t max_blocks, uint64_t* bytes);
+mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, const uint16_t* q,
+                       const int32_t* seq_start, const int32_t* lens, const int32_t* block_table,
+                       uint16_t* out, float* lse, void* ws, uint64_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ measurement aid
  * Streaming-read probe, not a step of the method: reads `bytes` of device memory at
  * src (16-byte aligned, a multiple of 16) with `blocks` x `threads` threads (threads

@@ -15,6 +15,7 @@ from ._native import (  # noqa: F401
     MBD_CASSANDRA, MBD_EALIGN, MBD_EFORMAT, MBD_EHIP, MBD_EINVAL, MBD_ENOMEM, MBD_ERANGE,
     MBD_CASSANDRA_MX, MBD_ESHAPE, MBD_INT4_G128, MBD_MX32, MBD_OK, MBD_TERNARY_B128, MBD_TERNARY_SKIP, MbdDWeights, MbdError,
     MbdEncodePlan, MbdPackParams, MbdSection, MbdStats, check, lib,
+    MBD_BF16, MBD_F32, MBD_KV_E4M3, MBD_KV_INT8, MbdKvAttnArgs, MbdKvCache, MbdKvPool,
 )
 
 SECTION_NAMES = {
@@ -204,6 +205,165 @@ def mbd_encode_cassandra(w, act_norm, keep_num: int, keep_den: int, plan: MbdEnc
     arr = (ctypes.c_void_p * 8)(*[t.data_ptr() for t in sections])
     check(lib().mbd_encode_cassandra(_ptr(w), _ptr(act_norm), M, K, keep_num, keep_den, ctypes.byref(plan), arr, _ptr(ws),
                                      ws.numel() * ws.element_size(), _stream(stream)), "mbd_encode_cassandra")
+
+
+# ------------------------------------------------------------------ KV cache
+
+def _on_device(**tensors):
+    """Every tensor on the current GPU, whose stream the call takes."""
+    import torch
+    here = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for name, t in tensors.items():
+        if t is not None and (t.device.type != "cuda" or t.device.index != here):
+            raise ValueError("%s is on %s, not on the current GPU" % (name, t.device))
+
+
+def _ints(n=None, **tensors):
+    """Contiguous int32 tensors, of n values where n is given."""
+    import torch
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n):
+            raise ValueError("%s must be a contiguous int32 tensor%s" % (name, "" if n is None else " of %d values" % n))
+
+
+def _rows(name, t, heads, dim, dtypes):
+    """[T][heads][dim] with dense rows; returns the elements from one token to the next."""
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim) or t.dtype not in dtypes:
+        raise ValueError("%s must be [T][%d][%d] of %s" % (name, heads, dim, " or ".join(str(d) for d in dtypes)))
+    if (heads > 1 and t.stride(1) != dim) or t.stride(2) != 1:
+        raise ValueError("%s: one token's heads must be dense" % name)
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * dim)
+
+
+class KvCache:
+    """An 8-bit paged KV cache over the caller's device tensors: codes uint8
+    [n_blocks][n_heads][block_size * head_dim] in the tile order of mbd.h, scales fp32
+    [n_blocks][n_heads].  Holds the tensors and the mbd_kv_cache that points at them."""
+
+    def __init__(self, fmt: int, block_size: int, head_dim: int, k_codes, v_codes, k_scale, v_scale):
+        import torch
+        if k_codes.dim() != 3 or k_codes.shape[2] != block_size * head_dim:
+            raise ValueError("codes must be [n_blocks][n_heads][block_size * head_dim]")
+        for t, shape, dtype in ((k_codes, k_codes.shape, torch.uint8), (v_codes, k_codes.shape, torch.uint8),
+                                (k_scale, k_codes.shape[:2], torch.float32), (v_scale, k_codes.shape[:2], torch.float32)):
+            if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+                raise ValueError("codes are contiguous uint8 tensors of one shape, scales contiguous fp32 [n_blocks][n_heads]")
+        _on_device(k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale)
+        self.tensors = dict(k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale)
+        self.fmt, self.block_size, self.n_heads, self.head_dim = fmt, block_size, k_codes.shape[1], head_dim
+        self.n_blocks = k_codes.shape[0]
+        self.desc = MbdKvCache(fmt, block_size, self.n_heads, head_dim, self.n_blocks, k_codes.data_ptr(), v_codes.data_ptr(),
+                               k_scale.data_ptr(), v_scale.data_ptr())
+
+    @classmethod
+    def empty(cls, fmt: int, n_blocks: int, n_heads: int, head_dim: int, block_size: int, device="cuda"):
+        import torch
+        codes = [torch.empty((n_blocks, n_heads, block_size * head_dim), dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.empty((n_blocks, n_heads), dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(fmt, block_size, head_dim, *codes, *scales)
+
+    def ref(self):
+        return ctypes.byref(self.desc)
+
+
+class KvPool:
+    """Block tables int32 [n_seqs][max_blocks] and the stack of free blocks int32 [n_blocks]."""
+
+    def __init__(self, block_size: int, block_table, free_blocks):
+        if block_table.dim() != 2 or free_blocks.dim() != 1:
+            raise ValueError("block_table must be [n_seqs][max_blocks], free_blocks [n_blocks]")
+        _ints(block_table=block_table, free_blocks=free_blocks)
+        _on_device(block_table=block_table, free_blocks=free_blocks)
+        self.block_table, self.free_blocks, self.block_size = block_table, free_blocks, block_size
+        self.n_seqs, self.max_blocks = block_table.shape
+        self.desc = MbdKvPool(self.n_seqs, block_size, self.max_blocks, free_blocks.shape[0], block_table.data_ptr(),
+                              free_blocks.data_ptr())
+
+    def ref(self):
+        return ctypes.byref(self.desc)
+
+
+def mbd_kv_slots(pool: KvPool, new_tokens, lens, held, n_free, seq_start, slots, positions, lens_out, held_out, n_free_out,
+                 status, stream=None) -> None:
+    """One step's block tables, slot map and ragged starts from request lengths; slots has
+    one value for each row of the step's token batch, positions may be None."""
+    n = pool.n_seqs
+    _ints(n, new_tokens=new_tokens, lens=lens, held=held, lens_out=lens_out, held_out=held_out, status=status)
+    _ints(1, n_free=n_free, n_free_out=n_free_out)
+    _ints(n + 1, seq_start=seq_start)
+    _ints(slots=slots)
+    _ints(slots.numel(), positions=positions)
+    _on_device(new_tokens=new_tokens, lens=lens, held=held, n_free=n_free, seq_start=seq_start, slots=slots, positions=positions,
+               lens_out=lens_out, held_out=held_out, n_free_out=n_free_out, status=status)
+    check(lib().mbd_kv_slots(pool.ref(), _ptr(new_tokens), _ptr(lens), _ptr(held), _ptr(n_free), slots.numel(), _ptr(seq_start),
+                             _ptr(slots), None if positions is None else _ptr(positions), _ptr(lens_out), _ptr(held_out),
+                             _ptr(n_free_out), _ptr(status), _stream(stream)), "mbd_kv_slots")
+
+
+def mbd_kv_append(cache: KvCache, k, v, slots, stream=None) -> None:
+    """Quantise k, v [T][n_heads][head_dim] (bf16 or fp32; rows may be slices) into their slots."""
+    import torch
+    kinds = (torch.bfloat16, torch.float32)
+    ks, vs = _rows("k", k, cache.n_heads, cache.head_dim, kinds), _rows("v", v, cache.n_heads, cache.head_dim, kinds)
+    if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must be alike")
+    _ints(k.shape[0], slots=slots)
+    _on_device(k=k, v=v, slots=slots)
+    check(lib().mbd_kv_append(cache.ref(), _ptr(k), _ptr(v), MBD_BF16 if k.dtype == torch.bfloat16 else MBD_F32, ks, vs, _ptr(slots),
+                              k.shape[0], _stream(stream)), "mbd_kv_append")
+
+
+def mbd_kv_gather(cache: KvCache, slots, k_out, v_out, stream=None) -> None:
+    """Dense keys and values [T][n_heads][head_dim] (bf16 or fp32) of the tokens in ``slots``."""
+    import torch
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _rows(name, t, cache.n_heads, cache.head_dim, (torch.bfloat16, torch.float32))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+    if k_out.dtype != v_out.dtype or k_out.shape != v_out.shape:
+        raise ValueError("k_out and v_out must be alike")
+    _ints(k_out.shape[0], slots=slots)
+    _on_device(slots=slots, k_out=k_out, v_out=v_out)
+    check(lib().mbd_kv_gather(cache.ref(), _ptr(slots), k_out.shape[0], MBD_BF16 if k_out.dtype == torch.bfloat16 else MBD_F32,
+                              _ptr(k_out), _ptr(v_out), _stream(stream)), "mbd_kv_gather")
+
+
+def mbd_kv_attn_workspace_bytes(cache: KvCache, n_heads: int, n_seqs: int, max_new: int, max_blocks: int) -> int:
+    b = ctypes.c_uint64(0)
+    check(lib().mbd_kv_attn_workspace_bytes(cache.ref(), n_heads, n_seqs, max_new, max_blocks, ctypes.byref(b)),
+          "mbd_kv_attn_workspace_bytes")
+    return int(b.value)
+
+
+def mbd_kv_attn(cache: KvCache, q, seq_start, lens, block_table, out, ws=None, max_new: int = 1, scale: float | None = None,
+                softcap: float = 0.0, window: int = 0, slopes=None, lse=None, stream=None) -> None:
+    """Causal attention of the requests' newest tokens q [T][n_heads][head_dim] bf16 over
+    their cached tokens, into out (alike; rows may be slices) and lse fp32 [T][n_heads].
+    scale defaults to head_dim ** -0.5."""
+    import torch
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError("q and out must be [T][n_heads][head_dim]")
+    heads = q.shape[1]
+    qs, outs = (_rows(name, t, heads, cache.head_dim, (torch.bfloat16,)) for name, t in (("q", q), ("out", out)))
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [n_seqs][max_blocks]")
+    n, width = block_table.shape
+    _ints(block_table=block_table)
+    _ints(n, lens=lens)
+    _ints(n + 1, seq_start=seq_start)
+    for name, t, shape in (("lse", lse, tuple(q.shape[:2])), ("slopes", slopes, (heads,))):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError("%s must be a contiguous fp32 tensor %s" % (name, list(shape)))
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    _on_device(q=q, seq_start=seq_start, lens=lens, block_table=block_table, out=out, ws=ws, slopes=slopes, lse=lse)
+    args = MbdKvAttnArgs(heads, n, width, q.shape[0], max_new, window, cache.head_dim ** -0.5 if scale is None else scale, softcap,
+                         None if slopes is None else slopes.data_ptr(), qs, outs)
+    check(lib().mbd_kv_attn(cache.ref(), ctypes.byref(args), _ptr(q), _ptr(seq_start), _ptr(lens), _ptr(block_table), _ptr(out),
+                            None if lse is None else _ptr(lse), None if ws is None else _ptr(ws),
+                            0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), "mbd_kv_attn")
 
 
 def mbd_probe_stream_read(src, sink, blocks: int, threads: int, stream=None) -> None:

@@ -3,13 +3,15 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, Structure, c_char_p, c_double, c_int32, c_int64, c_uint16, c_uint64, c_void_p
+from ctypes import POINTER, Structure, c_char_p, c_double, c_float, c_int32, c_int64, c_uint16, c_uint64, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmbd.so")
 
 MBD_OK, MBD_EINVAL, MBD_ESHAPE, MBD_EALIGN, MBD_ERANGE, MBD_EFORMAT, MBD_EHIP, MBD_ENOMEM = range(8)
 MBD_TERNARY_B128, MBD_INT4_G128, MBD_CASSANDRA, MBD_MX32, MBD_TERNARY_SKIP, MBD_CASSANDRA_MX = 1, 2, 3, 4, 5, 6
 MBD_MAX_SECTIONS = 8
+MBD_KV_INT8, MBD_KV_E4M3 = 1, 2
+MBD_BF16, MBD_F32 = 1, 2
 
 
 class MbdPackParams(Structure):
@@ -42,6 +44,23 @@ class MbdEncodePlan(Structure):
                 ("reserved", c_int32), ("bytes", c_uint64 * 8), ("padded_bytes", c_uint64 * 8)]
 
 
+class MbdKvCache(Structure):
+    _fields_ = [("fmt", c_int32), ("block_size", c_int32), ("n_heads", c_int32), ("head_dim", c_int32),
+                ("n_blocks", c_int64), ("k_codes", c_void_p), ("v_codes", c_void_p), ("k_scale", c_void_p),
+                ("v_scale", c_void_p)]
+
+
+class MbdKvPool(Structure):
+    _fields_ = [("n_seqs", c_int32), ("block_size", c_int32), ("max_blocks", c_int32), ("n_blocks", c_int32),
+                ("block_table", c_void_p), ("free_blocks", c_void_p)]
+
+
+class MbdKvAttnArgs(Structure):
+    _fields_ = [("n_heads", c_int32), ("n_seqs", c_int32), ("max_blocks", c_int32), ("T", c_int32), ("max_new", c_int32),
+                ("window", c_int32), ("scale", c_float), ("softcap", c_float), ("slopes", c_void_p),
+                ("q_stride", c_int64), ("out_stride", c_int64)]
+
+
 SIGNATURES = {
     "mbd_pack": (c_int32, [c_int32, POINTER(c_uint16), c_int64, c_int64, c_void_p,
                            POINTER(MbdPackParams), POINTER(c_void_p)]),
@@ -64,6 +83,12 @@ SIGNATURES = {
                                   POINTER(MbdEncodePlan), c_void_p]),
     "mbd_encode_cassandra": (c_int32, [c_void_p, c_void_p, c_int64, c_int64, c_int32, c_int32,
                                        POINTER(MbdEncodePlan), POINTER(c_void_p), c_void_p, c_uint64, c_void_p]),
+    "mbd_kv_slots": (c_int32, [POINTER(MbdKvPool)] + [c_void_p] * 4 + [c_int32] + [c_void_p] * 8),
+    "mbd_kv_append": (c_int32, [POINTER(MbdKvCache), c_void_p, c_void_p, c_int32, c_int64, c_int64, c_void_p, c_int32,
+                                c_void_p]),
+    "mbd_kv_gather": (c_int32, [POINTER(MbdKvCache), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p]),
+    "mbd_kv_attn_workspace_bytes": (c_int32, [POINTER(MbdKvCache), c_int32, c_int32, c_int32, c_int32, POINTER(c_uint64)]),
+    "mbd_kv_attn": (c_int32, [POINTER(MbdKvCache), POINTER(MbdKvAttnArgs)] + [c_void_p] * 7 + [c_uint64, c_void_p]),
     "mbd_probe_stream_read": (c_int32, [c_void_p, c_uint64, c_void_p, c_int32, c_int32, c_void_p]),
     "mbd_status_str": (c_char_p, [c_int32]),
     "mbd_last_error": (c_char_p, []),

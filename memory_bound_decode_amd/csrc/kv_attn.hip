@@ -1,0 +1,643 @@
+// Attention over the paged 8-bit KV cache ([Bolt] background: a decode step's time is
+// the bytes it reads; next to the weights those are the cached keys and values).
+//
+// Per KV head the query rows of one request (its new tokens times the query heads that
+// share the head) are the columns of both matrix products, the cached tokens the rows:
+//   S^T [tokens][rows] = K [tokens][d] Q^T,  O^T [d][rows] += V^T [d][tokens] P^T
+// with v_mfma_f32_16x16x32_bf16.  A lane's accumulators of S^T (4 tokens of a 16-token
+// tile, for one row) are then its own B operand of the second product, two tiles being
+// one k step of 32: nothing crosses lanes but the row maxima.  The cache stores each
+// tile as the lanes' A operands, so a wave reads whole KBs, and codes become bf16
+// (exact for int8 and e4m3) on their way into the product; the block's scale is one
+// factor of the 16 x 16 scores, or of the weights.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "kv_common.h"
+
+namespace mbd {
+namespace kv {
+
+constexpr int kWaves = 4;              // waves of a workgroup; each takes every fourth step
+constexpr int kStep = 2;               // tiles of one step: 32 tokens, the k of an MFMA
+constexpr int kRefill = 64 / kStep;    // steps whose block ids and scales one lane each holds
+constexpr int kMaxSeqs = 4096;
+constexpr int kMinChunk = 8;           // tiles: a workgroup's least share of a request
+constexpr int kTargetBlocks = 1024;    // workgroups that a call aims at
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+struct AttnArgs {
+    const uint8_t *k, *v;
+    const float *k_scale, *v_scale;
+    const uint16_t* q;
+    const int32_t *seq_start, *lens, *table;
+    uint16_t* out;
+    float *lse, *part_o, *part_ml;
+    const float* slopes;
+    int64_t q_stride, out_stride;
+    int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, target;
+    float scale, softcap;
+};
+
+// ---------------------------------------------------------------- shares of the work
+
+// A request as its workgroups see it.
+struct Seq {
+    int32_t row0, n_new, rows;   // first row of q, new tokens, rows a KV head (up to max_new tokens)
+    int32_t p0;                  // position of its first new token (below 0: before its start)
+    int32_t lo, hi;              // tiles that any of its queries sees
+    int32_t len;
+};
+
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int i) {
+    Seq s;
+    s.row0 = min(max(a.seq_start[i], 0), a.T);
+    s.n_new = min(max(a.seq_start[i + 1], s.row0), a.T) - s.row0;
+    s.len = min(max(a.lens[i], 0), a.max_blocks << a.shift);
+    const int32_t tokens = min(s.n_new, a.max_new);
+    s.rows = tokens * a.group;
+    s.p0 = s.len - s.n_new;
+    const int32_t end = max(s.p0 + tokens, 0);
+    s.lo = a.window > 0 ? max(max(s.p0, 0) - a.window + 1, 0) / kTok : 0;
+    s.hi = (end + kTok - 1) / kTok;
+    return s;
+}
+
+__device__ __forceinline__ int wave_sum(int v) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
+
+__device__ __forceinline__ int wave_before(int v) {
+    const int lane = threadIdx.x & 63;
+    int inc = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int up = __shfl_up(inc, d);
+        if (lane >= d) inc += up;
+    }
+    return inc - v;
+}
+
+// The lengths are known on the device alone, so every wave cuts the work up itself: all
+// tiles over the calls's aimed-at number of workgroups is a chunk, each request is
+// ceil(tiles / chunk) items, and an item's request follows from the prefix sums.  That is
+// two scans of 64 lanes, next to the table lookup that waits for the lengths anyway.
+struct Item {
+    int32_t seq, part, parts, slot, chunk;   // slot: of the first part's partial result
+};
+
+__device__ __forceinline__ int parts_of(const Seq& s, int32_t chunk) {
+    return s.n_new < 1 ? 0 : (max(s.hi - s.lo, 1) - 1) / chunk + 1;
+}
+
+// By item (by_seq false) or by request; seq is -1 if there is none.
+__device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, bool by_seq) {
+    const int lane = threadIdx.x & 63;
+    const int per = (a.n_seqs + 63) / 64;
+    const int i0 = min(lane * per, a.n_seqs), i1 = min(i0 + per, a.n_seqs);
+    int tiles = 0;
+    for (int i = i0; i < i1; ++i) {
+        const Seq s = load_seq(a, i);
+        if (s.n_new > 0) tiles += max(s.hi - s.lo, 0);
+    }
+    tiles = wave_sum(tiles);
+    Item it;
+    it.chunk = 0x7fffff00;
+    if (a.target > 1) {
+        const int round = kWaves * kStep;
+        it.chunk = max(kMinChunk, ((max(tiles, 1) - 1) / a.target + round) / round * round);
+    }
+    int items = 0, split = 0;
+    for (int i = i0; i < i1; ++i) {
+        const int p = parts_of(load_seq(a, i), it.chunk);
+        items += p;
+        split += p > 1 ? p : 0;
+    }
+    int item0 = wave_before(items), slot0 = wave_before(split);
+    int seq = -1, part = 0, parts = 0, slot = 0;
+    for (int i = i0; i < i1; ++i) {
+        const int p = parts_of(load_seq(a, i), it.chunk);
+        if (by_seq ? i == want : want >= item0 && want < item0 + p) {
+            seq = i;
+            part = by_seq ? 0 : want - item0;
+            parts = p;
+            slot = slot0;
+        }
+        item0 += p;
+        slot0 += p > 1 ? p : 0;
+    }
+    const uint64_t who = __ballot(seq >= 0);
+    it.seq = -1;
+    if (who) {
+        const int l = __builtin_ctzll(who);
+        it.seq = __builtin_amdgcn_readlane(seq, l);
+        it.part = __builtin_amdgcn_readlane(part, l);
+        it.parts = __builtin_amdgcn_readlane(parts, l);
+        it.slot = __builtin_amdgcn_readlane(slot, l);
+    }
+    return it;
+}
+
+// ---------------------------------------------------------------- operands
+
+// Eight codes as the bf16 values they stand for before scaling.
+template <bool E4M3>
+__device__ __forceinline__ bf16x8 operand(uint32_t w0, uint32_t w1) {
+    u32x4 r;
+    if constexpr (E4M3) {
+        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false));
+        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true));
+        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false));
+        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true));
+    } else {
+        // |code| <= 127 leaves the low half of its fp32 form zero: the high halves are the bf16s
+        const uint32_t w[2] = {w0, w1};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t f0 = __float_as_uint(code_value<false, 0>(w[h])), f1 = __float_as_uint(code_value<false, 1>(w[h]));
+            const uint32_t f2 = __float_as_uint(code_value<false, 2>(w[h])), f3 = __float_as_uint(code_value<false, 3>(w[h]));
+            r[2 * h] = __builtin_amdgcn_perm(f1, f0, 0x07060302);
+            r[2 * h + 1] = __builtin_amdgcn_perm(f3, f2, 0x07060302);
+        }
+    }
+    return __builtin_bit_cast(bf16x8, r);
+}
+
+// Bytes of a value word (tokens tok .. tok+4) whose tokens exist; the rest may be anything
+// in memory, NaN codes included, and a zero weight does not silence those.
+__device__ __forceinline__ uint32_t live_bytes(int tok, int len) {
+    const int n = min(max(len - tok, 0), 4);
+    return n == 4 ? 0xffffffffu : (1u << (8 * n)) - 1u;
+}
+
+__device__ __forceinline__ float lane_float(float v, int l) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+
+template <int DQ>
+struct Step {           // one step's codes: two tiles of keys and of values
+    u32x4 k[kStep][DQ], v[kStep][DQ];
+};
+
+// DQ = head_dim / 64, NT = tiles of 16 query rows, EXT: cap, window or distance bias.
+template <bool E4M3, int DQ, int NT, bool EXT>
+__global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
+    constexpr int D = 64 * DQ, ROWS = 16 * NT, PITCH = 68;
+    __shared__ float merge[kWaves][ROWS][PITCH];     // pitch: rows 4 banks apart
+    __shared__ float merge_m[kWaves][ROWS], merge_l[kWaves][ROWS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, n = lane & 15;
+    const int head = blockIdx.y % a.n_kv, r0 = blockIdx.y / a.n_kv * ROWS;
+    const Item it = find_item(a, blockIdx.x, false);
+    if (it.seq < 0) return;
+    const Seq sq = load_seq(a, it.seq);
+    if (r0 >= sq.rows) return;
+    const int rows = min(ROWS, sq.rows - r0);
+    // what the first and the last row see bounds what any row sees
+    const int pos_first = sq.p0 + r0 / a.group, pos_last = sq.p0 + (r0 + rows - 1) / a.group;
+    const int all_end = pos_first + 1, all_begin = a.window > 0 ? max(pos_last, 0) - a.window + 1 : 0;
+    int t0 = sq.lo + it.part * it.chunk;
+    int t1 = min(sq.hi, it.parts == 1 ? sq.hi : t0 + it.chunk);
+    t1 = min(t1, (max(pos_last + 1, 0) + kTok - 1) / kTok);
+    if (a.window > 0) t0 = max(t0, max(max(pos_first, 0) - a.window + 1, 0) / kTok);
+
+    bf16x8 qf[NT][2 * DQ];
+    int pos[NT];
+    float slope[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = r0 + 16 * t + n;
+        const bool in = r < sq.rows;
+        const int j = r / a.group, qh = head * a.group + (r - j * a.group);
+        pos[t] = in ? sq.p0 + j : -1;
+        slope[t] = 0.f;
+        if (EXT && a.slopes && in) slope[t] = a.slopes[qh] * kLog2e;
+        const uint16_t* row = a.q + int64_t(sq.row0 + j) * a.q_stride + int64_t(qh) * D + 16 * g;
+#pragma unroll
+        for (int c = 0; c < 2 * DQ; ++c) {
+            u32x4 w = {0, 0, 0, 0};
+            if (in) w = *reinterpret_cast<const u32x4*>(row + 64 * (c / 2) + 8 * (c % 2));
+            qf[t][c] = __builtin_bit_cast(bf16x8, w);
+        }
+    }
+
+    f32x4 acc[DQ][4][NT];
+    float top[NT], sum[NT];          // running maximum (log2 domain); this lane's share of the sum
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        top[t] = -INFINITY;
+        sum[t] = 0.f;
+#pragma unroll
+        for (int c = 0; c < DQ; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[c][j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    int32_t my_id = -1;
+    float my_ks = 0.f, my_vs = 0.f;
+    const int32_t* table = a.table + int64_t(it.seq) * a.max_blocks;
+    const int in_block = (1 << a.shift) - 1;
+
+    auto load = [&](Step<DQ>& b, int tile, int l) {
+#pragma unroll
+        for (int h = 0; h < kStep; ++h) {
+            const int32_t id = max(__builtin_amdgcn_readlane(my_id, l + h), 0);
+            const int64_t at = ((((int64_t(id) * a.n_kv + head) << a.shift) + (((tile + h) * kTok) & in_block)) * D);
+#pragma unroll
+            for (int c = 0; c < DQ; ++c) b.k[h][c] = *reinterpret_cast<const u32x4*>(a.k + at + c * 1024 + lane * 16);
+#pragma unroll
+            for (int c = 0; c < DQ; ++c) b.v[h][c] = *reinterpret_cast<const u32x4*>(a.v + at + c * 1024 + lane * 16);
+        }
+    };
+
+    auto compute = [&](Step<DQ>& b, int tile, int l) {
+        f32x4 s[kStep][NT];
+        bool whole = tile * kTok >= all_begin && (tile + kStep) * kTok <= all_end;
+        float ks[kStep], vs[kStep];
+#pragma unroll
+        for (int h = 0; h < kStep; ++h) {
+            ks[h] = lane_float(my_ks, l + h) * a.scale;
+            vs[h] = lane_float(my_vs, l + h);
+            whole = whole && __builtin_amdgcn_readlane(my_id, l + h) >= 0;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) s[h][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int c = 0; c < DQ; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int h = 0; h < kStep; ++h) {
+                    const bf16x8 kf = operand<E4M3>(b.k[h][c][2 * e], b.k[h][c][2 * e + 1]);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        s[h][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[t][2 * c + e], s[h][t], 0, 0, 0);
+                }
+        bf16x8 pf[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float u[kStep][4];
+#pragma unroll
+            for (int h = 0; h < kStep; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x = s[h][t][i] * ks[h];
+                    if (EXT && a.softcap > 0.f)     // cap * tanh(x / cap) = cap * (1 - 2 / (1 + e^(2 x / cap)))
+                        x = a.softcap * (1.f - 2.f * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * (2.f * kLog2e) / a.softcap)));
+                    x *= kLog2e;
+                    if (EXT) x += slope[t] * float((tile + h) * kTok + 4 * g + i - pos[t]);
+                    u[h][i] = x;
+                }
+            if (!whole) {
+#pragma unroll
+                for (int h = 0; h < kStep; ++h) {
+                    const bool id_ok = __builtin_amdgcn_readlane(my_id, l + h) >= 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = (tile + h) * kTok + 4 * g + i;
+                        bool sees = id_ok && tok <= pos[t];
+                        if (EXT && a.window > 0) sees = sees && pos[t] - tok < a.window;
+                        u[h][i] = sees ? u[h][i] : -INFINITY;
+                    }
+                }
+            }
+            float m = fmaxf(fmaxf(fmaxf(u[0][0], u[0][1]), fmaxf(u[0][2], u[0][3])),
+                            fmaxf(fmaxf(u[1][0], u[1][1]), fmaxf(u[1][2], u[1][3])));
+            m = fmaxf(m, __shfl_xor(m, 16));
+            m = fmaxf(m, __shfl_xor(m, 32));
+            m = fmaxf(m, top[t]);
+            const float base = m == -INFINITY ? 0.f : m;
+            if (__ballot(m > top[t])) {
+                const float f = __builtin_amdgcn_exp2f(top[t] - base);
+                sum[t] *= f;
+#pragma unroll
+                for (int c = 0; c < DQ; ++c)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[c][j][t] *= f;
+                top[t] = m;
+            }
+            float p[kStep][4];
+#pragma unroll
+            for (int h = 0; h < kStep; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    p[h][i] = __builtin_amdgcn_exp2f(u[h][i] - base);
+                    sum[t] += p[h][i];
+                    p[h][i] *= vs[h];
+                }
+            // the weights' rounding to bf16 (at most 2^-9 of each) averages out over a row's
+            // tokens; their sum is taken before it
+            const u32x4 w = {pack_bf16(p[0][0], p[0][1]), pack_bf16(p[0][2], p[0][3]), pack_bf16(p[1][0], p[1][1]), pack_bf16(p[1][2], p[1][3])};
+            pf[t] = __builtin_bit_cast(bf16x8, w);
+        }
+        if (!whole) {
+#pragma unroll
+            for (int h = 0; h < kStep; ++h) {
+                const bool id_ok = __builtin_amdgcn_readlane(my_id, l + h) >= 0;
+                const uint32_t live = id_ok ? live_bytes((tile + h) * kTok + 4 * g, sq.len) : 0u;
+#pragma unroll
+                for (int c = 0; c < DQ; ++c) b.v[h][c] &= live;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < DQ; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bf16x8 vf = operand<E4M3>(b.v[0][c][j], b.v[1][c][j]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[c][j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[t], acc[c][j][t], 0, 0, 0);
+            }
+    };
+
+    const int steps = (max(t1 - t0, 0) + kStep - 1) / kStep;
+    const int mine = steps > wave ? (steps - wave + kWaves - 1) / kWaves : 0;
+    auto tile_of = [&](int k) { return t0 + kStep * (wave + kWaves * k); };
+    for (int k0 = 0; k0 < mine; k0 += kRefill) {
+        // lane l: tile l % 2 of step k0 + l / 2
+        const int tile = tile_of(k0 + lane / kStep) + lane % kStep;
+        my_id = -1;
+        my_ks = my_vs = 0.f;
+        if (tile < t1) {
+            const int32_t id = table[(tile * kTok) >> a.shift];
+            if (id >= 0 && id < a.n_blocks) {
+                my_id = id;
+                my_ks = a.k_scale[int64_t(id) * a.n_kv + head];
+                my_vs = a.v_scale[int64_t(id) * a.n_kv + head];
+            }
+        }
+        const int end = min(mine - k0, kRefill);
+        if constexpr (NT * DQ > 4) {     // no registers for a second step in flight
+            Step<DQ> b;
+            for (int k = 0; k < end; ++k) {
+                load(b, tile_of(k0 + k), kStep * k);
+                compute(b, tile_of(k0 + k), kStep * k);
+            }
+            continue;
+        }
+        Step<DQ> b0, b1;
+        load(b0, tile_of(k0), 0);
+        for (int k = 0; k < end; k += 2) {
+            if (k + 1 < end) load(b1, tile_of(k0 + k + 1), kStep * (k + 1));
+            compute(b0, tile_of(k0 + k), kStep * k);
+            if (k + 1 < end) {
+                if (k + 2 < end) load(b0, tile_of(k0 + k + 2), kStep * (k + 2));
+                compute(b1, tile_of(k0 + k + 1), kStep * (k + 1));
+            }
+        }
+    }
+
+    // Join the waves: a common maximum a row, then sums slab by slab through LDS.
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        sum[t] += __shfl_xor(sum[t], 16);
+        sum[t] += __shfl_xor(sum[t], 32);
+        if (g == 0) {
+            merge_m[wave][16 * t + n] = top[t];
+            merge_l[wave][16 * t + n] = sum[t];
+        }
+    }
+    __syncthreads();
+    float f[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) m = fmaxf(m, merge_m[w][16 * t + n]);
+        f[t] = __builtin_amdgcn_exp2f(top[t] - (m == -INFINITY ? 0.f : m));
+    }
+#pragma unroll
+    for (int c = 0; c < DQ; ++c) {
+        if (c) __syncthreads();
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)      // register i of product j is channel 16g + 4i + j
+                *reinterpret_cast<f32x4*>(&merge[wave][16 * t + n][16 * g + 4 * i]) =
+                    f32x4{acc[c][0][t][i], acc[c][1][t][i], acc[c][2][t][i], acc[c][3][t][i]} * f[t];
+        __syncthreads();
+        for (int e = threadIdx.x; e < rows * 16; e += 64 * kWaves) {
+            const int r = e >> 4, d = (e & 15) * 4;
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) m = fmaxf(m, merge_m[w][r]);
+            const float base = m == -INFINITY ? 0.f : m;
+            f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                l += merge_l[w][r] * __builtin_amdgcn_exp2f(merge_m[w][r] - base);
+                o += *reinterpret_cast<const f32x4*>(&merge[w][r][d]);
+            }
+            if (it.parts == 1) {
+                const int j = (r0 + r) / a.group, qh = head * a.group + (r0 + r - j * a.group);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                uint16_t* to = a.out + int64_t(sq.row0 + j) * a.out_stride + int64_t(qh) * D + 64 * c + d;
+                *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+                if (c == 0 && d == 0 && a.lse)
+                    a.lse[int64_t(sq.row0 + j) * (a.n_kv * a.group) + qh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+            } else {
+                const int64_t at = (int64_t(it.slot + it.part) * gridDim.y + blockIdx.y) * ROWS + r;
+                *reinterpret_cast<f32x4*>(a.part_o + at * D + 64 * c + d) = o;
+                if (c == 0 && d == 0) *reinterpret_cast<f32x2*>(a.part_ml + at * 2) = f32x2{m, l};
+            }
+        }
+    }
+}
+
+// The parts of split requests, one workgroup a row: lanes over channels, waves over parts.
+template <int DQ>
+__global__ __launch_bounds__(64 * kWaves) void join_kernel(AttnArgs a, int rows_of_tile) {
+    constexpr int D = 64 * DQ;
+    __shared__ float part[kWaves][D];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const Item it = find_item(a, blockIdx.x, true);
+    if (it.seq < 0 || it.parts < 2) return;
+    const Seq sq = load_seq(a, it.seq);
+    const int head = blockIdx.y % a.n_kv, tile = blockIdx.y / a.n_kv;
+    const int r = tile * rows_of_tile + blockIdx.z;
+    if (r >= sq.rows) return;
+    const int64_t first = (int64_t(it.slot) * gridDim.y + blockIdx.y) * rows_of_tile + blockIdx.z;
+    const int64_t next = int64_t(gridDim.y) * rows_of_tile;       // rows from one part to the next
+    float m = -INFINITY;
+    for (int p = lane; p < it.parts; p += 64) m = fmaxf(m, a.part_ml[(first + p * next) * 2]);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    for (int p = lane; p < it.parts; p += 64) {
+        const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + (first + p * next) * 2);
+        l += ml[1] * __builtin_amdgcn_exp2f(ml[0] - base);
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
+    float o[DQ] = {};
+#pragma unroll 4
+    for (int p = wave; p < it.parts; p += kWaves) {
+        const int64_t at = first + p * next;
+        const float f = __builtin_amdgcn_exp2f(a.part_ml[at * 2] - base);
+#pragma unroll
+        for (int c = 0; c < DQ; ++c) o[c] += a.part_o[at * D + 64 * c + lane] * f;
+    }
+#pragma unroll
+    for (int c = 0; c < DQ; ++c) part[wave][64 * c + lane] = o[c];
+    __syncthreads();
+    const int j = r / a.group, qh = head * a.group + (r - j * a.group);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t* to = a.out + int64_t(sq.row0 + j) * a.out_stride + int64_t(qh) * D;
+    for (int d = threadIdx.x * 2; d < D; d += 128 * kWaves) {
+        float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            x0 += part[w][d];
+            x1 += part[w][d + 1];
+        }
+        *reinterpret_cast<uint32_t*>(to + d) = pack_bf16(x0 * inv, x1 * inv);
+    }
+    if (threadIdx.x == 0 && a.lse)
+        a.lse[int64_t(sq.row0 + j) * (a.n_kv * a.group) + qh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+}
+
+// How a call is laid out; the same for the workspace's size and the launch.
+struct Plan {
+    int32_t group, nt, row_tiles, target;
+    uint32_t grid_x, grid_y;
+    uint64_t parts;          // partial results, of nt * 16 rows for every grid_y
+    uint64_t bytes;
+};
+
+static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs, int32_t max_new, int32_t max_blocks, Plan* p) {
+    if (n_heads < 1 || n_heads % c->n_heads) return fail(MBD_ESHAPE, "n_heads %d is not a multiple of the cache's %d", n_heads, c->n_heads);
+    if (n_seqs < 1 || n_seqs > kMaxSeqs) return fail(MBD_ESHAPE, "n_seqs %d outside [1, %d]", n_seqs, kMaxSeqs);
+    if (max_blocks < 1 || int64_t(max_blocks) * c->block_size > (int64_t(1) << 30))
+        return fail(MBD_ESHAPE, "max_blocks * block_size outside [1, 2^30]");
+    const int64_t seq_tiles = int64_t(max_blocks) * (c->block_size / kTok);
+    if (seq_tiles * n_seqs >= (int64_t(1) << 31)) return fail(MBD_ESHAPE, "n_seqs * max_blocks * block_size / 16 is 2^31 or more");
+    p->group = n_heads / c->n_heads;
+    if (max_new < 1 || int64_t(max_new) * p->group >= (int64_t(1) << 24)) return fail(MBD_ESHAPE, "max_new * query heads a KV head outside [1, 2^24)");
+    const int32_t rows = max_new * p->group, widest = c->head_dim > 128 ? 2 : 4;
+    p->nt = rows <= 16 ? 1 : rows <= 32 ? 2 : widest;
+    p->row_tiles = (rows + 16 * p->nt - 1) / (16 * p->nt);
+    const int64_t y = int64_t(c->n_heads) * p->row_tiles;
+    if (y > 65535) return fail(MBD_ESHAPE, "KV heads times query row tiles above 65535");
+    p->grid_y = uint32_t(y);
+    p->target = int32_t(std::max<int64_t>(1, kTargetBlocks / y));
+    const int64_t most = (seq_tiles + kMinChunk - 1) / kMinChunk;      // parts of one request
+    if (most < 2) p->target = 1;
+    const bool split = p->target > 1;
+    p->grid_x = uint32_t(split ? std::min<int64_t>(p->target + n_seqs, n_seqs * most) : n_seqs);
+    // a request is split if it is longer than a chunk, so into fewer than twice its chunks
+    p->parts = split ? std::min<int64_t>(2 * p->target, p->grid_x) : 0;
+    p->bytes = p->parts * p->grid_y * (16u * p->nt) * (c->head_dim + 2) * sizeof(float);
+    return MBD_OK;
+}
+
+template <bool E4M3, int DQ, int NT>
+static void launch(const AttnArgs& a, const Plan& p, bool ext, hipStream_t s) {
+    const dim3 grid(p.grid_x, p.grid_y), block(64 * kWaves);
+    if (ext) hipLaunchKernelGGL((attn_kernel<E4M3, DQ, NT, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((attn_kernel<E4M3, DQ, NT, false>), grid, block, 0, s, a);
+    if (p.parts)
+        hipLaunchKernelGGL((join_kernel<DQ>), dim3(a.n_seqs, p.grid_y, std::min(16 * NT, a.max_new * a.group)), block, 0, s, a, 16 * NT);
+}
+
+template <bool E4M3, int DQ>
+static void launch_rows(const AttnArgs& a, const Plan& p, bool ext, hipStream_t s) {
+    if (p.nt == 1) return launch<E4M3, DQ, 1>(a, p, ext, s);
+    if (p.nt == 2) return launch<E4M3, DQ, 2>(a, p, ext, s);
+    if constexpr (DQ <= 2) launch<E4M3, DQ, 4>(a, p, ext, s);
+}
+
+template <bool E4M3>
+static void launch_dim(const AttnArgs& a, const Plan& p, int dq, bool ext, hipStream_t s) {
+    if (dq == 1) launch_rows<E4M3, 1>(a, p, ext, s);
+    else if (dq == 2) launch_rows<E4M3, 2>(a, p, ext, s);
+    else if (dq == 3) launch_rows<E4M3, 3>(a, p, ext, s);
+    else launch_rows<E4M3, 4>(a, p, ext, s);
+}
+
+}  // namespace kv
+}  // namespace mbd
+
+using namespace mbd;
+
+extern "C" {
+
+mbd_status mbd_kv_attn_workspace_bytes(const mbd_kv_cache* cache, int32_t n_heads, int32_t n_seqs, int32_t max_new,
+                                       int32_t max_blocks, uint64_t* bytes) {
+    if (!bytes) return fail(MBD_EINVAL, "NULL argument");
+    kv::Plan p;
+    mbd_status st = kv::check_cache(cache, false);
+    if (st == MBD_OK) st = kv::plan_of(cache, n_heads, n_seqs, max_new, max_blocks, &p);
+    if (st == MBD_OK) *bytes = p.bytes;
+    return st;
+}
+
+mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, const uint16_t* q, const int32_t* seq_start,
+                       const int32_t* lens, const int32_t* block_table, uint16_t* out, float* lse, void* ws, uint64_t ws_bytes,
+                       void* stream) {
+    hip_clear();
+    kv::Plan p;
+    mbd_status st = kv::check_cache(cache, true);
+    if (st != MBD_OK) return st;
+    if (!args) return fail(MBD_EINVAL, "NULL argument");
+    st = kv::plan_of(cache, args->n_heads, args->n_seqs, args->max_new, args->max_blocks, &p);
+    if (st != MBD_OK) return st;
+    if (args->T < 0 || args->T > (1 << 24)) return fail(MBD_ESHAPE, "T %d outside [0, 2^24]", args->T);
+    if (args->window < 0) return fail(MBD_EINVAL, "window %d below 0", args->window);
+    if (!std::isfinite(args->scale) || !std::isfinite(args->softcap) || args->softcap < 0)
+        return fail(MBD_EINVAL, "scale and softcap must be finite, softcap not below 0");
+    const int64_t row = int64_t(args->n_heads) * cache->head_dim;
+    if (args->q_stride < row || args->out_stride < row || args->q_stride % 8 || args->out_stride % 8)
+        return fail(MBD_ESHAPE, "row strides must be multiples of 8 and at least n_heads * head_dim");
+    if (!seq_start || !lens || !block_table) return fail(MBD_EINVAL, "NULL argument");
+    if (!kv::aligned(seq_start, 4) || !kv::aligned(lens, 4) || !kv::aligned(block_table, 4) || !kv::aligned(lse, 4) ||
+        !kv::aligned(args->slopes, 4))
+        return fail(MBD_EALIGN, "int32 and fp32 arrays must be 4-byte aligned");
+    if (args->T == 0) return MBD_OK;
+    if (!q || !out) return fail(MBD_EINVAL, "NULL argument");
+    if (!kv::aligned(q, 16) || !kv::aligned(out, 16)) return fail(MBD_EALIGN, "q and out must be 16-byte aligned");
+    if (p.bytes) {
+        if (!ws || ws_bytes < p.bytes) return fail(MBD_EINVAL, "workspace of %llu bytes needed", static_cast<unsigned long long>(p.bytes));
+        if (!kv::aligned(ws, 16)) return fail(MBD_EALIGN, "workspace must be 16-byte aligned");
+    }
+    kv::AttnArgs a{};
+    a.k = static_cast<const uint8_t*>(cache->k_codes);
+    a.v = static_cast<const uint8_t*>(cache->v_codes);
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+    a.q = q;
+    a.seq_start = seq_start;
+    a.lens = lens;
+    a.table = block_table;
+    a.out = out;
+    a.lse = lse;
+    a.part_o = static_cast<float*>(ws);
+    a.part_ml = a.part_o + p.parts * p.grid_y * (16u * p.nt) * cache->head_dim;
+    a.slopes = args->slopes;
+    a.q_stride = args->q_stride;
+    a.out_stride = args->out_stride;
+    a.n_blocks = int32_t(cache->n_blocks);
+    a.n_seqs = args->n_seqs;
+    a.max_blocks = args->max_blocks;
+    a.T = args->T;
+    a.max_new = args->max_new;
+    a.window = args->window < args->max_blocks * cache->block_size ? args->window : 0;   // else it hides nothing
+    a.shift = kv::log2_of(cache->block_size);
+    a.n_kv = cache->n_heads;
+    a.group = p.group;
+    a.target = p.target;
+    a.scale = args->scale;
+    a.softcap = args->softcap;
+    const bool ext = a.window > 0 || args->softcap > 0 || args->slopes;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (cache->fmt == MBD_KV_E4M3) kv::launch_dim<true>(a, p, cache->head_dim / 64, ext, s);
+    else kv::launch_dim<false>(a, p, cache->head_dim / 64, ext, s);
+    return hip_check("attention launch");
+}
+
+}  // extern "C"

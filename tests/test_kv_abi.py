@@ -1,0 +1,140 @@
+"""Argument checks of the KV-cache calls: each refusal with its status, before any GPU
+work (fake pointers, never dereferenced), and the binding's own checks."""
+import ctypes
+
+import pytest
+
+mbd = pytest.importorskip("memory_bound_decode_amd")
+torch = pytest.importorskip("torch")
+
+P = 0x10000
+
+
+@pytest.fixture(scope="module")
+def L():
+    try:
+        return mbd.lib()
+    except ImportError as e:                         # pragma: no cover
+        pytest.skip(str(e))
+
+
+def _cache(**kw):
+    d = dict(fmt=mbd.MBD_KV_INT8, block_size=16, n_heads=2, head_dim=128, n_blocks=8, k_codes=P, v_codes=P, k_scale=P, v_scale=P)
+    return mbd.MbdKvCache(**(d | kw))
+
+
+BAD_CACHES = [(dict(fmt=9), "EINVAL"), (dict(block_size=24), "ESHAPE"), (dict(block_size=512), "ESHAPE"), (dict(head_dim=96), "ESHAPE"),
+              (dict(head_dim=320), "ESHAPE"), (dict(n_heads=0), "ESHAPE"), (dict(n_blocks=0), "ESHAPE"), (dict(n_blocks=1 << 27), "ESHAPE"),
+              (dict(k_codes=None), "EINVAL"), (dict(v_scale=None), "EINVAL"), (dict(v_codes=P + 8), "EALIGN"), (dict(k_scale=P + 2), "EALIGN")]
+
+
+@pytest.mark.parametrize("change,status", BAD_CACHES)
+def test_bad_caches(L, change, status):
+    want = getattr(mbd, "MBD_" + status)
+    c = _cache(**change)
+    assert L.mbd_kv_append(ctypes.byref(c), P, P, mbd.MBD_BF16, 256, 256, P, 1, None) == want
+    assert L.mbd_kv_gather(ctypes.byref(c), P, 1, mbd.MBD_F32, P, P, None) == want
+    assert L.mbd_kv_attn(ctypes.byref(c), ctypes.byref(_args()), P, P, P, P, P, None, P, 1 << 30, None) == want
+    assert L.mbd_last_error()
+
+
+def test_append_and_gather_arguments(L):
+    c = ctypes.byref(_cache())
+    app = lambda k=P, v=P, dt=mbd.MBD_BF16, ks=256, vs=256, s=P, T=1: L.mbd_kv_append(c, k, v, dt, ks, vs, s, T, None)
+    assert L.mbd_kv_append(None, P, P, 1, 256, 256, P, 1, None) == mbd.MBD_EINVAL
+    assert app(k=None) == app(s=None) == app(dt=3) == mbd.MBD_EINVAL
+    assert app(k=P + 8) == app(v=P + 4) == app(s=P + 1) == mbd.MBD_EALIGN
+    assert app(ks=255) == app(vs=248) == app(ks=260) == app(T=-1) == app(T=(1 << 24) + 1) == mbd.MBD_ESHAPE
+    assert app(T=0, k=None, v=None, s=None) == mbd.MBD_OK
+    gat = lambda s=P, T=1, dt=mbd.MBD_F32, k=P, v=P: L.mbd_kv_gather(c, s, T, dt, k, v, None)
+    assert gat(k=None) == gat(s=None) == gat(dt=0) == mbd.MBD_EINVAL
+    assert gat(k=P + 8) == mbd.MBD_EALIGN and gat(T=-1) == mbd.MBD_ESHAPE and gat(T=0) == mbd.MBD_OK
+
+
+def test_slots_arguments(L):
+    base = dict(n_seqs=4, block_size=16, max_blocks=8, n_blocks=100, block_table=P, free_blocks=P)
+
+    def call(T=4, at=None, value=None, **kw):
+        pool = mbd.MbdKvPool(**(base | kw))
+        ptrs = [P] * 11
+        if at is not None:
+            ptrs[at] = value
+        return L.mbd_kv_slots(ctypes.byref(pool), *ptrs[:4], T, *ptrs[4:], None)
+
+    assert L.mbd_kv_slots(None, *[P] * 4, 1, *[P] * 7, None) == mbd.MBD_EINVAL
+    for kw in (dict(n_seqs=0), dict(n_seqs=4097), dict(block_size=8), dict(max_blocks=0), dict(max_blocks=1 << 27), dict(n_blocks=0),
+               dict(n_blocks=1 << 27), dict(T=-1)):
+        assert call(**kw) == mbd.MBD_ESHAPE, kw
+    assert call(block_table=None) == call(free_blocks=None) == mbd.MBD_EINVAL
+    assert call(free_blocks=P + 2) == mbd.MBD_EALIGN
+    for i in range(11):
+        if i != 6:                                   # positions may be NULL
+            assert call(at=i, value=None) == mbd.MBD_EINVAL, i
+        assert call(at=i, value=P + 2) == mbd.MBD_EALIGN, i
+
+
+def _args(**kw):
+    d = dict(n_heads=8, n_seqs=2, max_blocks=4, T=2, max_new=1, window=0, scale=0.1, softcap=0.0, slopes=None, q_stride=1024, out_stride=1024)
+    return mbd.MbdKvAttnArgs(**(d | kw))
+
+
+BAD_ARGS = [(dict(n_heads=7), "ESHAPE"), (dict(n_heads=0), "ESHAPE"), (dict(n_seqs=0), "ESHAPE"), (dict(n_seqs=4097), "ESHAPE"),
+            (dict(max_blocks=0), "ESHAPE"), (dict(max_blocks=(1 << 26) + 1), "ESHAPE"), (dict(max_blocks=1 << 26, n_seqs=32), "ESHAPE"),
+            (dict(T=-1), "ESHAPE"), (dict(T=(1 << 24) + 1), "ESHAPE"), (dict(max_new=0), "ESHAPE"), (dict(max_new=1 << 22), "ESHAPE"),
+            (dict(window=-1), "EINVAL"), (dict(scale=float("nan")), "EINVAL"), (dict(softcap=-1.0), "EINVAL"),
+            (dict(softcap=float("inf")), "EINVAL"), (dict(q_stride=1016), "ESHAPE"), (dict(out_stride=1028), "ESHAPE"),
+            (dict(slopes=P + 2), "EALIGN")]
+
+
+@pytest.mark.parametrize("change,status", BAD_ARGS)
+def test_bad_attention_arguments(L, change, status):
+    c, a = _cache(), _args(**change)
+    assert L.mbd_kv_attn(ctypes.byref(c), ctypes.byref(a), P, P, P, P, P, None, P, 1 << 40, None) == getattr(mbd, "MBD_" + status)
+
+
+def test_attention_pointers_and_workspace(L):
+    c = _cache()
+
+    def call(a, **kw):
+        d = dict(q=P, start=P, lens=P, table=P, out=P, lse=None, ws=P, size=1 << 40) | kw
+        return L.mbd_kv_attn(ctypes.byref(c), None if a is None else ctypes.byref(a), d["q"], d["start"], d["lens"], d["table"], d["out"],
+                             d["lse"], d["ws"], d["size"], None)
+
+    a = _args(max_blocks=512)
+    assert call(None) == mbd.MBD_EINVAL
+    for name in ("q", "start", "lens", "table", "out"):
+        assert call(a, **{name: None}) == mbd.MBD_EINVAL
+        assert call(a, **{name: P + 2}) == mbd.MBD_EALIGN
+    assert call(a, lse=P + 2) == mbd.MBD_EALIGN
+    need = ctypes.c_uint64()
+    assert L.mbd_kv_attn_workspace_bytes(ctypes.byref(c), 8, 2, 1, 512, ctypes.byref(need)) == mbd.MBD_OK and need.value > 0
+    assert call(a, ws=None) == call(a, size=need.value - 1) == mbd.MBD_EINVAL
+    assert call(a, ws=P + 8) == mbd.MBD_EALIGN
+    assert call(_args(T=0), q=None, out=None, ws=None, size=0) == mbd.MBD_OK      # nothing to do, nothing enqueued
+
+
+def test_workspace_sizes(L):
+    need = ctypes.c_uint64()
+    c = _cache(k_codes=None, v_codes=None, k_scale=None, v_scale=None)              # only its shape counts
+    ask = lambda *a: L.mbd_kv_attn_workspace_bytes(ctypes.byref(c), *a, ctypes.byref(need))
+    assert L.mbd_kv_attn_workspace_bytes(ctypes.byref(c), 8, 2, 1, 512, None) == mbd.MBD_EINVAL
+    assert L.mbd_kv_attn_workspace_bytes(None, 8, 2, 1, 512, ctypes.byref(need)) == mbd.MBD_EINVAL
+    assert ask(8, 2, 0, 512) == ask(9, 2, 1, 512) == ask(8, 0, 1, 512) == ask(8, 2, 1, 0) == mbd.MBD_ESHAPE
+    assert ask(8, 2, 1, 1) == mbd.MBD_OK and need.value == 0                        # 16 tokens: never split
+    assert ask(8, 4096, 1, 32768) == mbd.MBD_OK and 0 < need.value < 1 << 30
+    assert ask(8, 1, 8192, 1024) == mbd.MBD_OK and need.value == 0                  # prompts alone fill the chip
+
+
+def test_binding_checks():
+    codes = torch.zeros((4, 2, 16 * 128), dtype=torch.uint8)
+    scale = torch.zeros((4, 2))
+    with pytest.raises(ValueError, match="current GPU"):
+        mbd.KvCache(mbd.MBD_KV_INT8, 16, 128, codes, codes, scale, scale)
+    with pytest.raises(ValueError, match="block_size"):
+        mbd.KvCache(mbd.MBD_KV_INT8, 32, 128, codes, codes, scale, scale)
+    with pytest.raises(ValueError, match="contiguous"):
+        mbd.KvCache(mbd.MBD_KV_INT8, 16, 128, codes, codes, scale, scale.double())
+    with pytest.raises(ValueError, match="int32"):
+        mbd.KvPool(16, torch.zeros((2, 4), dtype=torch.int64), torch.zeros(9, dtype=torch.int32))
+    with pytest.raises(ValueError, match="n_seqs"):
+        mbd.KvPool(16, torch.zeros(4, dtype=torch.int32), torch.zeros(9, dtype=torch.int32))
