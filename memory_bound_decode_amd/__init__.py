@@ -135,7 +135,8 @@ def _stream(stream):
     if stream is not None:
         return ctypes.c_void_p(int(stream))
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the raw handle: building a torch.cuda.Stream for it takes 3 us, as long as a launch
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _ptr(t):
@@ -209,32 +210,37 @@ def mbd_encode_cassandra(w, act_norm, keep_num: int, keep_den: int, plan: MbdEnc
 
 # ------------------------------------------------------------------ KV cache
 
-def _on_device(**tensors):
-    """Every tensor on the current GPU, whose stream the call takes."""
+def _here():
+    """The current GPU's index, whose stream a call takes; -2 (no tensor's) without one."""
     import torch
-    here = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for name, t in tensors.items():
-        if t is not None and (t.device.type != "cuda" or t.device.index != here):
-            raise ValueError("%s is on %s, not on the current GPU" % (name, t.device))
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
 
 
-def _ints(n=None, **tensors):
-    """Contiguous int32 tensors, of n values where n is given."""
+def _refuse(here, name, t, dtype, n=None):
+    if t.get_device() != here:
+        raise ValueError("%s is on %s, not on the current GPU" % (name, t.device))
+    raise ValueError("%s must be a contiguous %s tensor%s" % (name, dtype, "" if n is None else " of %d values" % n))
+
+
+def _ints(here, *checks):
+    """(name, tensor, values) each: contiguous int32 on the current GPU."""
     import torch
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.dtype != torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n):
-            raise ValueError("%s must be a contiguous int32 tensor%s" % (name, "" if n is None else " of %d values" % n))
+    i32 = torch.int32
+    for name, t, n in checks:
+        if t.dtype is not i32 or t.numel() != n or t.get_device() != here or not t.is_contiguous():
+            _refuse(here, name, t, "int32", n)
 
 
-def _rows(name, t, heads, dim, dtypes):
+def _rows(here, name, t, heads, dim, dtypes):
     """[T][heads][dim] with dense rows; returns the elements from one token to the next."""
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim) or t.dtype not in dtypes:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or t.dtype not in dtypes:
         raise ValueError("%s must be [T][%d][%d] of %s" % (name, heads, dim, " or ".join(str(d) for d in dtypes)))
-    if (heads > 1 and t.stride(1) != dim) or t.stride(2) != 1:
+    if (heads > 1 and stride[1] != dim) or stride[2] != 1:
         raise ValueError("%s: one token's heads must be dense" % name)
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * dim)
+    if t.get_device() != here:
+        _refuse(here, name, t, "")
+    return stride[0] if shape[0] > 1 else max(stride[0], heads * dim)
 
 
 class KvCache:
@@ -250,7 +256,8 @@ class KvCache:
                                 (k_scale, k_codes.shape[:2], torch.float32), (v_scale, k_codes.shape[:2], torch.float32)):
             if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
                 raise ValueError("codes are contiguous uint8 tensors of one shape, scales contiguous fp32 [n_blocks][n_heads]")
-        _on_device(k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale)
+            if t.get_device() != _here():
+                _refuse(_here(), "the cache", t, "")
         self.tensors = dict(k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale)
         self.fmt, self.block_size, self.n_heads, self.head_dim = fmt, block_size, k_codes.shape[1], head_dim
         self.n_blocks = k_codes.shape[0]
@@ -274,8 +281,7 @@ class KvPool:
     def __init__(self, block_size: int, block_table, free_blocks):
         if block_table.dim() != 2 or free_blocks.dim() != 1:
             raise ValueError("block_table must be [n_seqs][max_blocks], free_blocks [n_blocks]")
-        _ints(block_table=block_table, free_blocks=free_blocks)
-        _on_device(block_table=block_table, free_blocks=free_blocks)
+        _ints(_here(), ("block_table", block_table, block_table.numel()), ("free_blocks", free_blocks, free_blocks.numel()))
         self.block_table, self.free_blocks, self.block_size = block_table, free_blocks, block_size
         self.n_seqs, self.max_blocks = block_table.shape
         self.desc = MbdKvPool(self.n_seqs, block_size, self.max_blocks, free_blocks.shape[0], block_table.data_ptr(),
@@ -289,45 +295,39 @@ def mbd_kv_slots(pool: KvPool, new_tokens, lens, held, n_free, seq_start, slots,
                  status, stream=None) -> None:
     """One step's block tables, slot map and ragged starts from request lengths; slots has
     one value for each row of the step's token batch, positions may be None."""
-    n = pool.n_seqs
-    _ints(n, new_tokens=new_tokens, lens=lens, held=held, lens_out=lens_out, held_out=held_out, status=status)
-    _ints(1, n_free=n_free, n_free_out=n_free_out)
-    _ints(n + 1, seq_start=seq_start)
-    _ints(slots=slots)
-    _ints(slots.numel(), positions=positions)
-    _on_device(new_tokens=new_tokens, lens=lens, held=held, n_free=n_free, seq_start=seq_start, slots=slots, positions=positions,
-               lens_out=lens_out, held_out=held_out, n_free_out=n_free_out, status=status)
-    check(lib().mbd_kv_slots(pool.ref(), _ptr(new_tokens), _ptr(lens), _ptr(held), _ptr(n_free), slots.numel(), _ptr(seq_start),
-                             _ptr(slots), None if positions is None else _ptr(positions), _ptr(lens_out), _ptr(held_out),
-                             _ptr(n_free_out), _ptr(status), _stream(stream)), "mbd_kv_slots")
+    n, T, here = pool.n_seqs, slots.numel(), _here()
+    _ints(here, ("new_tokens", new_tokens, n), ("lens", lens, n), ("held", held, n), ("n_free", n_free, 1), ("seq_start", seq_start, n + 1),
+          ("slots", slots, T), ("lens_out", lens_out, n), ("held_out", held_out, n), ("n_free_out", n_free_out, 1), ("status", status, n))
+    if positions is not None:
+        _ints(here, ("positions", positions, T))
+    check(lib().mbd_kv_slots(pool.ref(), new_tokens.data_ptr(), lens.data_ptr(), held.data_ptr(), n_free.data_ptr(), T, seq_start.data_ptr(),
+                             slots.data_ptr(), None if positions is None else positions.data_ptr(), lens_out.data_ptr(),
+                             held_out.data_ptr(), n_free_out.data_ptr(), status.data_ptr(), _stream(stream)), "mbd_kv_slots")
 
 
 def mbd_kv_append(cache: KvCache, k, v, slots, stream=None) -> None:
     """Quantise k, v [T][n_heads][head_dim] (bf16 or fp32; rows may be slices) into their slots."""
     import torch
-    kinds = (torch.bfloat16, torch.float32)
-    ks, vs = _rows("k", k, cache.n_heads, cache.head_dim, kinds), _rows("v", v, cache.n_heads, cache.head_dim, kinds)
-    if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
-        raise ValueError("k and v must be alike")
-    _ints(k.shape[0], slots=slots)
-    _on_device(k=k, v=v, slots=slots)
-    check(lib().mbd_kv_append(cache.ref(), _ptr(k), _ptr(v), MBD_BF16 if k.dtype == torch.bfloat16 else MBD_F32, ks, vs, _ptr(slots),
-                              k.shape[0], _stream(stream)), "mbd_kv_append")
+    here, heads, dim, T, dt = _here(), cache.n_heads, cache.head_dim, k.shape[0], k.dtype
+    ks, vs = _rows(here, "k", k, heads, dim, (torch.bfloat16, torch.float32)), _rows(here, "v", v, heads, dim, (dt,))
+    if v.shape[0] != T:
+        raise ValueError("k and v must have as many tokens")
+    _ints(here, ("slots", slots, T))
+    check(lib().mbd_kv_append(cache.ref(), k.data_ptr(), v.data_ptr(), MBD_BF16 if dt is torch.bfloat16 else MBD_F32, ks, vs, slots.data_ptr(),
+                              T, _stream(stream)), "mbd_kv_append")
 
 
 def mbd_kv_gather(cache: KvCache, slots, k_out, v_out, stream=None) -> None:
     """Dense keys and values [T][n_heads][head_dim] (bf16 or fp32) of the tokens in ``slots``."""
     import torch
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _rows(name, t, cache.n_heads, cache.head_dim, (torch.bfloat16, torch.float32))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-    if k_out.dtype != v_out.dtype or k_out.shape != v_out.shape:
-        raise ValueError("k_out and v_out must be alike")
-    _ints(k_out.shape[0], slots=slots)
-    _on_device(slots=slots, k_out=k_out, v_out=v_out)
-    check(lib().mbd_kv_gather(cache.ref(), _ptr(slots), k_out.shape[0], MBD_BF16 if k_out.dtype == torch.bfloat16 else MBD_F32,
-                              _ptr(k_out), _ptr(v_out), _stream(stream)), "mbd_kv_gather")
+    here, heads, dim, T, dt = _here(), cache.n_heads, cache.head_dim, k_out.shape[0], k_out.dtype
+    _rows(here, "k_out", k_out, heads, dim, (torch.bfloat16, torch.float32))
+    _rows(here, "v_out", v_out, heads, dim, (dt,))
+    if v_out.shape[0] != T or not k_out.is_contiguous() or not v_out.is_contiguous():
+        raise ValueError("k_out and v_out must be contiguous and alike")
+    _ints(here, ("slots", slots, T))
+    check(lib().mbd_kv_gather(cache.ref(), slots.data_ptr(), T, MBD_BF16 if dt is torch.bfloat16 else MBD_F32, k_out.data_ptr(),
+                              v_out.data_ptr(), _stream(stream)), "mbd_kv_gather")
 
 
 def mbd_kv_attn_workspace_bytes(cache: KvCache, n_heads: int, n_seqs: int, max_new: int, max_blocks: int) -> int:
@@ -343,26 +343,23 @@ def mbd_kv_attn(cache: KvCache, q, seq_start, lens, block_table, out, ws=None, m
     their cached tokens, into out (alike; rows may be slices) and lse fp32 [T][n_heads].
     scale defaults to head_dim ** -0.5."""
     import torch
-    if q.dim() != 3 or out.shape != q.shape:
-        raise ValueError("q and out must be [T][n_heads][head_dim]")
-    heads = q.shape[1]
-    qs, outs = (_rows(name, t, heads, cache.head_dim, (torch.bfloat16,)) for name, t in (("q", q), ("out", out)))
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [n_seqs][max_blocks]")
-    n, width = block_table.shape
-    _ints(block_table=block_table)
-    _ints(n, lens=lens)
-    _ints(n + 1, seq_start=seq_start)
-    for name, t, shape in (("lse", lse, tuple(q.shape[:2])), ("slopes", slopes, (heads,))):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous()):
-            raise ValueError("%s must be a contiguous fp32 tensor %s" % (name, list(shape)))
-    if ws is not None and not ws.is_contiguous():
-        raise ValueError("ws must be contiguous")
-    _on_device(q=q, seq_start=seq_start, lens=lens, block_table=block_table, out=out, ws=ws, slopes=slopes, lse=lse)
-    args = MbdKvAttnArgs(heads, n, width, q.shape[0], max_new, window, cache.head_dim ** -0.5 if scale is None else scale, softcap,
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be [T][n_heads][head_dim], block_table [n_seqs][max_blocks]")
+    here, (T, heads, dim), (n, width) = _here(), q.shape, block_table.shape
+    qs = _rows(here, "q", q, heads, cache.head_dim, (torch.bfloat16,))
+    outs = _rows(here, "out", out, heads, dim, (torch.bfloat16,))
+    if out.shape[0] != T:
+        raise ValueError("out must have as many rows as q")
+    _ints(here, ("block_table", block_table, n * width), ("lens", lens, n), ("seq_start", seq_start, n + 1))
+    for name, t, size in (("lse", lse, T * heads), ("slopes", slopes, heads)):
+        if t is not None and (t.dtype is not torch.float32 or t.numel() != size or t.get_device() != here or not t.is_contiguous()):
+            _refuse(here, name, t, "fp32", size)
+    if ws is not None and (ws.get_device() != here or not ws.is_contiguous()):
+        _refuse(here, "ws", ws, "")
+    args = MbdKvAttnArgs(heads, n, width, T, max_new, window, dim ** -0.5 if scale is None else scale, softcap,
                          None if slopes is None else slopes.data_ptr(), qs, outs)
-    check(lib().mbd_kv_attn(cache.ref(), ctypes.byref(args), _ptr(q), _ptr(seq_start), _ptr(lens), _ptr(block_table), _ptr(out),
-                            None if lse is None else _ptr(lse), None if ws is None else _ptr(ws),
+    check(lib().mbd_kv_attn(cache.ref(), ctypes.byref(args), q.data_ptr(), seq_start.data_ptr(), lens.data_ptr(), block_table.data_ptr(),
+                            out.data_ptr(), None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
                             0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), "mbd_kv_attn")
 
 

@@ -20,29 +20,30 @@ struct SlotArgs {
     int32_t *table, *free_blocks;
     int32_t *seq_start, *slots, *positions, *lens_out, *held_out, *n_free_out, *status;
     int32_t n, shift, max_blocks, n_blocks, T;
+    bool map_here;
 };
 
-// Exclusive sum over the workgroup's threads, and the total.
-template <class V>
-__device__ __forceinline__ V block_scan(V v, V* wave_sums, V* total) {
+// Exclusive sums of two values over the workgroup's threads, and the totals.
+struct Sums { int64_t u, v, all_u, all_v; };
+
+__device__ __forceinline__ Sums block_scan(int64_t u, int64_t v, int64_t (*wave_sums)[2]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    V inc = v;
+    int64_t iu = u, iv = v;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const V up = __shfl_up(inc, d);
-        if (lane >= d) inc += up;
+        const int64_t pu = __shfl_up(iu, d), pv = __shfl_up(iv, d);
+        if (lane >= d) { iu += pu; iv += pv; }
     }
-    if (lane == 63) wave_sums[wave] = inc;
+    if (lane == 63) { wave_sums[wave][0] = iu; wave_sums[wave][1] = iv; }
     __syncthreads();
-    V before = 0, all = 0;
+    Sums s{iu - u, iv - v, 0, 0};
     for (int w = 0; w < waves; ++w) {
-        const V s = wave_sums[w];
-        if (w < wave) before += s;
-        all += s;
+        const int64_t wu = wave_sums[w][0], wv = wave_sums[w][1];
+        if (w < wave) { s.u += wu; s.v += wv; }
+        s.all_u += wu;
+        s.all_v += wv;
     }
-    __syncthreads();
-    *total = all;
-    return before + inc - v;
+    return s;
 }
 
 // The last i in [0, n] with start[i] <= x; start[0] <= x, start does not fall.
@@ -57,13 +58,27 @@ __device__ __forceinline__ int owner(const int32_t* start, int n, int32_t x) {
 
 __device__ __forceinline__ int32_t capped(int64_t v) { return v > 0x7fffffff ? 0x7fffffff : int32_t(v); }
 
+constexpr int kMapTokens = 1024;   // of one workgroup of slot_map_kernel
+
+__device__ __forceinline__ void map_token(const SlotArgs& a, const int32_t* start, const int32_t* from, int32_t e) {
+    const int i = owner(start, a.n, e);
+    int32_t slot = -1, pos = -1;
+    if (i < a.n && from[i] >= 0) {
+        pos = from[i] + (e - start[i]);
+        const int32_t id = a.table[int64_t(i) * a.max_blocks + (pos >> a.shift)];
+        if (id >= 0 && id < a.n_blocks) slot = (id << a.shift) + (pos & ((1 << a.shift) - 1));
+    }
+    a.slots[e] = slot;
+    if (a.positions) a.positions[e] = pos;
+}
+
 // One workgroup: every request's place in the step's token batch, in the blocks that
 // come back and in the blocks that are taken is a prefix sum over the requests; the
 // entries behind each sum are then written flat over the threads, each finding its
-// request by bisection of the sums in LDS.  Work is a few KB, so the time is that of
-// the dependent loads (lengths, free stack, tables) and of two scans.
+// request by bisection of the sums in LDS.  A decode step's work is a few KB, so the time
+// is that of the dependent loads (lengths, free stack, tables) and of two scans.
 __global__ __launch_bounds__(kSlotThreads) void slots_kernel(SlotArgs a) {
-    __shared__ int64_t sums[2][kSlotThreads / 64];
+    __shared__ int64_t sums[2][kSlotThreads / 64][2];
     __shared__ int32_t start[kMaxSeqs + 1], back_at[kMaxSeqs + 1], take_at[kMaxSeqs + 1];
     __shared__ int32_t from[kMaxSeqs];       // position of the first new token, -1: not served
     __shared__ int32_t taken_all;
@@ -87,10 +102,10 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(SlotArgs a) {
             if (add[j] < 0 && st[j] == 0) my_back += held[j];
         }
     }
-    int64_t all_add, all_back;
-    int64_t at_add = block_scan(my_add, sums[0], &all_add);
-    int64_t at_back = block_scan(my_back, sums[1], &all_back);
     const int32_t n_free = min(max(*a.n_free, 0), a.n_blocks);
+    const Sums of_add = block_scan(my_add, my_back, sums[0]);
+    const int64_t all_add = of_add.all_u, all_back = of_add.all_v;
+    int64_t at_add = of_add.u, at_back = of_add.v;
     const int64_t top = min(n_free + all_back, int64_t(a.n_blocks));
     int64_t my_need = 0;
 #pragma unroll
@@ -110,8 +125,9 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(SlotArgs a) {
             }
         }
     }
-    int64_t all_need;
-    int64_t at_need = block_scan(my_need, sums[0], &all_need);
+    const Sums of_need = block_scan(my_need, 0, sums[1]);
+    const int64_t all_need = of_need.all_u;
+    int64_t at_need = of_need.u;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const int i = t * per + j;
@@ -149,16 +165,25 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(SlotArgs a) {
         a.table[int64_t(i) * a.max_blocks + blocks + (e - take_at[i])] = a.free_blocks[int32_t(top) - 1 - e];
     }
     __syncthreads();
-    for (int32_t e = t; e < a.T; e += blockDim.x) {
-        const int i = owner(start, n, e);
-        int32_t slot = -1, pos = -1;
-        if (i < n && from[i] >= 0) {
-            pos = from[i] + (e - start[i]);
-            const int32_t id = a.table[int64_t(i) * a.max_blocks + (pos >> a.shift)];
-            if (id >= 0 && id < a.n_blocks) slot = (id << a.shift) + (pos & (bs - 1));
+    if (!a.map_here) return;
+    for (int32_t e = t; e < a.T; e += blockDim.x) map_token(a, start, from, e);
+}
+
+// The slot map of many tokens, over the chip: the first kernel's outputs, in LDS.
+__global__ __launch_bounds__(256) void slot_map_kernel(SlotArgs a) {
+    __shared__ int32_t start[kMaxSeqs + 1], from[kMaxSeqs];
+    for (int i = threadIdx.x; i <= a.n; i += 256) {
+        start[i] = a.seq_start[i];
+        if (i < a.n) {                   // a served request's tokens end at its new length
+            const int32_t count = a.seq_start[i + 1] - a.seq_start[i];
+            from[i] = count > 0 && a.status[i] == 0 ? a.lens_out[i] - count : -1;
         }
-        a.slots[e] = slot;
-        if (a.positions) a.positions[e] = pos;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMapTokens / 256; ++k) {
+        const int64_t e = int64_t(blockIdx.x) * kMapTokens + 256 * k + threadIdx.x;
+        if (e < a.T) map_token(a, start, from, int32_t(e));
     }
 }
 
@@ -174,12 +199,6 @@ struct AppendArgs {
     int32_t T, window, n_heads, head_dim, shift;
 };
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
-}
-
 template <bool E4M3>
 __device__ __forceinline__ float wanted_scale(float amax) {
     if (!(amax > 0.f)) return 0.f;
@@ -191,7 +210,7 @@ __device__ __forceinline__ float wanted_scale(float amax) {
     return amax * (1.0f / 127.0f);
 }
 
-// Four scaled values as one word of codes.
+// Four scaled values as one word of codes; any values.
 template <bool E4M3>
 __device__ __forceinline__ uint32_t encode(const float v[4]) {
     float c[4];
@@ -210,133 +229,292 @@ __device__ __forceinline__ uint32_t encode(const float v[4]) {
     return w;
 }
 
-__device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
-__device__ __forceinline__ f32x4 load4(const uint16_t* p) {
-    const u32x2 w = *reinterpret_cast<const u32x2*>(p);
-    return f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                 __uint_as_float(w.y & 0xffff0000u)};
-}
-
-// A 16-byte unit of a code tile: lane (g, m) of slab s holds, of a key tile, token m and
-// channels 64s + 16g .. +16; of a value tile, tokens 4g .. +4 and channels 64s + 4m .. +4.
-// x[i] is the value of byte i, 0 where the byte's token is not among the call's (new_at).
-template <bool V, class T>
-__device__ __forceinline__ void load_unit(float x[16], const T* row0, int64_t stride, int tile, int s, int g, int m,
-                                          int fill, int end) {
-    if constexpr (V) {
+// Sixteen values x over a scale, as the codes of one unit.  Dividing costs about ten
+// operations a value, more than all the rest; the product with the reciprocal r costs one.
+// E4M3: the scale is a power of two, the product is the quotient.  INT8: x r + 1.5 * 2^23
+// rounds the exact product to a whole number, whose low byte is the code; the product is
+// off by at most 127.5 * 2^-24, so only where it lies within 2^-14 of a tie can the
+// quotient's own rounding matter, and the wave divides after all.
+template <bool E4M3>
+__device__ __forceinline__ u32x4 encode_unit(const float x[16], float div, float r, bool exact) {
+    u32x4 w;
+    if (!exact) {
+        if constexpr (E4M3) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int tok = tile * kTok + 4 * g + k;
-            f32x4 v = {0.f, 0.f, 0.f, 0.f};
-            if (tok >= fill && tok < end) v = load4(row0 + (tok - fill) * stride + 64 * s + 4 * m);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[4 * j + k] = v[j];
+            for (int q = 0; q < 4; ++q) {
+                const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * q] * r, x[4 * q + 1] * r, 0, false);
+                w[q] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(x[4 * q + 2] * r, x[4 * q + 3] * r, lo, true));
+            }
+            return w;
         }
-    } else {
-        const int tok = tile * kTok + m;
-        const bool in = tok >= fill && tok < end;
+        constexpr float magic = 12582912.f;
+        float off = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            f32x4 v = {0.f, 0.f, 0.f, 0.f};
-            if (in) v = load4(row0 + (tok - fill) * stride + 64 * s + 16 * g + 4 * k);
+        for (int q = 0; q < 4; ++q) {
+            uint32_t c[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[4 * k + j] = v[j];
+            for (int i = 0; i < 4; ++i) {
+                const float n = __builtin_fmaf(x[4 * q + i], r, magic);
+                c[i] = __float_as_uint(n);
+                off = fmaxf(off, fabsf(__builtin_fmaf(x[4 * q + i], r, magic - n)));
+            }
+            w[q] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(c[3], c[2], 0x0c0c0400), __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400), 0x05040100);
         }
+        if (!__any(off > 0.5f - 0x1p-14f)) return w;
     }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float v[4] = {x[4 * q] / div, x[4 * q + 1] / div, x[4 * q + 2] / div, x[4 * q + 3] / div};
+        w[q] = encode<E4M3>(v);
+    }
+    return w;
 }
 
-// One wave, one (run, head, keys or values): a run is the tokens of one block that the
-// call brings, places [fill, end).
-template <bool E4M3, bool V, class T>
-__device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, int64_t block, int fill, int end, int head) {
-    const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+template <bool E4M3>
+__device__ __forceinline__ u32x4 rescale_unit(const u32x4 w, float ratio) {
+    u32x4 res;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float v[4] = {code_value<E4M3, 0>(w[q]) * ratio, code_value<E4M3, 1>(w[q]) * ratio, code_value<E4M3, 2>(w[q]) * ratio,
+                            code_value<E4M3, 3>(w[q]) * ratio};
+        res[q] = encode<E4M3>(v);
+    }
+    return res;
+}
+
+// Four neighbouring channels of one token, as loaded.
+template <class T> struct Quad;
+template <> struct Quad<float> {
+    f32x4 v;
+    __device__ void load(const float* p) { v = *reinterpret_cast<const f32x4*>(p); }
+    __device__ void clear() { v = f32x4{0.f, 0.f, 0.f, 0.f}; }
+    __device__ float at(int j) const { return v[j]; }
+    // the largest |bits|: above every finite value's where one is infinite or NaN
+    __device__ uint32_t top() const {
+        const u32x4 b = __builtin_bit_cast(u32x4, v) & 0x7fffffffu;
+        return max(max(b.x, b.y), max(b.z, b.w));
+    }
+};
+template <> struct Quad<uint16_t> {
+    u32x2 v;
+    __device__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x2*>(p); }
+    __device__ void clear() { v = u32x2{0, 0}; }
+    __device__ float at(int j) const { return __uint_as_float(j & 1 ? v[j / 2] & 0xffff0000u : v[j / 2] << 16); }
+    __device__ uint32_t top() const {
+        const uint32_t a = v.x & 0x7fff7fffu, b = v.y & 0x7fff7fffu;
+        return max(max(a << 16, a & 0xffff0000u), max(b << 16, b & 0xffff0000u));
+    }
+};
+
+// The tokens of one block that the call brings, places [fill, end), for one head's keys
+// or values, by THREADS threads (a wave, or a workgroup of 256), each with KEEP units in
+// registers between the maximum and the codes (more are read again).  A unit is 16
+// bytes of a code tile: lane (g, m) of slab s holds, of a key tile, token m and channels
+// 64s + 16g .. +16; of a value tile, tokens 4g .. +4 and channels 64s + 4m .. +4.
+template <bool E4M3, bool V, class T, int THREADS, int KEEP>
+__device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, int64_t block, int fill, int end, int head, uint32_t* lds) {
+    const int tid = THREADS == 64 ? threadIdx.x & 63 : threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, m = lane & 15;
     const int D = a.head_dim, slabs = D / 64;
     const int64_t bh = block * a.n_heads + head;
     uint8_t* codes = a.codes[V] + ((bh * D) << a.shift);
     const int64_t stride = a.stride[V];
     const T* row0 = static_cast<const T*>(a.x[V]) + int64_t(token) * stride + int64_t(head) * D;
-    const float old = fill > 0 ? a.scales[V][bh] : 0.f;
-    float amax = 0.f;
-    for (int tile = fill / kTok; tile * kTok < end; ++tile)
-        for (int s = 0; s < slabs; ++s) {
-            float x[16];
-            load_unit<V>(x, row0, stride, tile, s, g, m, fill, end);
+    const float old_scale = fill > 0 ? a.scales[V][bh] : 0.f;
+    const int tile0 = fill / kTok, chunks = ((end - 1) / kTok + 1 - tile0) * slabs;   // 64 units each
+
+    Quad<T> x[KEEP][4];
+    u32x4 old[THREADS == 64 ? KEEP : 1];
+    auto first_token = [&](int tile) { return tile * kTok + (V ? 4 * g : m); };
+    auto unit_at = [&](int tile, int s) { return reinterpret_cast<u32x4*>(codes + int64_t(tile) * kTok * D + s * 1024 + lane * 16); };
+    // a unit that also holds tokens of before, or bytes behind the last
+    auto boundary = [&](bool in, int tile, int s) {
+        const int first = first_token(tile);
+        u32x4 w = {0, 0, 0, 0};
+        if (in && first < end && (first < fill || (V && first + 4 > end))) w = *unit_at(tile, s);
+        return w;
+    };
+    auto load = [&](int c0) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float v = fabsf(x[i]);
-                amax = v <= 3.4028235e38f ? fmaxf(amax, v) : amax;      // NaN and infinities do not count
+        for (int i = 0; i < KEEP; ++i) {
+            const int c = c0 + i * (THREADS / 64) + wave;
+            const int tile = tile0 + c / slabs, s = c % slabs, first = first_token(tile);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int tok = V ? first + k : first;
+                x[i][k].clear();
+                if (c < chunks && tok >= fill && tok < end)
+                    x[i][k].load(row0 + (tok - fill) * stride + 64 * s + (V ? 4 * m : 16 * g + 4 * k));
             }
+            if constexpr (THREADS == 64) old[i] = boundary(c < chunks, tile, s);   // early: few waves, so latency counts
         }
-    const float wanted = wanted_scale<E4M3>(wave_max(amax));
-    const bool grew = wanted > old;
-    const float now = grew ? wanted : old, div = now > 0.f ? now : 1.f;
-    const float ratio = old / div;
-    if (lane == 0 && (grew || fill == 0)) a.scales[V][bh] = now;
-    for (int tile = grew ? 0 : fill / kTok; tile * kTok < end; ++tile)
-        for (int s = 0; s < slabs; ++s) {
-            const int first = tile * kTok + (V ? 4 * g : m), last = first + (V ? 4 : 1);   // the unit's tokens
-            if (first >= end || (!grew && last <= fill)) continue;
-            u32x4* unit = reinterpret_cast<u32x4*>(codes + int64_t(tile) * kTok * D + s * 1024 + lane * 16);
-            u32x4 w = {0, 0, 0, 0};
-            if (first < fill || last > end) w = *unit;
-            float x[16];
-            load_unit<V>(x, row0, stride, tile, s, g, m, fill, end);
-            u32x4 res;
+    };
+    constexpr int round = KEEP * (THREADS / 64);
+    const bool once = chunks <= round;
+    uint32_t top = 0;
+    for (int c0 = 0; c0 < chunks; c0 += round) {
+        load(c0);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float fresh[4], kept[4];
+        for (int i = 0; i < KEEP; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) fresh[k] = x[4 * q + k] / div;
-                kept[0] = code_value<E4M3, 0>(w[q]) * ratio;
-                kept[1] = code_value<E4M3, 1>(w[q]) * ratio;
-                kept[2] = code_value<E4M3, 2>(w[q]) * ratio;
-                kept[3] = code_value<E4M3, 3>(w[q]) * ratio;
-                const uint32_t nw = encode<E4M3>(fresh), ow = grew ? encode<E4M3>(kept) : w[q];
-                uint32_t mask = 0;                  // bytes whose tokens are new
+            for (int k = 0; k < 4; ++k) top = max(top, x[i][k].top());
+    }
+    auto reduce = [&](uint32_t v) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int tok = V ? first + k : first;
-                    if (tok >= fill && tok < end) mask |= 255u << (8 * k);
-                }
-                res[q] = (nw & mask) | (ow & ~mask);
+        for (int d = 32; d; d >>= 1) v = max(v, uint32_t(__shfl_xor(int(v), d)));
+        if constexpr (THREADS > 64) {
+            __syncthreads();
+            if (lane == 0) lds[wave] = v;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < THREADS / 64; ++w) v = max(v, lds[w]);
+        }
+        return uint32_t(__builtin_amdgcn_readfirstlane(int(v)));
+    };
+    top = reduce(top);
+    const bool finite = top < 0x7f800000u;
+    if (!finite) {                       // the largest of the finite values
+        top = 0;
+        for (int c0 = 0; c0 < chunks; c0 += round) {
+            load(c0);
+#pragma unroll
+            for (int i = 0; i < KEEP; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t b = __float_as_uint(x[i][k].at(j)) & 0x7fffffffu;
+                        if (b < 0x7f800000u) top = max(top, b);
+                    }
+        }
+        top = reduce(top);
+    }
+    const float wanted = wanted_scale<E4M3>(__uint_as_float(top));
+    const bool grew = wanted > old_scale;
+    const float now = grew ? wanted : old_scale, div = now > 0.f ? now : 1.f;
+    const float r = 1.f / div, ratio = old_scale / div;
+    const bool exact = !finite || !(div >= 0x1p-126f);      // smaller ones have no reciprocal
+    if (tid == 0 && (grew || fill == 0)) a.scales[V][bh] = now;
+    for (int c0 = 0; c0 < chunks; c0 += round) {
+        if (!once) load(c0);
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) {
+            const int c = c0 + i * (THREADS / 64) + wave;
+            if (c >= chunks) break;
+            const int tile = tile0 + c / slabs, s = c % slabs, first = first_token(tile);
+            float v[16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[V ? 4 * j + k : 4 * k + j] = x[i][k].at(j);
+            const u32x4 fresh = encode_unit<E4M3>(v, div, r, exact);
+            if (first >= end || (!grew && first + (V ? 4 : 1) <= fill)) continue;
+            uint32_t mask = 0;           // bytes of a word whose tokens are new
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int tok = V ? first + k : first;
+                if (tok >= fill && tok < end) mask |= 255u << (8 * k);
             }
-            *unit = res;
+            u32x4 kept;
+            if constexpr (THREADS == 64) kept = old[i];
+            else kept = boundary(true, tile, s);
+            if (grew && fill > 0) kept = rescale_unit<E4M3>(kept, ratio);
+            *unit_at(tile, s) = (fresh & mask) | (kept & ~mask);
+        }
+    }
+    if (grew)                            // tiles that hold old tokens alone
+        for (int c = wave; c < tile0 * slabs; c += THREADS / 64) {
+            u32x4* unit = unit_at(c / slabs, c % slabs);
+            *unit = rescale_unit<E4M3>(*unit, ratio);
         }
 }
 
-// Each wave looks through a window of tokens for the first token of a run and takes the
-// runs that begin there; the waves of a workgroup take neighbouring (head, keys or
-// values), which lie side by side in the tokens' rows.
+// What a wave sees of the slots from token t0 on: lane l holds token t0 + l's; a bit of
+// `starts` is a token that begins a run, of `more[0]`, `more[1]` one of the first 128 that
+// goes on with its predecessor's run (the next place of the same block).
+struct Look {
+    int32_t slot;
+    uint64_t starts, more[2];
+};
+
+__device__ __forceinline__ Look look_at(const AppendArgs& a, int32_t t0) {
+    const int lane = threadIdx.x & 63, in_block = (1 << a.shift) - 1;
+    int32_t slot[2], prev[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int32_t t = t0 + 64 * h + lane;
+        slot[h] = t < a.T ? a.slots[t] : -1;
+        prev[h] = t < a.T && t > 0 ? a.slots[t - 1] : -2;
+    }
+    Look k;
+    k.slot = slot[0];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const bool good = slot[h] >= 0 && slot[h] < a.n_slots, goes_on = good && prev[h] == slot[h] - 1 && (slot[h] & in_block) != 0;
+        k.more[h] = __ballot(goes_on);
+        if (h == 0) k.starts = __ballot(good && !goes_on && lane < a.window);
+    }
+    return k;
+}
+
+// Tokens of the run that begins at bit l, `first` its slot.
+__device__ __forceinline__ int run_length(const AppendArgs& a, const Look& k, int32_t t0, int l, int32_t first) {
+    const uint64_t rest = l < 63 ? k.more[0] >> (l + 1) : 0;
+    int count = 1 + __builtin_ctzll(~rest);            // a shift leaves a zero at the top
+    if (count < 64 - l) return count;
+    count = 64 - l + (~k.more[1] ? __builtin_ctzll(~k.more[1]) : 64);
+    if (count < 128 - l) return count;
+    const int lane = threadIdx.x & 63, most = (1 << a.shift) - (first & ((1 << a.shift) - 1));
+    for (int at = count; at < most; at += 64) {        // a long run of a large block
+        const int i = at + lane;
+        const uint64_t off = ~__ballot(i < most && t0 + l + i < a.T && a.slots[t0 + l + i] == first + i);
+        count = at + (off ? __builtin_ctzll(off) : 64);
+        if (off) break;
+    }
+    return count;
+}
+
+// Few tokens: a wave for each (token, head, keys or values), busy where the token begins
+// a run.  The waves of a workgroup take neighbouring heads, which lie side by side.
 template <bool E4M3, class T>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int hw = blockIdx.y * 4 + wave;
+    const int hw = blockIdx.y * 4 + (threadIdx.x >> 6);
     if (hw >= 2 * a.n_heads) return;
     const int head = hw % a.n_heads;
-    const bool values = hw >= a.n_heads;
-    const int bs = 1 << a.shift;
+    const int32_t t0 = int32_t(blockIdx.x);
+    const Look k = look_at(a, t0);
+    if (!k.starts) return;
+    const int32_t first = __builtin_amdgcn_readfirstlane(k.slot);
+    const int fill = first & ((1 << a.shift) - 1), end = fill + run_length(a, k, t0, 0, first);
+    if (hw >= a.n_heads) append_run<E4M3, true, T, 64, 4>(a, t0, first >> a.shift, fill, end, head, nullptr);
+    else append_run<E4M3, false, T, 64, 4>(a, t0, first >> a.shift, fill, end, head, nullptr);
+}
+
+// Many tokens: a workgroup for each (window of tokens, head, keys or values).  Long runs
+// are taken by the whole workgroup, so that prompts are read once and all their loads are
+// in flight together; short ones (a wave's units at most) by one wave each.
+template <bool E4M3, class T>
+__global__ __launch_bounds__(256) void append_window_kernel(AppendArgs a) {
+    __shared__ uint32_t lds[4];
+    constexpr int kept = 2;            // fewer registers, more workgroups in flight
+    const int wave = threadIdx.x >> 6;
+    const int head = blockIdx.y % a.n_heads;
+    const bool values = int(blockIdx.y) >= a.n_heads;
     const int32_t t0 = int32_t(blockIdx.x) * a.window;
-    const int32_t mine = t0 + lane;
-    const int32_t slot = mine < a.T ? a.slots[mine] : -1;
-    const int32_t prev = mine < a.T && mine > 0 ? a.slots[mine - 1] : -2;
-    const bool good = slot >= 0 && slot < a.n_slots;
-    const bool leads = good && lane < a.window && (prev != slot - 1 || (slot & (bs - 1)) == 0);
-    uint64_t todo = __ballot(leads);
-    while (todo) {
+    const Look k = look_at(a, t0);                     // the same in every wave
+    uint64_t todo = k.starts;
+    for (int turn = 0; todo; ++turn) {
         const int l = __builtin_ctzll(todo);
         todo &= todo - 1;
-        const int32_t first = __shfl(slot, l), token = t0 + l;
-        const int fill = first & (bs - 1);
-        int count = 1;
-        for (int at = 1; at < bs - fill; at += 64) {
-            const int k = at + lane;
-            const bool on = k < bs - fill && token + k < a.T && a.slots[token + k] == first + k;
-            const uint64_t off = ~__ballot(on);
-            count = at + (off ? __builtin_ctzll(off) : 64);
-            if (off) break;
+        const int32_t first = __builtin_amdgcn_readlane(k.slot, l), token = t0 + l;
+        const int fill = first & ((1 << a.shift) - 1), end = fill + run_length(a, k, t0, l, first);
+        if (((end - 1) / kTok + 1 - fill / kTok) * a.head_dim > 64 * kept) {
+            if (values) append_run<E4M3, true, T, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
+            else append_run<E4M3, false, T, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
+        } else if (turn % 4 == wave) {
+            if (values) append_run<E4M3, true, T, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
+            else append_run<E4M3, false, T, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
         }
-        if (values) append_run<E4M3, true, T>(a, token, first >> a.shift, fill, fill + count, head);
-        else append_run<E4M3, false, T>(a, token, first >> a.shift, fill, fill + count, head);
     }
 }
 
@@ -350,9 +528,9 @@ struct GatherArgs {
     int32_t n_slots, T, n_heads, head_dim, shift;
 };
 
-__device__ __forceinline__ void store4(float* p, const f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+__device__ __forceinline__ void store4(float* p, const f32x4 v) { __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(p)); }
 __device__ __forceinline__ void store4(uint16_t* p, const f32x4 v) {
-    *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    __builtin_nontemporal_store(u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}, reinterpret_cast<u32x2*>(p));
 }
 
 constexpr int kGatherTokens = 4;   // tokens of one thread
@@ -440,8 +618,14 @@ mbd_status mbd_kv_slots(const mbd_kv_pool* pool, const int32_t* new_tokens, cons
     if (T > 0 && !slots) return fail(MBD_EINVAL, "NULL argument");
     if (!kv::aligned(slots, 4) || !kv::aligned(positions, 4)) return fail(MBD_EALIGN, "int32 arrays must be 4-byte aligned");
     kv::SlotArgs a{new_tokens, lens, held, n_free, pool->block_table, pool->free_blocks, seq_start, slots, positions, lens_out, held_out,
-                   n_free_out, status, pool->n_seqs, kv::log2_of(pool->block_size), pool->max_blocks, pool->n_blocks, T};
-    hipLaunchKernelGGL(kv::slots_kernel, dim3(1), dim3(kv::kSlotThreads), 0, reinterpret_cast<hipStream_t>(stream), a);
+                   n_free_out, status, pool->n_seqs, kv::log2_of(pool->block_size), pool->max_blocks, pool->n_blocks, T,
+                   T <= 2 * kv::kSlotThreads};
+    // a step that decodes has few entries behind its sums: fewer waves meet at the barriers sooner
+    const int threads = pool->n_seqs <= 256 && T <= 256 ? 256 : kv::kSlotThreads;
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    hipLaunchKernelGGL(kv::slots_kernel, dim3(1), dim3(threads), 0, s, a);
+    if (!a.map_here)
+        hipLaunchKernelGGL(kv::slot_map_kernel, dim3(unsigned((int64_t(T) + kv::kMapTokens - 1) / kv::kMapTokens)), dim3(256), 0, s, a);
     return hip_check("slots launch");
 }
 
@@ -455,21 +639,27 @@ mbd_status mbd_kv_append(const mbd_kv_cache* cache, const void* k, const void* v
     if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8)
         return fail(MBD_ESHAPE, "token strides must be multiples of 8 and at least n_heads * head_dim");
     if (T == 0) return MBD_OK;
-    // Waves look through windows of tokens: one token each while that gives no more waves than
-    // the chip holds twice over, longer windows beyond, so that idle waves do not add up.
+    // A wave a token until that is twice the chip's waves, then workgroups over windows that
+    // keep it full: 13 prompts of 16.4k tokens together took 88 us with a wave a run.
     const int64_t waves = int64_t(T) * 2 * cache->n_heads;
     int32_t window = 1;
-    while (window < 64 && waves / window > 16384) window *= 2;
+    while (window < 64 && waves / window > 4096) window *= 2;
+    const bool few = waves <= 16384;
+    if (few) window = 1;
     kv::AppendArgs a{{static_cast<uint8_t*>(cache->k_codes), static_cast<uint8_t*>(cache->v_codes)}, {cache->k_scale, cache->v_scale},
                      {k, v}, {k_stride, v_stride}, slots, int32_t(cache->n_blocks * cache->block_size), T, window, cache->n_heads,
                      cache->head_dim, kv::log2_of(cache->block_size)};
-    const dim3 grid(unsigned((T + window - 1) / window), unsigned((2 * cache->n_heads + 3) / 4));
+    const dim3 grid(unsigned((T + window - 1) / window), unsigned(few ? (2 * cache->n_heads + 3) / 4 : 2 * cache->n_heads));
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    const bool e4m3 = cache->fmt == MBD_KV_E4M3, wide = dtype == MBD_F32;
-    if (e4m3 && wide) hipLaunchKernelGGL((kv::append_kernel<true, float>), grid, dim3(256), 0, s, a);
-    else if (e4m3) hipLaunchKernelGGL((kv::append_kernel<true, uint16_t>), grid, dim3(256), 0, s, a);
-    else if (wide) hipLaunchKernelGGL((kv::append_kernel<false, float>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((kv::append_kernel<false, uint16_t>), grid, dim3(256), 0, s, a);
+    const bool wide = dtype == MBD_F32;
+    const auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a); };
+    if (cache->fmt == MBD_KV_E4M3) {
+        if (few) wide ? run(kv::append_kernel<true, float>) : run(kv::append_kernel<true, uint16_t>);
+        else wide ? run(kv::append_window_kernel<true, float>) : run(kv::append_window_kernel<true, uint16_t>);
+    } else {
+        if (few) wide ? run(kv::append_kernel<false, float>) : run(kv::append_kernel<false, uint16_t>);
+        else wide ? run(kv::append_window_kernel<false, float>) : run(kv::append_window_kernel<false, uint16_t>);
+    }
     return hip_check("append launch");
 }
 

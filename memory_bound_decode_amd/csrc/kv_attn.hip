@@ -24,8 +24,8 @@ constexpr int kWaves = 4;              // waves of a workgroup; each takes every
 constexpr int kStep = 2;               // tiles of one step: 32 tokens, the k of an MFMA
 constexpr int kRefill = 64 / kStep;    // steps whose block ids and scales one lane each holds
 constexpr int kMaxSeqs = 4096;
-constexpr int kMinChunk = 8;           // tiles: a workgroup's least share of a request
-constexpr int kTargetBlocks = 1024;    // workgroups that a call aims at
+constexpr int kMinShare = kWaves * kStep;   // tiles: a workgroup's least share
+constexpr int kCus = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -39,7 +39,8 @@ struct AttnArgs {
     float *lse, *part_o, *part_ml;
     const float* slopes;
     int64_t q_stride, out_stride;
-    int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, target;
+    int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, shares;
+    bool by_seq;
     float scale, softcap;
 };
 
@@ -84,64 +85,66 @@ __device__ __forceinline__ int wave_before(int v) {
     return inc - v;
 }
 
-// The lengths are known on the device alone, so every wave cuts the work up itself: all
-// tiles over the calls's aimed-at number of workgroups is a chunk, each request is
-// ceil(tiles / chunk) items, and an item's request follows from the prefix sums.  That is
-// two scans of 64 lanes, next to the table lookup that waits for the lengths anyway.
-struct Item {
-    int32_t seq, part, parts, slot, chunk;   // slot: of the first part's partial result
+// The lengths are known on the device alone, so every wave cuts the work up itself: the
+// requests' tiles stand in one row, and each workgroup of a head takes an equal share of
+// it, whatever requests that meets, so all end together.  A request that falls into
+// several shares is joined from their partial results.  What a workgroup has to know
+// is one prefix sum of the requests' tiles: a scan of 64 lanes.  Where the requests alone
+// fill the chip (by_seq), each has a workgroup of its own and nothing is joined.
+__device__ __forceinline__ int tiles_of(const Seq& s) { return s.n_new < 1 ? 0 : max(s.hi - s.lo, 1); }
+
+struct Place {
+    int32_t seq, start, share;   // a request, its first tile in the row of all, tiles of a share
 };
 
-__device__ __forceinline__ int parts_of(const Seq& s, int32_t chunk) {
-    return s.n_new < 1 ? 0 : (max(s.hi - s.lo, 1) - 1) / chunk + 1;
-}
-
-// By item (by_seq false) or by request; seq is -1 if there is none.
-__device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, bool by_seq) {
+// The request that holds tile blockIdx-share's first tile (by_seq false), or request `want`.
+__device__ __forceinline__ Place find_place(const AttnArgs& a, int32_t want, bool is_seq) {
     const int lane = threadIdx.x & 63;
     const int per = (a.n_seqs + 63) / 64;
     const int i0 = min(lane * per, a.n_seqs), i1 = min(i0 + per, a.n_seqs);
-    int tiles = 0;
+    int mine = 0;
+    for (int i = i0; i < i1; ++i) mine += tiles_of(load_seq(a, i));
+    const int before = wave_before(mine);
+    const int total = __builtin_amdgcn_readlane(before + mine, 63);
+    Place p;
+    p.share = max(kMinShare, ((max(total, 1) - 1) / a.shares + kStep) / kStep * kStep);
+    const int64_t target = is_seq ? 0 : int64_t(want) * p.share;
+    int seq = -1, start = before, at = before;
     for (int i = i0; i < i1; ++i) {
-        const Seq s = load_seq(a, i);
-        if (s.n_new > 0) tiles += max(s.hi - s.lo, 0);
-    }
-    tiles = wave_sum(tiles);
-    Item it;
-    it.chunk = 0x7fffff00;
-    if (a.target > 1) {
-        const int round = kWaves * kStep;
-        it.chunk = max(kMinChunk, ((max(tiles, 1) - 1) / a.target + round) / round * round);
-    }
-    int items = 0, split = 0;
-    for (int i = i0; i < i1; ++i) {
-        const int p = parts_of(load_seq(a, i), it.chunk);
-        items += p;
-        split += p > 1 ? p : 0;
-    }
-    int item0 = wave_before(items), slot0 = wave_before(split);
-    int seq = -1, part = 0, parts = 0, slot = 0;
-    for (int i = i0; i < i1; ++i) {
-        const int p = parts_of(load_seq(a, i), it.chunk);
-        if (by_seq ? i == want : want >= item0 && want < item0 + p) {
+        const int n = tiles_of(load_seq(a, i));
+        if (is_seq ? i == want : target >= at && target < at + n) {
             seq = i;
-            part = by_seq ? 0 : want - item0;
-            parts = p;
-            slot = slot0;
+            start = at;
         }
-        item0 += p;
-        slot0 += p > 1 ? p : 0;
+        at += n;
     }
     const uint64_t who = __ballot(seq >= 0);
-    it.seq = -1;
+    p.seq = -1;
+    p.start = 0;
     if (who) {
         const int l = __builtin_ctzll(who);
-        it.seq = __builtin_amdgcn_readlane(seq, l);
-        it.part = __builtin_amdgcn_readlane(part, l);
-        it.parts = __builtin_amdgcn_readlane(parts, l);
-        it.slot = __builtin_amdgcn_readlane(slot, l);
+        p.seq = __builtin_amdgcn_readlane(seq, l);
+        p.start = __builtin_amdgcn_readlane(start, l);
     }
-    return it;
+    return p;
+}
+
+// Shares that a request falls into, and where each leaves its partial result: a share
+// has at most two requests that it does not hold whole, its first and its last.
+struct Parts {
+    int32_t first, count;
+};
+
+__device__ __forceinline__ Parts parts_of(int start, int tiles, int share) {
+    const int f = start / share;
+    return {f, (start + tiles - 1) / share - f + 1};
+}
+
+__device__ __forceinline__ int64_t part_slot(int start, int share, int w) { return 2 * int64_t(w) + (start >= int64_t(w) * share ? 1 : 0); }
+
+__device__ __forceinline__ float lane_max(float v) {     // over the four lanes of a query row
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
 }
 
 // ---------------------------------------------------------------- operands
@@ -157,6 +160,9 @@ __device__ __forceinline__ bf16x8 operand(uint32_t w0, uint32_t w1) {
         r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true));
     } else {
         // |code| <= 127 leaves the low half of its fp32 form zero: the high halves are the bf16s
+        // (the empty asm keeps the words whole until here: taken apart at their loads, each byte
+        // would hold a register of its own while the step is in flight)
+        asm("" : "+v"(w0), "+v"(w1));
         const uint32_t w[2] = {w0, w1};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -176,35 +182,55 @@ __device__ __forceinline__ uint32_t live_bytes(int tok, int len) {
     return n == 4 ? 0xffffffffu : (1u << (8 * n)) - 1u;
 }
 
+// Codes unpacked far ahead of their product would cost a wave or two a SIMD in registers.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
 __device__ __forceinline__ float lane_float(float v, int l) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
 }
 
-template <int DQ>
-struct Step {           // one step's codes: two tiles of keys and of values
-    u32x4 k[kStep][DQ], v[kStep][DQ];
-};
+// Workgroups a CU (waves a SIMD) that a variant's registers are held to: enough loads in
+// flight for the memory, and as many shares as there are places for them.
+constexpr int per_cu(int dq, int nt) { return dq * nt == 1 ? 4 : dq * nt == 2 ? 3 : dq * nt <= 4 ? 2 : 1; }
 
 // DQ = head_dim / 64, NT = tiles of 16 query rows, EXT: cap, window or distance bias.
 template <bool E4M3, int DQ, int NT, bool EXT>
-__global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per_cu(DQ, NT)))) void attn_kernel(AttnArgs a) {
     constexpr int D = 64 * DQ, ROWS = 16 * NT, PITCH = 68;
     __shared__ float merge[kWaves][ROWS][PITCH];     // pitch: rows 4 banks apart
     __shared__ float merge_m[kWaves][ROWS], merge_l[kWaves][ROWS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, n = lane & 15;
     const int head = blockIdx.y % a.n_kv, r0 = blockIdx.y / a.n_kv * ROWS;
-    const Item it = find_item(a, blockIdx.x, false);
-    if (it.seq < 0) return;
-    const Seq sq = load_seq(a, it.seq);
-    if (r0 >= sq.rows) return;
+    const int w = blockIdx.x, in_block = (1 << a.shift) - 1;
+    Place at = {w, 0, 0};
+    if (!a.by_seq) {
+        at = find_place(a, w, false);
+        if (at.seq < 0) return;
+    }
+  for (int todo = at.share, from = w * at.share; ;) {
+    // the request's part in this share: tiles [skip, skip + part) of its own
+    const Seq sq = load_seq(a, at.seq);
+    const int tiles = tiles_of(sq);
+    int skip = 0, part = tiles, parts = 1;
+    int64_t slot = 0;
+    if (!a.by_seq) {
+        if (tiles == 0) {
+            if (++at.seq >= a.n_seqs) return;
+            continue;
+        }
+        skip = from - at.start;
+        part = min(tiles - skip, todo);
+        parts = parts_of(at.start, tiles, at.share).count;
+        slot = part_slot(at.start, at.share, w);
+    }
+   if (r0 < sq.rows) {
     const int rows = min(ROWS, sq.rows - r0);
     // what the first and the last row see bounds what any row sees
     const int pos_first = sq.p0 + r0 / a.group, pos_last = sq.p0 + (r0 + rows - 1) / a.group;
     const int all_end = pos_first + 1, all_begin = a.window > 0 ? max(pos_last, 0) - a.window + 1 : 0;
-    int t0 = sq.lo + it.part * it.chunk;
-    int t1 = min(sq.hi, it.parts == 1 ? sq.hi : t0 + it.chunk);
-    t1 = min(t1, (max(pos_last + 1, 0) + kTok - 1) / kTok);
+    int t0 = sq.lo + skip;
+    const int t1 = min(min(sq.hi, t0 + part), (max(pos_last + 1, 0) + kTok - 1) / kTok);
     if (a.window > 0) t0 = max(t0, max(max(pos_first, 0) - a.window + 1, 0) / kTok);
 
     bf16x8 qf[NT][2 * DQ];
@@ -228,7 +254,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
     }
 
     f32x4 acc[DQ][4][NT];
-    float top[NT], sum[NT];          // running maximum (log2 domain); this lane's share of the sum
+    float top[NT], sum[NT];          // base of the weights (log2 domain); this lane's share of their sum
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         top[t] = -INFINITY;
@@ -241,22 +267,22 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
 
     int32_t my_id = -1;
     float my_ks = 0.f, my_vs = 0.f;
-    const int32_t* table = a.table + int64_t(it.seq) * a.max_blocks;
-    const int in_block = (1 << a.shift) - 1;
+    const int32_t* table = a.table + int64_t(at.seq) * a.max_blocks;
 
-    auto load = [&](Step<DQ>& b, int tile, int l) {
+    u32x4 kc[kStep][DQ], vc[kStep][DQ];      // one step's codes
+    auto load = [&](u32x4 (&to)[kStep][DQ], const uint8_t* codes, int tile, int l) {
 #pragma unroll
         for (int h = 0; h < kStep; ++h) {
             const int32_t id = max(__builtin_amdgcn_readlane(my_id, l + h), 0);
-            const int64_t at = ((((int64_t(id) * a.n_kv + head) << a.shift) + (((tile + h) * kTok) & in_block)) * D);
+            const uint8_t* from = codes + ((((int64_t(id) * a.n_kv + head) << a.shift) + (((tile + h) * kTok) & in_block)) * D);
 #pragma unroll
-            for (int c = 0; c < DQ; ++c) b.k[h][c] = *reinterpret_cast<const u32x4*>(a.k + at + c * 1024 + lane * 16);
-#pragma unroll
-            for (int c = 0; c < DQ; ++c) b.v[h][c] = *reinterpret_cast<const u32x4*>(a.v + at + c * 1024 + lane * 16);
+            for (int c = 0; c < DQ; ++c) to[h][c] = *reinterpret_cast<const u32x4*>(from + c * 1024 + lane * 16);
         }
     };
 
-    auto compute = [&](Step<DQ>& b, int tile, int l) {
+    // The next step's keys are asked for as soon as this one's are used up, and so the values:
+    // each load has the other product and the softmax to arrive in, and needs no second buffer.
+    auto step = [&](int tile, int l, int next_tile, bool more) {
         f32x4 s[kStep][NT];
         bool whole = tile * kTok >= all_begin && (tile + kStep) * kTok <= all_end;
         float ks[kStep], vs[kStep];
@@ -269,16 +295,21 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
             for (int t = 0; t < NT; ++t) s[h][t] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
 #pragma unroll
-        for (int c = 0; c < DQ; ++c)
+        for (int c = 0; c < DQ; ++c) {
+            keep_order();
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int h = 0; h < kStep; ++h) {
-                    const bf16x8 kf = operand<E4M3>(b.k[h][c][2 * e], b.k[h][c][2 * e + 1]);
+                    const bf16x8 kf = operand<E4M3>(kc[h][c][2 * e], kc[h][c][2 * e + 1]);
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
                         s[h][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[t][2 * c + e], s[h][t], 0, 0, 0);
                 }
+        }
+        keep_order();
+        if (more) load(kc, a.k, next_tile, l + kStep);
+        keep_order();
         bf16x8 pf[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -309,12 +340,12 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
             }
             float m = fmaxf(fmaxf(fmaxf(u[0][0], u[0][1]), fmaxf(u[0][2], u[0][3])),
                             fmaxf(fmaxf(u[1][0], u[1][1]), fmaxf(u[1][2], u[1][3])));
-            m = fmaxf(m, __shfl_xor(m, 16));
-            m = fmaxf(m, __shfl_xor(m, 32));
-            m = fmaxf(m, top[t]);
-            const float base = m == -INFINITY ? 0.f : m;
-            if (__ballot(m > top[t])) {
-                const float f = __builtin_amdgcn_exp2f(top[t] - base);
+            m = lane_max(m);
+            // the base of the weights need not be the maximum, only near it: it moves where a
+            // weight would pass 2^8, so most steps leave the sums as they are
+            if (__ballot(m > top[t] + 8.f)) {
+                m = fmaxf(m, top[t]);
+                const float f = __builtin_amdgcn_exp2f(top[t] - (m == -INFINITY ? 0.f : m));
                 sum[t] *= f;
 #pragma unroll
                 for (int c = 0; c < DQ; ++c)
@@ -322,6 +353,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
                     for (int j = 0; j < 4; ++j) acc[c][j][t] *= f;
                 top[t] = m;
             }
+            const float base = top[t] == -INFINITY ? 0.f : top[t];
             float p[kStep][4];
 #pragma unroll
             for (int h = 0; h < kStep; ++h)
@@ -342,17 +374,21 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
                 const bool id_ok = __builtin_amdgcn_readlane(my_id, l + h) >= 0;
                 const uint32_t live = id_ok ? live_bytes((tile + h) * kTok + 4 * g, sq.len) : 0u;
 #pragma unroll
-                for (int c = 0; c < DQ; ++c) b.v[h][c] &= live;
+                for (int c = 0; c < DQ; ++c) vc[h][c] &= live;
             }
         }
 #pragma unroll
-        for (int c = 0; c < DQ; ++c)
+        for (int c = 0; c < DQ; ++c) {
+            keep_order();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bf16x8 vf = operand<E4M3>(b.v[0][c][j], b.v[1][c][j]);
+                const bf16x8 vf = operand<E4M3>(vc[0][c][j], vc[1][c][j]);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) acc[c][j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[t], acc[c][j][t], 0, 0, 0);
             }
+        }
+        keep_order();
+        if (more) load(vc, a.v, next_tile, l + kStep);
     };
 
     const int steps = (max(t1 - t0, 0) + kStep - 1) / kStep;
@@ -372,24 +408,9 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
             }
         }
         const int end = min(mine - k0, kRefill);
-        if constexpr (NT * DQ > 4) {     // no registers for a second step in flight
-            Step<DQ> b;
-            for (int k = 0; k < end; ++k) {
-                load(b, tile_of(k0 + k), kStep * k);
-                compute(b, tile_of(k0 + k), kStep * k);
-            }
-            continue;
-        }
-        Step<DQ> b0, b1;
-        load(b0, tile_of(k0), 0);
-        for (int k = 0; k < end; k += 2) {
-            if (k + 1 < end) load(b1, tile_of(k0 + k + 1), kStep * (k + 1));
-            compute(b0, tile_of(k0 + k), kStep * k);
-            if (k + 1 < end) {
-                if (k + 2 < end) load(b0, tile_of(k0 + k + 2), kStep * (k + 2));
-                compute(b1, tile_of(k0 + k + 1), kStep * (k + 1));
-            }
-        }
+        load(kc, a.k, tile_of(k0), 0);
+        load(vc, a.v, tile_of(k0), 0);
+        for (int k = 0; k < end; ++k) step(tile_of(k0 + k), kStep * k, tile_of(k0 + k + 1), k + 1 < end);
     }
 
     // Join the waves: a common maximum a row, then sums slab by slab through LDS.
@@ -433,7 +454,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
                 l += merge_l[w][r] * __builtin_amdgcn_exp2f(merge_m[w][r] - base);
                 o += *reinterpret_cast<const f32x4*>(&merge[w][r][d]);
             }
-            if (it.parts == 1) {
+            if (parts == 1) {
                 const int j = (r0 + r) / a.group, qh = head * a.group + (r0 + r - j * a.group);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 uint16_t* to = a.out + int64_t(sq.row0 + j) * a.out_stride + int64_t(qh) * D + 64 * c + d;
@@ -441,12 +462,20 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
                 if (c == 0 && d == 0 && a.lse)
                     a.lse[int64_t(sq.row0 + j) * (a.n_kv * a.group) + qh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
             } else {
-                const int64_t at = (int64_t(it.slot + it.part) * gridDim.y + blockIdx.y) * ROWS + r;
-                *reinterpret_cast<f32x4*>(a.part_o + at * D + 64 * c + d) = o;
-                if (c == 0 && d == 0) *reinterpret_cast<f32x2*>(a.part_ml + at * 2) = f32x2{m, l};
+                const int64_t to = (slot * gridDim.y + blockIdx.y) * ROWS + r;
+                *reinterpret_cast<f32x4*>(a.part_o + to * D + 64 * c + d) = o;
+                if (c == 0 && d == 0) *reinterpret_cast<f32x2*>(a.part_ml + to * 2) = f32x2{m, l};
             }
         }
-    }
+    }   }
+    if (a.by_seq) return;
+    todo -= part;
+    from += part;
+    if (todo <= 0) return;
+    at.start += tiles;
+    if (++at.seq >= a.n_seqs) return;
+    __syncthreads();                     // the merge buffers are free again
+  }
 }
 
 // The parts of split requests, one workgroup a row: lanes over channels, waves over parts.
@@ -455,33 +484,37 @@ __global__ __launch_bounds__(64 * kWaves) void join_kernel(AttnArgs a, int rows_
     constexpr int D = 64 * DQ;
     __shared__ float part[kWaves][D];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Item it = find_item(a, blockIdx.x, true);
-    if (it.seq < 0 || it.parts < 2) return;
-    const Seq sq = load_seq(a, it.seq);
+    const Place at = find_place(a, blockIdx.x, true);
+    const Seq sq = load_seq(a, blockIdx.x);
+    const int tiles = tiles_of(sq);
+    if (tiles == 0) return;
+    const Parts parts = parts_of(at.start, tiles, at.share);
+    if (parts.count < 2) return;
     const int head = blockIdx.y % a.n_kv, tile = blockIdx.y / a.n_kv;
     const int r = tile * rows_of_tile + blockIdx.z;
     if (r >= sq.rows) return;
-    const int64_t first = (int64_t(it.slot) * gridDim.y + blockIdx.y) * rows_of_tile + blockIdx.z;
-    const int64_t next = int64_t(gridDim.y) * rows_of_tile;       // rows from one part to the next
+    auto row_of = [&](int p) {
+        return (part_slot(at.start, at.share, parts.first + p) * gridDim.y + blockIdx.y) * rows_of_tile + blockIdx.z;
+    };
     float m = -INFINITY;
-    for (int p = lane; p < it.parts; p += 64) m = fmaxf(m, a.part_ml[(first + p * next) * 2]);
+    for (int p = lane; p < parts.count; p += 64) m = fmaxf(m, a.part_ml[row_of(p) * 2]);
 #pragma unroll
     for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f;
-    for (int p = lane; p < it.parts; p += 64) {
-        const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + (first + p * next) * 2);
+    for (int p = lane; p < parts.count; p += 64) {
+        const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + row_of(p) * 2);
         l += ml[1] * __builtin_amdgcn_exp2f(ml[0] - base);
     }
 #pragma unroll
     for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
     float o[DQ] = {};
 #pragma unroll 4
-    for (int p = wave; p < it.parts; p += kWaves) {
-        const int64_t at = first + p * next;
-        const float f = __builtin_amdgcn_exp2f(a.part_ml[at * 2] - base);
+    for (int p = wave; p < parts.count; p += kWaves) {
+        const int64_t row = row_of(p);
+        const float f = __builtin_amdgcn_exp2f(a.part_ml[row * 2] - base);
 #pragma unroll
-        for (int c = 0; c < DQ; ++c) o[c] += a.part_o[at * D + 64 * c + lane] * f;
+        for (int c = 0; c < DQ; ++c) o[c] += a.part_o[row * D + 64 * c + lane] * f;
     }
 #pragma unroll
     for (int c = 0; c < DQ; ++c) part[wave][64 * c + lane] = o[c];
@@ -504,7 +537,8 @@ __global__ __launch_bounds__(64 * kWaves) void join_kernel(AttnArgs a, int rows_
 
 // How a call is laid out; the same for the workspace's size and the launch.
 struct Plan {
-    int32_t group, nt, row_tiles, target;
+    int32_t group, nt, row_tiles, shares;
+    bool by_seq;
     uint32_t grid_x, grid_y;
     uint64_t parts;          // partial results, of nt * 16 rows for every grid_y
     uint64_t bytes;
@@ -519,19 +553,19 @@ static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs
     if (seq_tiles * n_seqs >= (int64_t(1) << 31)) return fail(MBD_ESHAPE, "n_seqs * max_blocks * block_size / 16 is 2^31 or more");
     p->group = n_heads / c->n_heads;
     if (max_new < 1 || int64_t(max_new) * p->group >= (int64_t(1) << 24)) return fail(MBD_ESHAPE, "max_new * query heads a KV head outside [1, 2^24)");
-    const int32_t rows = max_new * p->group, widest = c->head_dim > 128 ? 2 : 4;
-    p->nt = rows <= 16 ? 1 : rows <= 32 ? 2 : widest;
+    const int32_t rows = max_new * p->group;
+    p->nt = rows <= 16 ? 1 : 2;
     p->row_tiles = (rows + 16 * p->nt - 1) / (16 * p->nt);
     const int64_t y = int64_t(c->n_heads) * p->row_tiles;
     if (y > 65535) return fail(MBD_ESHAPE, "KV heads times query row tiles above 65535");
     p->grid_y = uint32_t(y);
-    p->target = int32_t(std::max<int64_t>(1, kTargetBlocks / y));
-    const int64_t most = (seq_tiles + kMinChunk - 1) / kMinChunk;      // parts of one request
-    if (most < 2) p->target = 1;
-    const bool split = p->target > 1;
-    p->grid_x = uint32_t(split ? std::min<int64_t>(p->target + n_seqs, n_seqs * most) : n_seqs);
-    // a request is split if it is longer than a chunk, so into fewer than twice its chunks
-    p->parts = split ? std::min<int64_t>(2 * p->target, p->grid_x) : 0;
+    const int64_t room = kCus * per_cu(c->head_dim / 64, p->nt);
+    // a share holds kMinShare tiles at least, and no more than all requests' tiles are there
+    p->shares = int32_t(std::max<int64_t>(1, std::min<int64_t>(room / y, (seq_tiles * n_seqs + kMinShare - 1) / kMinShare)));
+    p->by_seq = seq_tiles <= kMinShare || p->shares < 2 || (p->row_tiles > 1 && y * n_seqs >= room);
+    if (p->by_seq) p->shares = 1;
+    p->grid_x = uint32_t(p->by_seq ? n_seqs : p->shares);
+    p->parts = p->by_seq ? 0 : 2 * uint64_t(p->shares);
     p->bytes = p->parts * p->grid_y * (16u * p->nt) * (c->head_dim + 2) * sizeof(float);
     return MBD_OK;
 }
@@ -548,8 +582,7 @@ static void launch(const AttnArgs& a, const Plan& p, bool ext, hipStream_t s) {
 template <bool E4M3, int DQ>
 static void launch_rows(const AttnArgs& a, const Plan& p, bool ext, hipStream_t s) {
     if (p.nt == 1) return launch<E4M3, DQ, 1>(a, p, ext, s);
-    if (p.nt == 2) return launch<E4M3, DQ, 2>(a, p, ext, s);
-    if constexpr (DQ <= 2) launch<E4M3, DQ, 4>(a, p, ext, s);
+    launch<E4M3, DQ, 2>(a, p, ext, s);
 }
 
 template <bool E4M3>
@@ -630,7 +663,8 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     a.shift = kv::log2_of(cache->block_size);
     a.n_kv = cache->n_heads;
     a.group = p.group;
-    a.target = p.target;
+    a.shares = p.shares;
+    a.by_seq = p.by_seq;
     a.scale = args->scale;
     a.softcap = args->softcap;
     const bool ext = a.window > 0 || args->softcap > 0 || args->slopes;

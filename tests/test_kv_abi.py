@@ -134,7 +134,7 @@ def test_binding_checks():
         mbd.KvCache(mbd.MBD_KV_INT8, 32, 128, codes, codes, scale, scale)
     with pytest.raises(ValueError, match="contiguous"):
         mbd.KvCache(mbd.MBD_KV_INT8, 16, 128, codes, codes, scale, scale.double())
-    with pytest.raises(ValueError, match="int32"):
-        mbd.KvPool(16, torch.zeros((2, 4), dtype=torch.int64), torch.zeros(9, dtype=torch.int32))
+    with pytest.raises(ValueError, match="current GPU"):
+        mbd.KvPool(16, torch.zeros((2, 4), dtype=torch.int32), torch.zeros(9, dtype=torch.int32))
     with pytest.raises(ValueError, match="n_seqs"):
         mbd.KvPool(16, torch.zeros(4, dtype=torch.int32), torch.zeros(9, dtype=torch.int32))
