@@ -256,6 +256,7 @@ class KvCache:
                                 (k_scale, k_codes.shape[:2], torch.float32), (v_scale, k_codes.shape[:2], torch.float32)):
             if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
                 raise ValueError("codes are contiguous uint8 tensors of one shape, scales contiguous fp32 [n_blocks][n_heads]")
+        for t in (k_codes, v_codes, k_scale, v_scale):
             if t.get_device() != _here():
                 _refuse(_here(), "the cache", t, "")
         self.tensors = dict(k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale)

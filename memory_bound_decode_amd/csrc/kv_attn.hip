@@ -24,7 +24,9 @@ constexpr int kWaves = 4;              // waves of a workgroup; each takes every
 constexpr int kStep = 2;               // tiles of one step: 32 tokens, the k of an MFMA
 constexpr int kRefill = 64 / kStep;    // steps whose block ids and scales one lane each holds
 constexpr int kMaxSeqs = 4096;
-constexpr int kMinShare = kWaves * kStep;   // tiles: a workgroup's least share
+constexpr int kMinPart = kWaves * kStep;    // tiles: the least part of a request, a step a wave
+constexpr int kShortPart = 4 * kMinPart;
+constexpr int kRounds = 4;                  // workgroups aimed at for each place on the chip
 constexpr int kCus = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -39,7 +41,7 @@ struct AttnArgs {
     float *lse, *part_o, *part_ml;
     const float* slopes;
     int64_t q_stride, out_stride;
-    int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, shares;
+    int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, places, most;
     bool by_seq;
     float scale, softcap;
 };
@@ -85,62 +87,58 @@ __device__ __forceinline__ int wave_before(int v) {
     return inc - v;
 }
 
-// The lengths are known on the device alone, so every wave cuts the work up itself: the
-// requests' tiles stand in one row, and each workgroup of a head takes an equal share of
-// it, whatever requests that meets, so all end together.  A request that falls into
-// several shares is joined from their partial results.  What a workgroup has to know
-// is one prefix sum of the requests' tiles: a scan of 64 lanes.  Where the requests alone
-// fill the chip (by_seq), each has a workgroup of its own and nothing is joined.
+// The lengths are known on the device alone, so every wave cuts the work up itself: all
+// tiles over the workgroups that the call aims at is a chunk, a request is cut into
+// ceil(tiles / chunk) even parts, and a workgroup's part follows from the prefix sums of
+// their counts: two scans of 64 lanes.
 __device__ __forceinline__ int tiles_of(const Seq& s) { return s.n_new < 1 ? 0 : max(s.hi - s.lo, 1); }
 
-struct Place {
-    int32_t seq, start, share;   // a request, its first tile in the row of all, tiles of a share
+// A work group's part of a request, or (by_seq) all of a request's.
+struct Item {
+    int32_t seq, part, parts, slot;      // slot: of the request's first partial result
 };
 
-// The request that holds tile blockIdx-share's first tile (by_seq false), or request `want`.
-__device__ __forceinline__ Place find_place(const AttnArgs& a, int32_t want, bool is_seq) {
+__device__ __forceinline__ int32_t even_part(int tiles, int parts) {     // tiles of a part, whole steps
+    return ((tiles - 1) / parts + kStep) / kStep * kStep;
+}
+
+__device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, bool is_seq) {
     const int lane = threadIdx.x & 63;
     const int per = (a.n_seqs + 63) / 64;
     const int i0 = min(lane * per, a.n_seqs), i1 = min(i0 + per, a.n_seqs);
-    int mine = 0;
-    for (int i = i0; i < i1; ++i) mine += tiles_of(load_seq(a, i));
-    const int before = wave_before(mine);
-    const int total = __builtin_amdgcn_readlane(before + mine, 63);
-    Place p;
-    p.share = max(kMinShare, ((max(total, 1) - 1) / a.shares + kStep) / kStep * kStep);
-    const int64_t target = is_seq ? 0 : int64_t(want) * p.share;
-    int seq = -1, start = before, at = before;
+    int tiles = 0, used = 0;
     for (int i = i0; i < i1; ++i) {
         const int n = tiles_of(load_seq(a, i));
-        if (is_seq ? i == want : target >= at && target < at + n) {
-            seq = i;
-            start = at;
-        }
-        at += n;
+        tiles += n;
+        used += n > 0;
     }
-    const uint64_t who = __ballot(seq >= 0);
-    p.seq = -1;
-    p.start = 0;
-    if (who) {
-        const int l = __builtin_ctzll(who);
-        p.seq = __builtin_amdgcn_readlane(seq, l);
-        p.start = __builtin_amdgcn_readlane(start, l);
+    tiles = wave_sum(tiles);
+    used = wave_sum(used);
+    // ceil(tiles_i / chunk) add up to at most tiles / chunk + used.  One round of the places
+    // that the chip has, if that leaves short parts (their time is the way to the first
+    // product, not the bytes); else the longer row of workgroups, which ends evenly.
+    int chunk = (max(tiles, 1) - 1) / max(a.places - used, 1) + 1;
+    if (chunk > kShortPart) chunk = (max(tiles, 1) - 1) / max(a.most - used, 1) + 1;
+    chunk = max(chunk, kMinPart);
+    int items = 0, split = 0;
+    for (int i = i0; i < i1; ++i) {
+        const int n = tiles_of(load_seq(a, i)), p = (n + chunk - 1) / chunk;
+        items += p;
+        split += p > 1 ? p : 0;
     }
-    return p;
+    int item0 = wave_before(items), slot0 = wave_before(split);
+    Item it{-1, 0, 0, 0};
+    for (int i = i0; i < i1; ++i) {
+        const int n = tiles_of(load_seq(a, i)), p = (n + chunk - 1) / chunk;
+        if (is_seq ? i == want : want >= item0 && want < item0 + p) it = {i, want - item0, p, slot0};
+        item0 += p;
+        slot0 += p > 1 ? p : 0;
+    }
+    const uint64_t who = __ballot(it.seq >= 0);
+    const int l = who ? __builtin_ctzll(who) : 0;
+    return {__builtin_amdgcn_readlane(it.seq, l), __builtin_amdgcn_readlane(it.part, l), __builtin_amdgcn_readlane(it.parts, l),
+            __builtin_amdgcn_readlane(it.slot, l)};
 }
-
-// Shares that a request falls into, and where each leaves its partial result: a share
-// has at most two requests that it does not hold whole, its first and its last.
-struct Parts {
-    int32_t first, count;
-};
-
-__device__ __forceinline__ Parts parts_of(int start, int tiles, int share) {
-    const int f = start / share;
-    return {f, (start + tiles - 1) / share - f + 1};
-}
-
-__device__ __forceinline__ int64_t part_slot(int start, int share, int w) { return 2 * int64_t(w) + (start >= int64_t(w) * share ? 1 : 0); }
 
 __device__ __forceinline__ float lane_max(float v) {     // over the four lanes of a query row
     v = fmaxf(v, __shfl_xor(v, 16));
@@ -202,35 +200,22 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, n = lane & 15;
     const int head = blockIdx.y % a.n_kv, r0 = blockIdx.y / a.n_kv * ROWS;
-    const int w = blockIdx.x, in_block = (1 << a.shift) - 1;
-    Place at = {w, 0, 0};
-    if (!a.by_seq) {
-        at = find_place(a, w, false);
-        if (at.seq < 0) return;
-    }
-  for (int todo = at.share, from = w * at.share; ;) {
-    // the request's part in this share: tiles [skip, skip + part) of its own
-    const Seq sq = load_seq(a, at.seq);
-    const int tiles = tiles_of(sq);
-    int skip = 0, part = tiles, parts = 1;
-    int64_t slot = 0;
-    if (!a.by_seq) {
-        if (tiles == 0) {
-            if (++at.seq >= a.n_seqs) return;
-            continue;
-        }
-        skip = from - at.start;
-        part = min(tiles - skip, todo);
-        parts = parts_of(at.start, tiles, at.share).count;
-        slot = part_slot(at.start, at.share, w);
-    }
-   if (r0 < sq.rows) {
+    const int in_block = (1 << a.shift) - 1;
+    Item it{int32_t(blockIdx.x), 0, 1, 0};
+    if (!a.by_seq) it = find_item(a, blockIdx.x, false);
+    if (it.seq < 0) return;
+    const Seq sq = load_seq(a, it.seq);
+    if (r0 >= sq.rows) return;
     const int rows = min(ROWS, sq.rows - r0);
     // what the first and the last row see bounds what any row sees
     const int pos_first = sq.p0 + r0 / a.group, pos_last = sq.p0 + (r0 + rows - 1) / a.group;
     const int all_end = pos_first + 1, all_begin = a.window > 0 ? max(pos_last, 0) - a.window + 1 : 0;
-    int t0 = sq.lo + skip;
-    const int t1 = min(min(sq.hi, t0 + part), (max(pos_last + 1, 0) + kTok - 1) / kTok);
+    int t0 = sq.lo, t1 = min(sq.hi, (max(pos_last + 1, 0) + kTok - 1) / kTok);
+    if (it.parts > 1) {
+        const int part = even_part(tiles_of(sq), it.parts);
+        t0 += it.part * part;
+        t1 = min(t1, t0 + part);
+    }
     if (a.window > 0) t0 = max(t0, max(max(pos_first, 0) - a.window + 1, 0) / kTok);
 
     bf16x8 qf[NT][2 * DQ];
@@ -267,7 +252,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
 
     int32_t my_id = -1;
     float my_ks = 0.f, my_vs = 0.f;
-    const int32_t* table = a.table + int64_t(at.seq) * a.max_blocks;
+    const int32_t* table = a.table + int64_t(it.seq) * a.max_blocks;
 
     u32x4 kc[kStep][DQ], vc[kStep][DQ];      // one step's codes
     auto load = [&](u32x4 (&to)[kStep][DQ], const uint8_t* codes, int tile, int l) {
@@ -454,7 +439,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
                 l += merge_l[w][r] * __builtin_amdgcn_exp2f(merge_m[w][r] - base);
                 o += *reinterpret_cast<const f32x4*>(&merge[w][r][d]);
             }
-            if (parts == 1) {
+            if (it.parts == 1) {
                 const int j = (r0 + r) / a.group, qh = head * a.group + (r0 + r - j * a.group);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 uint16_t* to = a.out + int64_t(sq.row0 + j) * a.out_stride + int64_t(qh) * D + 64 * c + d;
@@ -462,21 +447,12 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
                 if (c == 0 && d == 0 && a.lse)
                     a.lse[int64_t(sq.row0 + j) * (a.n_kv * a.group) + qh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
             } else {
-                const int64_t to = (slot * gridDim.y + blockIdx.y) * ROWS + r;
+                const int64_t to = (int64_t(it.slot + it.part) * gridDim.y + blockIdx.y) * ROWS + r;
                 *reinterpret_cast<f32x4*>(a.part_o + to * D + 64 * c + d) = o;
                 if (c == 0 && d == 0) *reinterpret_cast<f32x2*>(a.part_ml + to * 2) = f32x2{m, l};
             }
         }
-    }   }
-    if (a.by_seq) return;
-    todo -= part;
-    from += part;
-    if (todo <= 0) return;
-    at.start += tiles;
-    if (++at.seq >= a.n_seqs) return;
-    __syncthreads();                     // the merge buffers are free again
-  }
-}
+    }}
 
 // The parts of split requests, one workgroup a row: lanes over channels, waves over parts.
 template <int DQ>
@@ -484,25 +460,20 @@ __global__ __launch_bounds__(64 * kWaves) void join_kernel(AttnArgs a, int rows_
     constexpr int D = 64 * DQ;
     __shared__ float part[kWaves][D];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Place at = find_place(a, blockIdx.x, true);
-    const Seq sq = load_seq(a, blockIdx.x);
-    const int tiles = tiles_of(sq);
-    if (tiles == 0) return;
-    const Parts parts = parts_of(at.start, tiles, at.share);
-    if (parts.count < 2) return;
+    const Item it = find_item(a, blockIdx.x, true);
+    if (it.parts < 2) return;
+    const Seq sq = load_seq(a, it.seq);
     const int head = blockIdx.y % a.n_kv, tile = blockIdx.y / a.n_kv;
     const int r = tile * rows_of_tile + blockIdx.z;
     if (r >= sq.rows) return;
-    auto row_of = [&](int p) {
-        return (part_slot(at.start, at.share, parts.first + p) * gridDim.y + blockIdx.y) * rows_of_tile + blockIdx.z;
-    };
+    auto row_of = [&](int p) { return (int64_t(it.slot + p) * gridDim.y + blockIdx.y) * rows_of_tile + blockIdx.z; };
     float m = -INFINITY;
-    for (int p = lane; p < parts.count; p += 64) m = fmaxf(m, a.part_ml[row_of(p) * 2]);
+    for (int p = lane; p < it.parts; p += 64) m = fmaxf(m, a.part_ml[row_of(p) * 2]);
 #pragma unroll
     for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f;
-    for (int p = lane; p < parts.count; p += 64) {
+    for (int p = lane; p < it.parts; p += 64) {
         const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + row_of(p) * 2);
         l += ml[1] * __builtin_amdgcn_exp2f(ml[0] - base);
     }
@@ -510,7 +481,7 @@ __global__ __launch_bounds__(64 * kWaves) void join_kernel(AttnArgs a, int rows_
     for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
     float o[DQ] = {};
 #pragma unroll 4
-    for (int p = wave; p < parts.count; p += kWaves) {
+    for (int p = wave; p < it.parts; p += kWaves) {
         const int64_t row = row_of(p);
         const float f = __builtin_amdgcn_exp2f(a.part_ml[row * 2] - base);
 #pragma unroll
@@ -537,7 +508,7 @@ __global__ __launch_bounds__(64 * kWaves) void join_kernel(AttnArgs a, int rows_
 
 // How a call is laid out; the same for the workspace's size and the launch.
 struct Plan {
-    int32_t group, nt, row_tiles, shares;
+    int32_t group, nt, row_tiles, places, most;
     bool by_seq;
     uint32_t grid_x, grid_y;
     uint64_t parts;          // partial results, of nt * 16 rows for every grid_y
@@ -560,12 +531,13 @@ static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs
     if (y > 65535) return fail(MBD_ESHAPE, "KV heads times query row tiles above 65535");
     p->grid_y = uint32_t(y);
     const int64_t room = kCus * per_cu(c->head_dim / 64, p->nt);
-    // a share holds kMinShare tiles at least, and no more than all requests' tiles are there
-    p->shares = int32_t(std::max<int64_t>(1, std::min<int64_t>(room / y, (seq_tiles * n_seqs + kMinShare - 1) / kMinShare)));
-    p->by_seq = seq_tiles <= kMinShare || p->shares < 2 || (p->row_tiles > 1 && y * n_seqs >= room);
-    if (p->by_seq) p->shares = 1;
-    p->grid_x = uint32_t(p->by_seq ? n_seqs : p->shares);
-    p->parts = p->by_seq ? 0 : 2 * uint64_t(p->shares);
+    const int64_t longest = (seq_tiles + kMinPart - 1) / kMinPart;         // parts of one request at most
+    p->places = int32_t(std::max<int64_t>(1, room / y));
+    p->most = int32_t(std::max<int64_t>(1, kRounds * room / y));
+    p->by_seq = longest < 2 || p->most < 2 || (p->row_tiles > 1 && y * n_seqs >= room);
+    p->grid_x = uint32_t(p->by_seq ? n_seqs : std::min<int64_t>(p->most + n_seqs, n_seqs * longest));
+    // a request is split if it is longer than a chunk, so into fewer than twice its chunks
+    p->parts = p->by_seq ? 0 : std::min<int64_t>(2 * p->most, p->grid_x);
     p->bytes = p->parts * p->grid_y * (16u * p->nt) * (c->head_dim + 2) * sizeof(float);
     return MBD_OK;
 }
@@ -663,7 +635,8 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     a.shift = kv::log2_of(cache->block_size);
     a.n_kv = cache->n_heads;
     a.group = p.group;
-    a.shares = p.shares;
+    a.places = p.places;
+    a.most = p.most;
     a.by_seq = p.by_seq;
     a.scale = args->scale;
     a.softcap = args->softcap;
