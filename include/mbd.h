@@ -426,7 +426,8 @@ mbd_status mbd_kv_gather(const mbd_kv_cache* cache, const int32_t* slots, int32_
  * NULL: no distance bias. */
 typedef struct {
     int32_t n_heads;      /* query heads, a multiple of the cache's; query head h reads
-                             KV head h / (n_heads / cache n_heads)                      */
+                             KV head h / (n_heads / cache n_heads); at most 256 of them
+                             a KV head                                                  */
     int32_t n_seqs;       /* 1..4096                                                    */
     int32_t max_blocks;   /* columns of the block table                                 */
     int32_t T;            /* rows of q, out and lse                                     */

@@ -41,10 +41,14 @@ struct AttnArgs {
     float *lse, *part_o, *part_ml;
     const float* slopes;
     int64_t q_stride, out_stride;
+    uint32_t per_group;                  // ceil(2^32 / group)
     int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, places, most;
     bool by_seq;
     float scale, softcap;
 };
+
+// Token of a query row: r / group, exact for r * group below 2^32.
+__device__ __forceinline__ int token_of(const AttnArgs& a, int r) { return a.group == 1 ? r : int(__umulhi(uint32_t(r), a.per_group)); }
 
 // ---------------------------------------------------------------- shares of the work
 
@@ -70,21 +74,17 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int i) {
     return s;
 }
 
-__device__ __forceinline__ int wave_sum(int v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    return v;
-}
+// Inclusive sum over the wave's lanes, by row shifts and row broadcasts (no LDS trips).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int plus_dpp(int v) { return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false); }
 
-__device__ __forceinline__ int wave_before(int v) {
-    const int lane = threadIdx.x & 63;
-    int inc = v;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int up = __shfl_up(inc, d);
-        if (lane >= d) inc += up;
-    }
-    return inc - v;
+__device__ __forceinline__ int wave_scan(int v) {
+    v = plus_dpp<0x111, 0xf>(v);       // row_shr 1, 2, 4, 8
+    v = plus_dpp<0x112, 0xf>(v);
+    v = plus_dpp<0x114, 0xf>(v);
+    v = plus_dpp<0x118, 0xf>(v);
+    v = plus_dpp<0x142, 0xa>(v);       // row_bcast 15 into rows 1 and 3
+    return plus_dpp<0x143, 0xc>(v);    // row_bcast 31 into rows 2 and 3
 }
 
 // The lengths are known on the device alone, so every wave cuts the work up itself: all
@@ -93,7 +93,7 @@ __device__ __forceinline__ int wave_before(int v) {
 // their counts: two scans of 64 lanes.
 __device__ __forceinline__ int tiles_of(const Seq& s) { return s.n_new < 1 ? 0 : max(s.hi - s.lo, 1); }
 
-// A work group's part of a request, or (by_seq) all of a request's.
+// A workgroup's part of a request, or (by_seq) all of one.
 struct Item {
     int32_t seq, part, parts, slot;      // slot: of the request's first partial result
 };
@@ -102,47 +102,66 @@ __device__ __forceinline__ int32_t even_part(int tiles, int parts) {     // tile
     return ((tiles - 1) / parts + kStep) / kStep * kStep;
 }
 
-__device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, bool is_seq) {
+// The item `want`, or request `want` as a whole (is_seq); seq is -1 if there is none.
+__device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, bool is_seq, Seq* sq) {
     const int lane = threadIdx.x & 63;
     const int per = (a.n_seqs + 63) / 64;
-    const int i0 = min(lane * per, a.n_seqs), i1 = min(i0 + per, a.n_seqs);
-    int tiles = 0, used = 0;
-    for (int i = i0; i < i1; ++i) {
+    const int i0 = lane * per, i1 = min(i0 + per, a.n_seqs);
+    const Seq mine = load_seq(a, min(i0, a.n_seqs - 1));        // up to 64 requests: one a lane, read once
+    const int n0 = i0 < a.n_seqs ? tiles_of(mine) : 0;
+    int tiles = n0, used = n0 > 0;
+    for (int i = i0 + 1; i < i1; ++i) {
         const int n = tiles_of(load_seq(a, i));
         tiles += n;
         used += n > 0;
     }
-    tiles = wave_sum(tiles);
-    used = wave_sum(used);
+    tiles = max(__builtin_amdgcn_readlane(wave_scan(tiles), 63), 1);
+    used = __builtin_amdgcn_readlane(wave_scan(used), 63);
     // ceil(tiles_i / chunk) add up to at most tiles / chunk + used.  One round of the places
     // that the chip has, if that leaves short parts (their time is the way to the first
     // product, not the bytes); else the longer row of workgroups, which ends evenly.
-    int chunk = (max(tiles, 1) - 1) / max(a.places - used, 1) + 1;
-    if (chunk > kShortPart) chunk = (max(tiles, 1) - 1) / max(a.most - used, 1) + 1;
-    chunk = max(chunk, kMinPart);
-    int items = 0, split = 0;
-    for (int i = i0; i < i1; ++i) {
-        const int n = tiles_of(load_seq(a, i)), p = (n + chunk - 1) / chunk;
+    uint32_t chunk = uint32_t(tiles - 1) / uint32_t(max(a.places - used, 1)) + 1;
+    if (chunk > kShortPart) chunk = uint32_t(tiles - 1) / uint32_t(max(a.most - used, 1)) + 1;
+    chunk = max(chunk, uint32_t(kMinPart));
+    auto parts_of = [&](int n) { return int((uint32_t(n) + chunk - 1) / chunk); };
+    const int p0 = parts_of(n0);
+    int items = p0, split = p0 > 1 ? p0 : 0;
+    for (int i = i0 + 1; i < i1; ++i) {
+        const int p = parts_of(tiles_of(load_seq(a, i)));
         items += p;
         split += p > 1 ? p : 0;
     }
-    int item0 = wave_before(items), slot0 = wave_before(split);
+    int item0 = wave_scan(items) - items, slot0 = wave_scan(split) - split;
     Item it{-1, 0, 0, 0};
-    for (int i = i0; i < i1; ++i) {
-        const int n = tiles_of(load_seq(a, i)), p = (n + chunk - 1) / chunk;
-        if (is_seq ? i == want : want >= item0 && want < item0 + p) it = {i, want - item0, p, slot0};
+    Seq s = mine;
+    auto look = [&](int i, int p, const Seq& is) {
+        if (is_seq ? i == want : want >= item0 && want < item0 + p) {
+            it = {i, want - item0, p, slot0};
+            s = is;
+        }
         item0 += p;
         slot0 += p > 1 ? p : 0;
+    };
+    if (i0 < a.n_seqs) look(i0, p0, mine);
+    for (int i = i0 + 1; i < i1; ++i) {
+        const Seq is = load_seq(a, i);
+        look(i, parts_of(tiles_of(is)), is);
     }
     const uint64_t who = __ballot(it.seq >= 0);
     const int l = who ? __builtin_ctzll(who) : 0;
-    return {__builtin_amdgcn_readlane(it.seq, l), __builtin_amdgcn_readlane(it.part, l), __builtin_amdgcn_readlane(it.parts, l),
-            __builtin_amdgcn_readlane(it.slot, l)};
+    auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+    *sq = {of(s.row0), of(s.n_new), of(s.rows), of(s.p0), of(s.lo), of(s.hi), of(s.len)};
+    return {who ? of(it.seq) : -1, of(it.part), of(it.parts), of(it.slot)};
 }
 
-__device__ __forceinline__ float lane_max(float v) {     // over the four lanes of a query row
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
+// Maximum over the four lanes of a query row (lane % 16): the rows of 16 lanes swap places.
+__device__ __forceinline__ float lane_max(float v) {
+    const uint32_t x = __float_as_uint(v);
+    const auto h = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    const float m = fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1]));
+    const uint32_t y = __float_as_uint(m);
+    const auto r = __builtin_amdgcn_permlane16_swap(y, y, false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 // ---------------------------------------------------------------- operands
@@ -189,7 +208,7 @@ __device__ __forceinline__ float lane_float(float v, int l) {
 
 // Workgroups a CU (waves a SIMD) that a variant's registers are held to: enough loads in
 // flight for the memory, and as many shares as there are places for them.
-constexpr int per_cu(int dq, int nt) { return dq * nt == 1 ? 4 : dq * nt == 2 ? 3 : dq * nt <= 4 ? 2 : 1; }
+constexpr int per_cu(int dq, int nt) { return nt == 1 ? (dq <= 2 ? 4 : dq == 3 ? 3 : 2) : (dq == 1 ? 3 : dq == 2 ? 2 : 1); }
 
 // DQ = head_dim / 64, NT = tiles of 16 query rows, EXT: cap, window or distance bias.
 template <bool E4M3, int DQ, int NT, bool EXT>
@@ -202,13 +221,14 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
     const int head = blockIdx.y % a.n_kv, r0 = blockIdx.y / a.n_kv * ROWS;
     const int in_block = (1 << a.shift) - 1;
     Item it{int32_t(blockIdx.x), 0, 1, 0};
-    if (!a.by_seq) it = find_item(a, blockIdx.x, false);
+    Seq sq;
+    if (a.by_seq) sq = load_seq(a, it.seq);
+    else it = find_item(a, blockIdx.x, false, &sq);
     if (it.seq < 0) return;
-    const Seq sq = load_seq(a, it.seq);
     if (r0 >= sq.rows) return;
     const int rows = min(ROWS, sq.rows - r0);
     // what the first and the last row see bounds what any row sees
-    const int pos_first = sq.p0 + r0 / a.group, pos_last = sq.p0 + (r0 + rows - 1) / a.group;
+    const int pos_first = sq.p0 + token_of(a, r0), pos_last = sq.p0 + token_of(a, r0 + rows - 1);
     const int all_end = pos_first + 1, all_begin = a.window > 0 ? max(pos_last, 0) - a.window + 1 : 0;
     int t0 = sq.lo, t1 = min(sq.hi, (max(pos_last + 1, 0) + kTok - 1) / kTok);
     if (it.parts > 1) {
@@ -218,6 +238,17 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
     }
     if (a.window > 0) t0 = max(t0, max(max(pos_first, 0) - a.window + 1, 0) / kTok);
 
+    const int steps = (max(t1 - t0, 0) + kStep - 1) / kStep;
+    const int mine = steps > wave ? (steps - wave + kWaves - 1) / kWaves : 0;
+    auto tile_of = [&](int k) { return t0 + kStep * (wave + kWaves * k); };
+    // lane l looks up tile l % 2 of step k0 + l / 2; the first look is on its way before the queries
+    const int32_t* table = a.table + int64_t(it.seq) * a.max_blocks;
+    auto look_up = [&](int k0) {
+        const int tile = tile_of(k0 + lane / kStep) + lane % kStep;
+        return tile < t1 ? table[(tile * kTok) >> a.shift] : -1;
+    };
+    int32_t next_id = look_up(0);
+
     bf16x8 qf[NT][2 * DQ];
     int pos[NT];
     float slope[NT];
@@ -225,7 +256,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
     for (int t = 0; t < NT; ++t) {
         const int r = r0 + 16 * t + n;
         const bool in = r < sq.rows;
-        const int j = r / a.group, qh = head * a.group + (r - j * a.group);
+        const int j = token_of(a, r), qh = head * a.group + (r - j * a.group);
         pos[t] = in ? sq.p0 + j : -1;
         slope[t] = 0.f;
         if (EXT && a.slopes && in) slope[t] = a.slopes[qh] * kLog2e;
@@ -252,7 +283,6 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
 
     int32_t my_id = -1;
     float my_ks = 0.f, my_vs = 0.f;
-    const int32_t* table = a.table + int64_t(it.seq) * a.max_blocks;
 
     u32x4 kc[kStep][DQ], vc[kStep][DQ];      // one step's codes
     auto load = [&](u32x4 (&to)[kStep][DQ], const uint8_t* codes, int tile, int l) {
@@ -261,7 +291,12 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
             const int32_t id = max(__builtin_amdgcn_readlane(my_id, l + h), 0);
             const uint8_t* from = codes + ((((int64_t(id) * a.n_kv + head) << a.shift) + (((tile + h) * kTok) & in_block)) * D);
 #pragma unroll
-            for (int c = 0; c < DQ; ++c) to[h][c] = *reinterpret_cast<const u32x4*>(from + c * 1024 + lane * 16);
+            for (int c = 0; c < DQ; ++c) {
+                const u32x4* p = reinterpret_cast<const u32x4*>(from + c * 1024 + lane * 16);
+                // one tile of query rows is all there is: the codes are read once (with several,
+                // the other tiles find them in L2)
+                to[h][c] = NT == 1 ? __builtin_nontemporal_load(p) : *p;
+            }
         }
     };
 
@@ -376,25 +411,17 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
         if (more) load(vc, a.v, next_tile, l + kStep);
     };
 
-    const int steps = (max(t1 - t0, 0) + kStep - 1) / kStep;
-    const int mine = steps > wave ? (steps - wave + kWaves - 1) / kWaves : 0;
-    auto tile_of = [&](int k) { return t0 + kStep * (wave + kWaves * k); };
     for (int k0 = 0; k0 < mine; k0 += kRefill) {
-        // lane l: tile l % 2 of step k0 + l / 2
-        const int tile = tile_of(k0 + lane / kStep) + lane % kStep;
-        my_id = -1;
+        my_id = next_id >= 0 && next_id < a.n_blocks ? next_id : -1;
         my_ks = my_vs = 0.f;
-        if (tile < t1) {
-            const int32_t id = table[(tile * kTok) >> a.shift];
-            if (id >= 0 && id < a.n_blocks) {
-                my_id = id;
-                my_ks = a.k_scale[int64_t(id) * a.n_kv + head];
-                my_vs = a.v_scale[int64_t(id) * a.n_kv + head];
-            }
+        if (my_id >= 0) {
+            my_ks = a.k_scale[int64_t(my_id) * a.n_kv + head];
+            my_vs = a.v_scale[int64_t(my_id) * a.n_kv + head];
         }
         const int end = min(mine - k0, kRefill);
         load(kc, a.k, tile_of(k0), 0);
         load(vc, a.v, tile_of(k0), 0);
+        next_id = look_up(k0 + kRefill);
         for (int k = 0; k < end; ++k) step(tile_of(k0 + k), kStep * k, tile_of(k0 + k + 1), k + 1 < end);
     }
 
@@ -440,7 +467,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
                 o += *reinterpret_cast<const f32x4*>(&merge[w][r][d]);
             }
             if (it.parts == 1) {
-                const int j = (r0 + r) / a.group, qh = head * a.group + (r0 + r - j * a.group);
+                const int j = token_of(a, r0 + r), qh = head * a.group + (r0 + r - j * a.group);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 uint16_t* to = a.out + int64_t(sq.row0 + j) * a.out_stride + int64_t(qh) * D + 64 * c + d;
                 *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
@@ -460,9 +487,9 @@ __global__ __launch_bounds__(64 * kWaves) void join_kernel(AttnArgs a, int rows_
     constexpr int D = 64 * DQ;
     __shared__ float part[kWaves][D];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Item it = find_item(a, blockIdx.x, true);
+    Seq sq;
+    const Item it = find_item(a, blockIdx.x, true, &sq);
     if (it.parts < 2) return;
-    const Seq sq = load_seq(a, it.seq);
     const int head = blockIdx.y % a.n_kv, tile = blockIdx.y / a.n_kv;
     const int r = tile * rows_of_tile + blockIdx.z;
     if (r >= sq.rows) return;
@@ -490,7 +517,7 @@ __global__ __launch_bounds__(64 * kWaves) void join_kernel(AttnArgs a, int rows_
 #pragma unroll
     for (int c = 0; c < DQ; ++c) part[wave][64 * c + lane] = o[c];
     __syncthreads();
-    const int j = r / a.group, qh = head * a.group + (r - j * a.group);
+    const int j = token_of(a, r), qh = head * a.group + (r - j * a.group);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint16_t* to = a.out + int64_t(sq.row0 + j) * a.out_stride + int64_t(qh) * D;
     for (int d = threadIdx.x * 2; d < D; d += 128 * kWaves) {
@@ -523,6 +550,7 @@ static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs
     const int64_t seq_tiles = int64_t(max_blocks) * (c->block_size / kTok);
     if (seq_tiles * n_seqs >= (int64_t(1) << 31)) return fail(MBD_ESHAPE, "n_seqs * max_blocks * block_size / 16 is 2^31 or more");
     p->group = n_heads / c->n_heads;
+    if (p->group > 256) return fail(MBD_ESHAPE, "%d query heads a KV head, more than 256", p->group);
     if (max_new < 1 || int64_t(max_new) * p->group >= (int64_t(1) << 24)) return fail(MBD_ESHAPE, "max_new * query heads a KV head outside [1, 2^24)");
     const int32_t rows = max_new * p->group;
     p->nt = rows <= 16 ? 1 : 2;
@@ -635,6 +663,7 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     a.shift = kv::log2_of(cache->block_size);
     a.n_kv = cache->n_heads;
     a.group = p.group;
+    a.per_group = uint32_t(((uint64_t(1) << 32) + p.group - 1) / p.group);
     a.places = p.places;
     a.most = p.most;
     a.by_seq = p.by_seq;
