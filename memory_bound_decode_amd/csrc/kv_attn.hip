@@ -25,12 +25,15 @@ constexpr int kStep = 2;               // tiles of one step: 32 tokens, the k of
 constexpr int kRefill = 64 / kStep;    // steps whose block ids and scales one lane each holds
 constexpr int kMaxSeqs = 4096;
 constexpr int kMinPart = kWaves * kStep;    // tiles: the least part of a request, a step a wave
-constexpr int kShortPart = 4 * kMinPart;
-constexpr int kRounds = 4;                  // workgroups aimed at for each place on the chip
 constexpr int kCus = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// A request that is cut into parts, for what joins them; parts = 0 behind the last.
+struct Split {
+    int32_t parts, slot, row0, rows;     // slot: of its first partial result
+};
 
 struct AttnArgs {
     const uint8_t *k, *v;
@@ -39,10 +42,11 @@ struct AttnArgs {
     const int32_t *seq_start, *lens, *table;
     uint16_t* out;
     float *lse, *part_o, *part_ml;
+    Split* splits;                       // [n_splits]
     const float* slopes;
     int64_t q_stride, out_stride;
     uint32_t per_group;                  // ceil(2^32 / group)
-    int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, places, most;
+    int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, places, n_splits;
     bool by_seq;
     float scale, softcap;
 };
@@ -88,22 +92,25 @@ __device__ __forceinline__ int wave_scan(int v) {
 }
 
 // The lengths are known on the device alone, so every wave cuts the work up itself: all
-// tiles over the workgroups that the call aims at is a chunk, a request is cut into
+// tiles over the places that the chip has for workgroups is a chunk, a request is cut into
 // ceil(tiles / chunk) even parts, and a workgroup's part follows from the prefix sums of
-// their counts: two scans of 64 lanes.
+// their counts.  One round of workgroups: two or four rounds of shorter ones, which end
+// more evenly, lost more on the way to their first product (32 requests of 32768 tokens
+// 201 and 207 us against 193, one of 131072 64 and 77 against 57).
 __device__ __forceinline__ int tiles_of(const Seq& s) { return s.n_new < 1 ? 0 : max(s.hi - s.lo, 1); }
 
 // A workgroup's part of a request, or (by_seq) all of one.
 struct Item {
     int32_t seq, part, parts, slot;      // slot: of the request's first partial result
+    int32_t split;                       // split requests before it
 };
 
 __device__ __forceinline__ int32_t even_part(int tiles, int parts) {     // tiles of a part, whole steps
     return ((tiles - 1) / parts + kStep) / kStep * kStep;
 }
 
-// The item `want`, or request `want` as a whole (is_seq); seq is -1 if there is none.
-__device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, bool is_seq, Seq* sq) {
+// Item `want` (seq is -1 if there is none), its request, and how many requests are split.
+__device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, Seq* sq, int* splits) {
     const int lane = threadIdx.x & 63;
     const int per = (a.n_seqs + 63) / 64;
     const int i0 = lane * per, i1 = min(i0 + per, a.n_seqs);
@@ -117,29 +124,39 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, bool 
     }
     tiles = max(__builtin_amdgcn_readlane(wave_scan(tiles), 63), 1);
     used = __builtin_amdgcn_readlane(wave_scan(used), 63);
-    // ceil(tiles_i / chunk) add up to at most tiles / chunk + used.  One round of the places
-    // that the chip has, if that leaves short parts (their time is the way to the first
-    // product, not the bytes); else the longer row of workgroups, which ends evenly.
-    uint32_t chunk = uint32_t(tiles - 1) / uint32_t(max(a.places - used, 1)) + 1;
-    if (chunk > kShortPart) chunk = uint32_t(tiles - 1) / uint32_t(max(a.most - used, 1)) + 1;
-    chunk = max(chunk, uint32_t(kMinPart));
+    // ceil(tiles_i / chunk) add up to between tiles / chunk and that + used: the smallest
+    // of three chunks whose parts fit the places, of which the last always does (unless
+    // there are more requests than places: those stay whole)
+    uint32_t chunk = 0;
+    int items = 0, slots = 0, cut = 0, p0 = 0;     // parts, those of split requests, split requests
     auto parts_of = [&](int n) { return int((uint32_t(n) + chunk - 1) / chunk); };
-    const int p0 = parts_of(n0);
-    int items = p0, split = p0 > 1 ? p0 : 0;
-    for (int i = i0 + 1; i < i1; ++i) {
-        const int p = parts_of(tiles_of(load_seq(a, i)));
-        items += p;
-        split += p > 1 ? p : 0;
+#pragma unroll 1
+    for (int tries = 0; tries < 3; ++tries) {
+        const int room = a.places - (tries * used + 1) / 2;
+        chunk = max(room > 0 ? uint32_t(tiles - 1) / uint32_t(room) + 1 : uint32_t(tiles), uint32_t(kMinPart));
+        p0 = parts_of(n0);
+        items = p0;
+        cut = p0 > 1;
+        slots = p0 > 1 ? p0 : 0;
+        for (int i = i0 + 1; i < i1; ++i) {
+            const int p = parts_of(tiles_of(load_seq(a, i)));
+            items += p;
+            cut += p > 1;
+            slots += p > 1 ? p : 0;
+        }
+        if (__builtin_amdgcn_readlane(wave_scan(items), 63) <= a.places) break;
     }
-    int item0 = wave_scan(items) - items, slot0 = wave_scan(split) - split;
-    Item it{-1, 0, 0, 0};
+    const int cut_end = wave_scan(cut);
+    int item0 = wave_scan(items) - items, slot0 = wave_scan(slots) - slots, cut0 = cut_end - cut;
+    Item it{-1, 0, 0, 0, 0};
     Seq s = mine;
     auto look = [&](int i, int p, const Seq& is) {
-        if (is_seq ? i == want : want >= item0 && want < item0 + p) {
-            it = {i, want - item0, p, slot0};
+        if (want >= item0 && want < item0 + p) {
+            it = {i, want - item0, p, slot0, cut0};
             s = is;
         }
         item0 += p;
+        cut0 += p > 1;
         slot0 += p > 1 ? p : 0;
     };
     if (i0 < a.n_seqs) look(i0, p0, mine);
@@ -151,7 +168,8 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, bool 
     const int l = who ? __builtin_ctzll(who) : 0;
     auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
     *sq = {of(s.row0), of(s.n_new), of(s.rows), of(s.p0), of(s.lo), of(s.hi), of(s.len)};
-    return {who ? of(it.seq) : -1, of(it.part), of(it.parts), of(it.slot)};
+    *splits = __builtin_amdgcn_readlane(cut_end, 63);
+    return {who ? of(it.seq) : -1, of(it.part), of(it.parts), of(it.slot), of(it.split)};
 }
 
 // Maximum over the four lanes of a query row (lane % 16): the rows of 16 lanes swap places.
@@ -220,12 +238,23 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
     const int g = lane >> 4, n = lane & 15;
     const int head = blockIdx.y % a.n_kv, r0 = blockIdx.y / a.n_kv * ROWS;
     const int in_block = (1 << a.shift) - 1;
-    Item it{int32_t(blockIdx.x), 0, 1, 0};
+    Item it{int32_t(blockIdx.x), 0, 1, 0, 0};
     Seq sq;
     if (a.by_seq) sq = load_seq(a, it.seq);
-    else it = find_item(a, blockIdx.x, false, &sq);
-    if (it.seq < 0) return;
-    if (r0 >= sq.rows) return;
+    else {
+        int splits;
+        it = find_item(a, blockIdx.x, &sq, &splits);
+        if (blockIdx.y == 0 && threadIdx.x == 0) {
+            const int w = blockIdx.x;
+            if (w >= splits && w < a.n_splits) a.splits[w] = Split{0, 0, 0, 0};
+            if (it.seq >= 0 && it.parts > 1 && it.part == 0) a.splits[it.split] = Split{it.parts, it.slot, sq.row0, sq.rows};
+        }
+    }
+    if (it.seq < 0 || r0 >= sq.rows) return;
+    // the same in all lanes, which the compiler cannot see of loaded values: scalar registers
+    auto same = [](int32_t& v) { v = __builtin_amdgcn_readfirstlane(v); };
+    same(sq.row0), same(sq.n_new), same(sq.rows), same(sq.p0), same(sq.lo), same(sq.hi), same(sq.len);
+    same(it.seq), same(it.part), same(it.parts), same(it.slot);
     const int rows = min(ROWS, sq.rows - r0);
     // what the first and the last row see bounds what any row sees
     const int pos_first = sq.p0 + token_of(a, r0), pos_last = sq.p0 + token_of(a, r0 + rows - 1);
@@ -425,6 +454,17 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
         for (int k = 0; k < end; ++k) step(tile_of(k0 + k), kStep * k, tile_of(k0 + k + 1), k + 1 < end);
     }
 
+    // A row's four channels from d on: final, from their weighted sum, and the row's sum of weights.
+    auto put = [&](int r, int d, const f32x4 o, float m, float l) {
+        const int j = token_of(a, r0 + r), qh = head * a.group + (r0 + r - j * a.group);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint16_t* to = a.out + int64_t(sq.row0 + j) * a.out_stride + int64_t(qh) * D + d;
+        *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+        if (d == 0 && a.lse) a.lse[int64_t(sq.row0 + j) * (a.n_kv * a.group) + qh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    };
+    auto row_of = [&](int part) { return (int64_t(it.slot + part) * gridDim.y + blockIdx.y) * ROWS; };
+
+
     // Join the waves: a common maximum a row, then sums slab by slab through LDS.
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -467,78 +507,106 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
                 o += *reinterpret_cast<const f32x4*>(&merge[w][r][d]);
             }
             if (it.parts == 1) {
-                const int j = token_of(a, r0 + r), qh = head * a.group + (r0 + r - j * a.group);
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                uint16_t* to = a.out + int64_t(sq.row0 + j) * a.out_stride + int64_t(qh) * D + 64 * c + d;
-                *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
-                if (c == 0 && d == 0 && a.lse)
-                    a.lse[int64_t(sq.row0 + j) * (a.n_kv * a.group) + qh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+                put(r, 64 * c + d, o, m, l);
             } else {
-                const int64_t to = (int64_t(it.slot + it.part) * gridDim.y + blockIdx.y) * ROWS + r;
+                const int64_t to = row_of(it.part) + r;
                 *reinterpret_cast<f32x4*>(a.part_o + to * D + 64 * c + d) = o;
                 if (c == 0 && d == 0) *reinterpret_cast<f32x2*>(a.part_ml + to * 2) = f32x2{m, l};
             }
         }
-    }}
+    }
+}
 
-// The parts of split requests, one workgroup a row: lanes over channels, waves over parts.
-template <int DQ>
-__global__ __launch_bounds__(64 * kWaves) void join_kernel(AttnArgs a, int rows_of_tile) {
+// The parts of the split requests: a workgroup for each four query rows of a request and
+// head, WAVES waves a row; lanes over channels, waves over parts.
+// A second launch: joining in the last workgroup to arrive needs partial results that
+// pass the XCDs' L2s and a counter, which took longer (one request of 2048 tokens 10.5
+// against 8.9 us, one of 131072 84 against 57).
+constexpr int kJoinRows = 4, kJoinAhead = 8;
+
+template <int DQ, int WAVES>
+__global__ __launch_bounds__(64 * kJoinRows * WAVES) void join_kernel(AttnArgs a, int rows_of_tile) {
     constexpr int D = 64 * DQ;
-    __shared__ float part[kWaves][D];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    Seq sq;
-    const Item it = find_item(a, blockIdx.x, true, &sq);
-    if (it.parts < 2) return;
-    const int head = blockIdx.y % a.n_kv, tile = blockIdx.y / a.n_kv;
-    const int r = tile * rows_of_tile + blockIdx.z;
-    if (r >= sq.rows) return;
-    auto row_of = [&](int p) { return (int64_t(it.slot + p) * gridDim.y + blockIdx.y) * rows_of_tile + blockIdx.z; };
-    float m = -INFINITY;
-    for (int p = lane; p < it.parts; p += 64) m = fmaxf(m, a.part_ml[row_of(p) * 2]);
+    __shared__ float joined[kJoinRows][WAVES][D], top[kJoinRows][WAVES], sum[kJoinRows][WAVES];
+    const int lane = threadIdx.x & 63, row = threadIdx.x / (64 * WAVES), wave = (threadIdx.x >> 6) % WAVES;
+    const Split sp = a.splits[blockIdx.x];
+    const int head = blockIdx.y % a.n_kv, in_tile = blockIdx.z * kJoinRows + row;
+    const int r = blockIdx.y / a.n_kv * rows_of_tile + in_tile;
+    if (sp.parts == 0 || r - row >= sp.rows) return;
+    const bool mine = in_tile < rows_of_tile && r < sp.rows;
+    auto row_of = [&](int p) { return (int64_t(sp.slot + p) * gridDim.y + blockIdx.y) * rows_of_tile + (mine ? in_tile : 0); };
+    float m = -INFINITY, l = 0.f, o[DQ] = {};
+    for (int p0 = wave; p0 < sp.parts; p0 += kJoinAhead * WAVES) {
+        f32x2 ml[kJoinAhead];
+        float x[kJoinAhead][DQ];
 #pragma unroll
-    for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int p = lane; p < it.parts; p += 64) {
-        const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + row_of(p) * 2);
-        l += ml[1] * __builtin_amdgcn_exp2f(ml[0] - base);
+        for (int k = 0; k < kJoinAhead; ++k) {
+            const int64_t at = row_of(min(p0 + k * WAVES, sp.parts - 1));
+            ml[k] = *reinterpret_cast<const f32x2*>(a.part_ml + at * 2);
+#pragma unroll
+            for (int c = 0; c < DQ; ++c) x[k][c] = a.part_o[at * D + 64 * c + lane];
+        }
+        float most = m;
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k)
+            if (p0 + k * WAVES < sp.parts) most = fmaxf(most, ml[k][0]);
+        const float base = most == -INFINITY ? 0.f : most, f0 = __builtin_amdgcn_exp2f(m - base);
+        m = most;
+        l *= f0;
+#pragma unroll
+        for (int c = 0; c < DQ; ++c) o[c] *= f0;
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k)
+            if (p0 + k * WAVES < sp.parts) {
+                const float f = __builtin_amdgcn_exp2f(ml[k][0] - base);
+                l += ml[k][1] * f;
+#pragma unroll
+                for (int c = 0; c < DQ; ++c) o[c] += x[k][c] * f;
+            }
     }
+    if (WAVES > 1 && lane == 0) top[row][wave] = m;
+    if (WAVES > 1) {
+        __syncthreads();
+        float most = top[row][0];
 #pragma unroll
-    for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
-    float o[DQ] = {};
-#pragma unroll 4
-    for (int p = wave; p < it.parts; p += kWaves) {
-        const int64_t row = row_of(p);
-        const float f = __builtin_amdgcn_exp2f(a.part_ml[row * 2] - base);
+        for (int w = 1; w < WAVES; ++w) most = fmaxf(most, top[row][w]);
+        const float f = __builtin_amdgcn_exp2f(m - (most == -INFINITY ? 0.f : most));
+        m = most;
+        l *= f;
 #pragma unroll
-        for (int c = 0; c < DQ; ++c) o[c] += a.part_o[row * D + 64 * c + lane] * f;
+        for (int c = 0; c < DQ; ++c) o[c] *= f;
     }
+    if (lane == 0) sum[row][wave] = l;
 #pragma unroll
-    for (int c = 0; c < DQ; ++c) part[wave][64 * c + lane] = o[c];
+    for (int c = 0; c < DQ; ++c) joined[row][wave][64 * c + lane] = o[c];
     __syncthreads();
+    if (!mine) return;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) l += sum[row][w];
     const int j = token_of(a, r), qh = head * a.group + (r - j * a.group);
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t* to = a.out + int64_t(sq.row0 + j) * a.out_stride + int64_t(qh) * D;
-    for (int d = threadIdx.x * 2; d < D; d += 128 * kWaves) {
+    const int64_t token = sp.row0 + j;
+    const int first = (threadIdx.x % (64 * WAVES)) * 2;
+    for (int d = first; d < D; d += 128 * WAVES) {
         float x0 = 0.f, x1 = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            x0 += part[w][d];
-            x1 += part[w][d + 1];
+        for (int w = 0; w < WAVES; ++w) {
+            x0 += joined[row][w][d];
+            x1 += joined[row][w][d + 1];
         }
-        *reinterpret_cast<uint32_t*>(to + d) = pack_bf16(x0 * inv, x1 * inv);
+        *reinterpret_cast<uint32_t*>(a.out + token * a.out_stride + int64_t(qh) * D + d) = pack_bf16(x0 * inv, x1 * inv);
     }
-    if (threadIdx.x == 0 && a.lse)
-        a.lse[int64_t(sq.row0 + j) * (a.n_kv * a.group) + qh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    if (first == 0 && a.lse) a.lse[token * (a.n_kv * a.group) + qh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
 // How a call is laid out; the same for the workspace's size and the launch.
 struct Plan {
-    int32_t group, nt, row_tiles, places, most;
+    int32_t group, nt, row_tiles, places;
     bool by_seq;
     uint32_t grid_x, grid_y;
     uint64_t parts;          // partial results, of nt * 16 rows for every grid_y
+    uint64_t splits;         // requests that they can come from
     uint64_t bytes;
 };
 
@@ -561,12 +629,11 @@ static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs
     const int64_t room = kCus * per_cu(c->head_dim / 64, p->nt);
     const int64_t longest = (seq_tiles + kMinPart - 1) / kMinPart;         // parts of one request at most
     p->places = int32_t(std::max<int64_t>(1, room / y));
-    p->most = int32_t(std::max<int64_t>(1, kRounds * room / y));
-    p->by_seq = longest < 2 || p->most < 2 || (p->row_tiles > 1 && y * n_seqs >= room);
-    p->grid_x = uint32_t(p->by_seq ? n_seqs : std::min<int64_t>(p->most + n_seqs, n_seqs * longest));
-    // a request is split if it is longer than a chunk, so into fewer than twice its chunks
-    p->parts = p->by_seq ? 0 : std::min<int64_t>(2 * p->most, p->grid_x);
-    p->bytes = p->parts * p->grid_y * (16u * p->nt) * (c->head_dim + 2) * sizeof(float);
+    p->by_seq = longest < 2 || p->places < 2 || (p->row_tiles > 1 && y * n_seqs >= room);
+    p->grid_x = uint32_t(p->by_seq ? n_seqs : std::min<int64_t>(std::max(p->places, n_seqs), n_seqs * longest));
+    p->parts = p->by_seq ? 0 : std::min<int64_t>(p->places, p->grid_x);    // more requests than places: none is split
+    p->splits = std::min<int64_t>(n_seqs, p->parts / 2);
+    p->bytes = p->parts * p->grid_y * (16u * p->nt) * (c->head_dim + 2) * sizeof(float) + p->splits * sizeof(Split);
     return MBD_OK;
 }
 
@@ -575,8 +642,15 @@ static void launch(const AttnArgs& a, const Plan& p, bool ext, hipStream_t s) {
     const dim3 grid(p.grid_x, p.grid_y), block(64 * kWaves);
     if (ext) hipLaunchKernelGGL((attn_kernel<E4M3, DQ, NT, true>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((attn_kernel<E4M3, DQ, NT, false>), grid, block, 0, s, a);
-    if (p.parts)
-        hipLaunchKernelGGL((join_kernel<DQ>), dim3(a.n_seqs, p.grid_y, std::min(16 * NT, a.max_new * a.group)), block, 0, s, a, 16 * NT);
+    if (p.parts) {
+        const int rows = std::min(16 * NT, a.max_new * a.group);
+        const dim3 joins(unsigned(p.splits), p.grid_y, unsigned((rows + kJoinRows - 1) / kJoinRows));
+        // few requests can have many parts each: more waves over them
+        if (p.parts > 8 * p.splits)
+            hipLaunchKernelGGL((join_kernel<DQ, 4>), joins, dim3(64 * kJoinRows * 4), 0, s, a, 16 * NT);
+        else
+            hipLaunchKernelGGL((join_kernel<DQ, 1>), joins, dim3(64 * kJoinRows), 0, s, a, 16 * NT);
+    }
 }
 
 template <bool E4M3, int DQ>
@@ -651,6 +725,7 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     a.lse = lse;
     a.part_o = static_cast<float*>(ws);
     a.part_ml = a.part_o + p.parts * p.grid_y * (16u * p.nt) * cache->head_dim;
+    a.splits = reinterpret_cast<kv::Split*>(a.part_ml + p.parts * p.grid_y * (16u * p.nt) * 2);
     a.slopes = args->slopes;
     a.q_stride = args->q_stride;
     a.out_stride = args->out_stride;
@@ -665,7 +740,7 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     a.group = p.group;
     a.per_group = uint32_t(((uint64_t(1) << 32) + p.group - 1) / p.group);
     a.places = p.places;
-    a.most = p.most;
+    a.n_splits = int32_t(p.splits);
     a.by_seq = p.by_seq;
     a.scale = args->scale;
     a.softcap = args->softcap;
