@@ -434,7 +434,7 @@ typedef struct {
     int32_t max_new;      /* most new tokens of one request, >= 1: 1 for decode, N+1 to
                              verify N drafts, more for prompts                          */
     int32_t window;       /* >= 0                                                       */
-    float scale, softcap; /* finite; softcap >= 0                                       */
+    float scale, softcap; /* finite; softcap in [0, 2^64]                               */
     const float* slopes;  /* device fp32 [n_heads], or NULL                             */
     int64_t q_stride;     /* elements from one token's row to the next, a multiple of 8 */
     int64_t out_stride;   /*   and at least n_heads * head_dim                          */

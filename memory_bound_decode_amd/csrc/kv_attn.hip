@@ -48,7 +48,7 @@ struct AttnArgs {
     uint32_t per_group;                  // ceil(2^32 / group)
     int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, places, n_splits;
     bool by_seq;
-    float scale, softcap;
+    float to_score, softcap;             // product to score in the log2 domain (or over the cap); the cap there
 };
 
 // Token of a query row: r / group, exact for r * group below 2^32.
@@ -217,6 +217,14 @@ __device__ __forceinline__ uint32_t live_bytes(int tok, int len) {
     return n == 4 ? 0xffffffffu : (1u << (8 * n)) - 1u;
 }
 
+// Near 0, where 1 - 2 / (1 + e^2x) would cancel, the series (next term below 2^-26 of it).
+__device__ __forceinline__ float tanh_of(float x) {
+    const float y = x * x;
+    const float near = x * (1.f + y * (-1.f / 3 + y * (2.f / 15 + y * (-17.f / 315 + y * (62.f / 2835)))));
+    const float far = 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * (2.f * kLog2e)));
+    return y < 0.0625f ? near : far;
+}
+
 // Codes unpacked far ahead of their product would cost a wave or two a SIMD in registers.
 __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
 
@@ -236,12 +244,16 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
     __shared__ float merge_m[kWaves][ROWS], merge_l[kWaves][ROWS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, n = lane & 15;
-    const int head = blockIdx.y % a.n_kv, r0 = blockIdx.y / a.n_kv * ROWS;
     const int in_block = (1 << a.shift) - 1;
-    Item it{int32_t(blockIdx.x), 0, 1, 0, 0};
+    // By request: heads side by side, so that a head's row tiles share an XCD's L2 and every
+    // XCD has all requests; a request's last rows, which see most, first.
+    int head = blockIdx.x, r0 = (gridDim.y - 1 - blockIdx.y) * ROWS;
+    Item it{int32_t(blockIdx.z), 0, 1, 0, 0};
     Seq sq;
     if (a.by_seq) sq = load_seq(a, it.seq);
     else {
+        head = blockIdx.y % a.n_kv;
+        r0 = blockIdx.y / a.n_kv * ROWS;
         int splits;
         it = find_item(a, blockIdx.x, &sq, &splits);
         if (blockIdx.y == 0 && threadIdx.x == 0) {
@@ -337,7 +349,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
         float ks[kStep], vs[kStep];
 #pragma unroll
         for (int h = 0; h < kStep; ++h) {
-            ks[h] = lane_float(my_ks, l + h) * a.scale;
+            ks[h] = lane_float(my_ks, l + h) * a.to_score;
             vs[h] = lane_float(my_vs, l + h);
             whole = whole && __builtin_amdgcn_readlane(my_id, l + h) >= 0;
 #pragma unroll
@@ -363,15 +375,14 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             float u[kStep][4];
+            const float away = float(tile * kTok + 4 * g - pos[t]);
 #pragma unroll
             for (int h = 0; h < kStep; ++h)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float x = s[h][t][i] * ks[h];
-                    if (EXT && a.softcap > 0.f)     // cap * tanh(x / cap) = cap * (1 - 2 / (1 + e^(2 x / cap)))
-                        x = a.softcap * (1.f - 2.f * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * (2.f * kLog2e) / a.softcap)));
-                    x *= kLog2e;
-                    if (EXT) x += slope[t] * float((tile + h) * kTok + 4 * g + i - pos[t]);
+                    if (EXT && a.softcap > 0.f) x = a.softcap * tanh_of(x);
+                    if (EXT) x += slope[t] * (away + float(h * kTok + i));
                     u[h][i] = x;
                 }
             if (!whole) {
@@ -639,7 +650,7 @@ static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs
 
 template <bool E4M3, int DQ, int NT>
 static void launch(const AttnArgs& a, const Plan& p, bool ext, hipStream_t s) {
-    const dim3 grid(p.grid_x, p.grid_y), block(64 * kWaves);
+    const dim3 grid = p.by_seq ? dim3(a.n_kv, p.row_tiles, a.n_seqs) : dim3(p.grid_x, p.grid_y), block(64 * kWaves);
     if (ext) hipLaunchKernelGGL((attn_kernel<E4M3, DQ, NT, true>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((attn_kernel<E4M3, DQ, NT, false>), grid, block, 0, s, a);
     if (p.parts) {
@@ -696,8 +707,8 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     if (st != MBD_OK) return st;
     if (args->T < 0 || args->T > (1 << 24)) return fail(MBD_ESHAPE, "T %d outside [0, 2^24]", args->T);
     if (args->window < 0) return fail(MBD_EINVAL, "window %d below 0", args->window);
-    if (!std::isfinite(args->scale) || !std::isfinite(args->softcap) || args->softcap < 0)
-        return fail(MBD_EINVAL, "scale and softcap must be finite, softcap not below 0");
+    if (!std::isfinite(args->scale) || !(args->softcap >= 0 && args->softcap <= 0x1p64f))
+        return fail(MBD_EINVAL, "scale must be finite, softcap in [0, 2^64]");
     const int64_t row = int64_t(args->n_heads) * cache->head_dim;
     if (args->q_stride < row || args->out_stride < row || args->q_stride % 8 || args->out_stride % 8)
         return fail(MBD_ESHAPE, "row strides must be multiples of 8 and at least n_heads * head_dim");
@@ -742,8 +753,8 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     a.places = p.places;
     a.n_splits = int32_t(p.splits);
     a.by_seq = p.by_seq;
-    a.scale = args->scale;
-    a.softcap = args->softcap;
+    a.to_score = args->softcap > 0 ? args->scale / args->softcap : kv::kLog2e * args->scale;
+    a.softcap = args->softcap * kv::kLog2e;
     const bool ext = a.window > 0 || args->softcap > 0 || args->slopes;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     if (cache->fmt == MBD_KV_E4M3) kv::launch_dim<true>(a, p, cache->head_dim / 64, ext, s);

@@ -450,6 +450,22 @@ def test_attn_split_long(dev, fmt):
     _run_attn(dev, fmt, 64, 16, 2, 2, [6001, 50], [5, 2], softcap=30.0, window=4000)
 
 
+def test_attn_wide_cap_is_no_cap(dev):
+    """A cap far above every score leaves them as they are: cap tanh(u / cap) = u - u^3 / (3 cap^2) + ..,
+    so with |u| < 100 and a cap of 1e6 within 1e-6, far inside the tolerance of the uncapped call."""
+    call, check, (out, lse, _) = _attn_case(dev, INT8, 128, 16, 2, 2, [300, 90], [2, 1])
+    call()
+    torch.cuda.synchronize()
+    check()
+    want, wlse = out.float().clone(), lse.clone()
+    capped, _, (out, lse, _) = _attn_case(dev, INT8, 128, 16, 2, 2, [300, 90], [2, 1], softcap=1e6)
+    capped()
+    torch.cuda.synchronize()
+    assert (lse - wlse).abs().max().item() <= 2.0 ** -16
+    # scores that close move a bf16 weight or output by one of its steps at most
+    assert ((out.float() - want).abs() <= 2.0 ** -7 * want.abs() + 2.0 ** -9 * want.abs().max()).all()
+
+
 def test_attn_many_requests(dev):
     _run_attn(dev, INT8, 64, 16, 1, 2, list(np.random.default_rng(1).integers(1, 60, 300)), [1] * 300)
 

@@ -82,7 +82,7 @@ BAD_ARGS = [(dict(n_heads=7), "ESHAPE"), (dict(n_heads=0), "ESHAPE"), (dict(n_se
             (dict(max_blocks=0), "ESHAPE"), (dict(max_blocks=(1 << 26) + 1), "ESHAPE"), (dict(max_blocks=1 << 26, n_seqs=32), "ESHAPE"),
             (dict(T=-1), "ESHAPE"), (dict(T=(1 << 24) + 1), "ESHAPE"), (dict(max_new=0), "ESHAPE"), (dict(max_new=1 << 22), "ESHAPE"),
             (dict(window=-1), "EINVAL"), (dict(scale=float("nan")), "EINVAL"), (dict(softcap=-1.0), "EINVAL"),
-            (dict(softcap=float("inf")), "EINVAL"), (dict(q_stride=1016), "ESHAPE"), (dict(out_stride=1028), "ESHAPE"),
+            (dict(softcap=float("inf")), "EINVAL"), (dict(softcap=float("nan")), "EINVAL"), (dict(n_heads=514), "ESHAPE"), (dict(q_stride=1016), "ESHAPE"), (dict(out_stride=1028), "ESHAPE"),
             (dict(slopes=P + 2), "EALIGN")]
 
 
