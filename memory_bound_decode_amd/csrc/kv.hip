@@ -229,38 +229,36 @@ __device__ __forceinline__ uint32_t encode(const float v[4]) {
     return w;
 }
 
-// Sixteen values x over a scale, as the codes of one unit.  Dividing costs about ten
-// operations a value, more than all the rest; the product with the reciprocal r costs one.
-// E4M3: the scale is a power of two, the product is the quotient.  INT8: x r + 1.5 * 2^23
-// rounds the exact product to a whole number, whose low byte is the code; the product is
-// off by at most 127.5 * 2^-24, so only where it lies within 2^-14 of a tie can the
-// quotient's own rounding matter, and the wave divides after all.
+// Sixteen values x over a scale, as the codes of one unit.  r is the scale's reciprocal,
+// correctly rounded.  E4M3: the scale is a power of two, the product is the quotient.  INT8:
+// Markstein's theorem (IBM J. Res. Dev. 34, 1990): for such an r and a q within an ulp of
+// x / s, q + r (x - q s) with fused operations rounds correctly; three operations where a
+// division without r takes ten and more.  Adding 1.5 * 2^23 then rounds to a whole number,
+// ties to even, whose low byte is the code.  (The bare product x r will not do: a value of half
+// the block's maximum is a tie, 63.5, which is found in two of three waves.)
 template <bool E4M3>
-__device__ __forceinline__ u32x4 encode_unit(const float x[16], float div, float r, bool exact) {
+__device__ __forceinline__ u32x4 encode_unit(const float x[16], float div, float r, bool any_values) {
     u32x4 w;
-    if (!exact) {
+    if (!any_values) {
         if constexpr (E4M3) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * q] * r, x[4 * q + 1] * r, 0, false);
                 w[q] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(x[4 * q + 2] * r, x[4 * q + 3] * r, lo, true));
             }
-            return w;
-        }
-        constexpr float magic = 12582912.f;
-        float off = 0.f;
+        } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t c[4];
+            for (int q = 0; q < 4; ++q) {
+                uint32_t c[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float n = __builtin_fmaf(x[4 * q + i], r, magic);
-                c[i] = __float_as_uint(n);
-                off = fmaxf(off, fabsf(__builtin_fmaf(x[4 * q + i], r, magic - n)));
+                for (int i = 0; i < 4; ++i) {
+                    const float v = x[4 * q + i], near = v * r;
+                    c[i] = __float_as_uint(__builtin_fmaf(__builtin_fmaf(-near, div, v), r, near) + 12582912.f);
+                }
+                w[q] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(c[3], c[2], 0x0c0c0400), __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400), 0x05040100);
             }
-            w[q] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(c[3], c[2], 0x0c0c0400), __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400), 0x05040100);
         }
-        if (!__any(off > 0.5f - 0x1p-14f)) return w;
+        return w;
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -290,9 +288,11 @@ template <> struct Quad<float> {
     __device__ void clear() { v = f32x4{0.f, 0.f, 0.f, 0.f}; }
     __device__ float at(int j) const { return v[j]; }
     // the largest |bits|: above every finite value's where one is infinite or NaN
-    __device__ uint32_t top() const {
+    typedef uint32_t Top;
+    static __device__ uint32_t bits(Top t) { return t; }
+    __device__ void raise(Top& t) const {
         const u32x4 b = __builtin_bit_cast(u32x4, v) & 0x7fffffffu;
-        return max(max(b.x, b.y), max(b.z, b.w));
+        t = max(max(t, max(b.x, b.y)), max(b.z, b.w));
     }
 };
 template <> struct Quad<uint16_t> {
@@ -300,9 +300,11 @@ template <> struct Quad<uint16_t> {
     __device__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x2*>(p); }
     __device__ void clear() { v = u32x2{0, 0}; }
     __device__ float at(int j) const { return __uint_as_float(j & 1 ? v[j / 2] & 0xffff0000u : v[j / 2] << 16); }
-    __device__ uint32_t top() const {
-        const uint32_t a = v.x & 0x7fff7fffu, b = v.y & 0x7fff7fffu;
-        return max(max(a << 16, a & 0xffff0000u), max(b << 16, b & 0xffff0000u));
+    typedef uint16_t Top __attribute__((ext_vector_type(2)));
+    static __device__ uint32_t bits(Top t) { return uint32_t(max(t.x, t.y)) << 16; }
+    __device__ void raise(Top& t) const {
+        t = __builtin_elementwise_max(t, __builtin_bit_cast(Top, v.x & 0x7fff7fffu));
+        t = __builtin_elementwise_max(t, __builtin_bit_cast(Top, v.y & 0x7fff7fffu));
     }
 };
 
@@ -327,6 +329,7 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
     u32x4 old[THREADS == 64 ? KEEP : 1];
     auto first_token = [&](int tile) { return tile * kTok + (V ? 4 * g : m); };
     auto unit_at = [&](int tile, int s) { return reinterpret_cast<u32x4*>(codes + int64_t(tile) * kTok * D + s * 1024 + lane * 16); };
+    auto all_new = [&](int tile) { return tile * kTok >= fill && (tile + 1) * kTok <= end; };     // in every lane
     // a unit that also holds tokens of before, or bytes behind the last
     auto boundary = [&](bool in, int tile, int s) {
         const int first = first_token(tile);
@@ -339,25 +342,30 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
         for (int i = 0; i < KEEP; ++i) {
             const int c = c0 + i * (THREADS / 64) + wave;
             const int tile = tile0 + c / slabs, s = c % slabs, first = first_token(tile);
+            const T* from = row0 + (first - fill) * stride + 64 * s + (V ? 4 * m : 16 * g);
+            if (c < chunks && all_new(tile)) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[i][k].load(from + (V ? k * stride : 4 * k));
+                continue;
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int tok = V ? first + k : first;
                 x[i][k].clear();
-                if (c < chunks && tok >= fill && tok < end)
-                    x[i][k].load(row0 + (tok - fill) * stride + 64 * s + (V ? 4 * m : 16 * g + 4 * k));
+                if (c < chunks && tok >= fill && tok < end) x[i][k].load(from + (V ? k * stride : 4 * k));
             }
             if constexpr (THREADS == 64) old[i] = boundary(c < chunks, tile, s);   // early: few waves, so latency counts
         }
     };
     constexpr int round = KEEP * (THREADS / 64);
     const bool once = chunks <= round;
-    uint32_t top = 0;
+    typename Quad<T>::Top most{};
     for (int c0 = 0; c0 < chunks; c0 += round) {
         load(c0);
 #pragma unroll
         for (int i = 0; i < KEEP; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) top = max(top, x[i][k].top());
+            for (int k = 0; k < 4; ++k) x[i][k].raise(most);
     }
     auto reduce = [&](uint32_t v) {
 #pragma unroll
@@ -371,7 +379,7 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
         }
         return uint32_t(__builtin_amdgcn_readfirstlane(int(v)));
     };
-    top = reduce(top);
+    uint32_t top = reduce(Quad<T>::bits(most));
     const bool finite = top < 0x7f800000u;
     if (!finite) {                       // the largest of the finite values
         top = 0;
@@ -393,7 +401,7 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
     const bool grew = wanted > old_scale;
     const float now = grew ? wanted : old_scale, div = now > 0.f ? now : 1.f;
     const float r = 1.f / div, ratio = old_scale / div;
-    const bool exact = !finite || !(div >= 0x1p-126f);      // smaller ones have no reciprocal
+    const bool any_values = !finite || !(div >= 0x1p-100f);    // a smaller scale's remainders lose bits
     if (tid == 0 && (grew || fill == 0)) a.scales[V][bh] = now;
     for (int c0 = 0; c0 < chunks; c0 += round) {
         if (!once) load(c0);
@@ -407,7 +415,11 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
             for (int k = 0; k < 4; ++k)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[V ? 4 * j + k : 4 * k + j] = x[i][k].at(j);
-            const u32x4 fresh = encode_unit<E4M3>(v, div, r, exact);
+            const u32x4 fresh = encode_unit<E4M3>(v, div, r, any_values);
+            if (all_new(tile)) {
+                *unit_at(tile, s) = fresh;
+                continue;
+            }
             if (first >= end || (!grew && first + (V ? 4 : 1) <= fill)) continue;
             uint32_t mask = 0;           // bytes of a word whose tokens are new
 #pragma unroll
@@ -494,7 +506,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // are taken by the whole workgroup, so that prompts are read once and all their loads are
 // in flight together; short ones (a wave's units at most) by one wave each.
 template <bool E4M3, class T>
-__global__ __launch_bounds__(256) void append_window_kernel(AppendArgs a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 6 : 4))) void append_window_kernel(AppendArgs a) {
     __shared__ uint32_t lds[4];
     constexpr int kept = 2;            // fewer registers, more workgroups in flight
     const int wave = threadIdx.x >> 6;
