@@ -8,6 +8,7 @@ symbols raises.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import numpy as np
 
@@ -135,8 +136,7 @@ def _stream(stream):
     if stream is not None:
         return ctypes.c_void_p(int(stream))
     import torch
-    # the raw handle: building a torch.cuda.Stream for it takes 3 us, as long as a launch
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
 def _ptr(t):
@@ -210,10 +210,16 @@ def mbd_encode_cassandra(w, act_norm, keep_num: int, keep_den: int, plan: MbdEnc
 
 # ------------------------------------------------------------------ KV cache
 
-def _here():
-    """The current GPU's index, whose stream a call takes; -2 (no tensor's) without one."""
+# A decode step makes these calls for every layer, and a launch takes 3 us: the checks look
+# at each tensor once, and build nothing.
+
+def _gpu(name, t):
+    """The index of the GPU that holds ``t``, which has to be the current one: its stream is taken."""
     import torch
-    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
+    here = t.get_device()
+    if here < 0 or here != torch.cuda.current_device():
+        raise ValueError("%s is on %s, not on the current GPU" % (name, t.device))
+    return here
 
 
 def _refuse(here, name, t, dtype, n=None):
@@ -222,25 +228,33 @@ def _refuse(here, name, t, dtype, n=None):
     raise ValueError("%s must be a contiguous %s tensor%s" % (name, dtype, "" if n is None else " of %d values" % n))
 
 
-def _ints(here, *checks):
-    """(name, tensor, values) each: contiguous int32 on the current GPU."""
-    import torch
-    i32 = torch.int32
+def _ints(here, i32, *checks):
+    """(name, tensor, values) each: contiguous int32 on GPU ``here``."""
     for name, t, n in checks:
         if t.dtype is not i32 or t.numel() != n or t.get_device() != here or not t.is_contiguous():
             _refuse(here, name, t, "int32", n)
 
 
 def _rows(here, name, t, heads, dim, dtypes):
-    """[T][heads][dim] with dense rows; returns the elements from one token to the next."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or t.dtype not in dtypes:
+    """[T][heads][dim] with dense rows on GPU ``here``; returns the elements from one token to the next."""
+    if t.dim() != 3 or t.dtype not in dtypes:
         raise ValueError("%s must be [T][%d][%d] of %s" % (name, heads, dim, " or ".join(str(d) for d in dtypes)))
-    if (heads > 1 and stride[1] != dim) or stride[2] != 1:
+    (n, h, d), (s0, s1, s2) = t.shape, t.stride()
+    if h != heads or d != dim:
+        raise ValueError("%s must be [T][%d][%d]" % (name, heads, dim))
+    if (heads > 1 and s1 != dim) or s2 != 1:
         raise ValueError("%s: one token's heads must be dense" % name)
     if t.get_device() != here:
         _refuse(here, name, t, "")
-    return stride[0] if shape[0] > 1 else max(stride[0], heads * dim)
+    return s0 if n > 1 else max(s0, heads * dim)
+
+
+def _queue(stream, here):
+    """The raw handle of ``stream``, or of the current one (0: the default stream)."""
+    if stream is not None:
+        return int(stream)
+    import torch
+    return torch._C._cuda_getCurrentRawStream(here)
 
 
 class KvCache:
@@ -257,13 +271,13 @@ class KvCache:
             if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
                 raise ValueError("codes are contiguous uint8 tensors of one shape, scales contiguous fp32 [n_blocks][n_heads]")
         for t in (k_codes, v_codes, k_scale, v_scale):
-            if t.get_device() != _here():
-                _refuse(_here(), "the cache", t, "")
+            _gpu("the cache", t)
         self.tensors = dict(k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale)
         self.fmt, self.block_size, self.n_heads, self.head_dim = fmt, block_size, k_codes.shape[1], head_dim
         self.n_blocks = k_codes.shape[0]
         self.desc = MbdKvCache(fmt, block_size, self.n_heads, head_dim, self.n_blocks, k_codes.data_ptr(), v_codes.data_ptr(),
                                k_scale.data_ptr(), v_scale.data_ptr())
+        self._ref = ctypes.byref(self.desc)
 
     @classmethod
     def empty(cls, fmt: int, n_blocks: int, n_heads: int, head_dim: int, block_size: int, device="cuda"):
@@ -273,7 +287,7 @@ class KvCache:
         return cls(fmt, block_size, head_dim, *codes, *scales)
 
     def ref(self):
-        return ctypes.byref(self.desc)
+        return self._ref
 
 
 class KvPool:
@@ -282,53 +296,60 @@ class KvPool:
     def __init__(self, block_size: int, block_table, free_blocks):
         if block_table.dim() != 2 or free_blocks.dim() != 1:
             raise ValueError("block_table must be [n_seqs][max_blocks], free_blocks [n_blocks]")
-        _ints(_here(), ("block_table", block_table, block_table.numel()), ("free_blocks", free_blocks, free_blocks.numel()))
+        import torch
+        _ints(_gpu("block_table", block_table), torch.int32, ("block_table", block_table, block_table.numel()),
+              ("free_blocks", free_blocks, free_blocks.numel()))
         self.block_table, self.free_blocks, self.block_size = block_table, free_blocks, block_size
         self.n_seqs, self.max_blocks = block_table.shape
         self.desc = MbdKvPool(self.n_seqs, block_size, self.max_blocks, free_blocks.shape[0], block_table.data_ptr(),
                               free_blocks.data_ptr())
+        self._ref = ctypes.byref(self.desc)
 
     def ref(self):
-        return ctypes.byref(self.desc)
+        return self._ref
 
 
 def mbd_kv_slots(pool: KvPool, new_tokens, lens, held, n_free, seq_start, slots, positions, lens_out, held_out, n_free_out,
                  status, stream=None) -> None:
     """One step's block tables, slot map and ragged starts from request lengths; slots has
     one value for each row of the step's token batch, positions may be None."""
-    n, T, here = pool.n_seqs, slots.numel(), _here()
-    _ints(here, ("new_tokens", new_tokens, n), ("lens", lens, n), ("held", held, n), ("n_free", n_free, 1), ("seq_start", seq_start, n + 1),
+    import torch
+    n, T, here, i32 = pool.n_seqs, slots.numel(), _gpu("slots", slots), torch.int32
+    _ints(here, i32, ("new_tokens", new_tokens, n), ("lens", lens, n), ("held", held, n), ("n_free", n_free, 1), ("seq_start", seq_start, n + 1),
           ("slots", slots, T), ("lens_out", lens_out, n), ("held_out", held_out, n), ("n_free_out", n_free_out, 1), ("status", status, n))
     if positions is not None:
-        _ints(here, ("positions", positions, T))
-    check(lib().mbd_kv_slots(pool.ref(), new_tokens.data_ptr(), lens.data_ptr(), held.data_ptr(), n_free.data_ptr(), T, seq_start.data_ptr(),
-                             slots.data_ptr(), None if positions is None else positions.data_ptr(), lens_out.data_ptr(),
-                             held_out.data_ptr(), n_free_out.data_ptr(), status.data_ptr(), _stream(stream)), "mbd_kv_slots")
+        _ints(here, i32, ("positions", positions, T))
+    st = lib().mbd_kv_slots(pool._ref, new_tokens.data_ptr(), lens.data_ptr(), held.data_ptr(), n_free.data_ptr(), T, seq_start.data_ptr(),
+                            slots.data_ptr(), None if positions is None else positions.data_ptr(), lens_out.data_ptr(),
+                            held_out.data_ptr(), n_free_out.data_ptr(), status.data_ptr(), _queue(stream, here))
+    check(st, "mbd_kv_slots")
 
 
 def mbd_kv_append(cache: KvCache, k, v, slots, stream=None) -> None:
     """Quantise k, v [T][n_heads][head_dim] (bf16 or fp32; rows may be slices) into their slots."""
     import torch
-    here, heads, dim, T, dt = _here(), cache.n_heads, cache.head_dim, k.shape[0], k.dtype
+    here, heads, dim, T, dt = _gpu("k", k), cache.n_heads, cache.head_dim, k.shape[0], k.dtype
     ks, vs = _rows(here, "k", k, heads, dim, (torch.bfloat16, torch.float32)), _rows(here, "v", v, heads, dim, (dt,))
     if v.shape[0] != T:
         raise ValueError("k and v must have as many tokens")
-    _ints(here, ("slots", slots, T))
-    check(lib().mbd_kv_append(cache.ref(), k.data_ptr(), v.data_ptr(), MBD_BF16 if dt is torch.bfloat16 else MBD_F32, ks, vs, slots.data_ptr(),
-                              T, _stream(stream)), "mbd_kv_append")
+    _ints(here, torch.int32, ("slots", slots, T))
+    st = lib().mbd_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), MBD_BF16 if dt is torch.bfloat16 else MBD_F32, ks, vs, slots.data_ptr(), T,
+                             _queue(stream, here))
+    check(st, "mbd_kv_append")
 
 
 def mbd_kv_gather(cache: KvCache, slots, k_out, v_out, stream=None) -> None:
     """Dense keys and values [T][n_heads][head_dim] (bf16 or fp32) of the tokens in ``slots``."""
     import torch
-    here, heads, dim, T, dt = _here(), cache.n_heads, cache.head_dim, k_out.shape[0], k_out.dtype
+    here, heads, dim, T, dt = _gpu("k_out", k_out), cache.n_heads, cache.head_dim, k_out.shape[0], k_out.dtype
     _rows(here, "k_out", k_out, heads, dim, (torch.bfloat16, torch.float32))
     _rows(here, "v_out", v_out, heads, dim, (dt,))
     if v_out.shape[0] != T or not k_out.is_contiguous() or not v_out.is_contiguous():
         raise ValueError("k_out and v_out must be contiguous and alike")
-    _ints(here, ("slots", slots, T))
-    check(lib().mbd_kv_gather(cache.ref(), slots.data_ptr(), T, MBD_BF16 if dt is torch.bfloat16 else MBD_F32, k_out.data_ptr(),
-                              v_out.data_ptr(), _stream(stream)), "mbd_kv_gather")
+    _ints(here, torch.int32, ("slots", slots, T))
+    st = lib().mbd_kv_gather(cache._ref, slots.data_ptr(), T, MBD_BF16 if dt is torch.bfloat16 else MBD_F32, k_out.data_ptr(), v_out.data_ptr(),
+                             _queue(stream, here))
+    check(st, "mbd_kv_gather")
 
 
 def mbd_kv_attn_workspace_bytes(cache: KvCache, n_heads: int, n_seqs: int, max_new: int, max_blocks: int) -> int:
@@ -336,6 +357,9 @@ def mbd_kv_attn_workspace_bytes(cache: KvCache, n_heads: int, n_seqs: int, max_n
     check(lib().mbd_kv_attn_workspace_bytes(cache.ref(), n_heads, n_seqs, max_new, max_blocks, ctypes.byref(b)),
           "mbd_kv_attn_workspace_bytes")
     return int(b.value)
+
+
+_ATTN_ARGS = struct.Struct("@6i2fPqq")                 # MbdKvAttnArgs, in the machine's own layout
 
 
 def mbd_kv_attn(cache: KvCache, q, seq_start, lens, block_table, out, ws=None, max_new: int = 1, scale: float | None = None,
@@ -346,22 +370,23 @@ def mbd_kv_attn(cache: KvCache, q, seq_start, lens, block_table, out, ws=None, m
     import torch
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q must be [T][n_heads][head_dim], block_table [n_seqs][max_blocks]")
-    here, (T, heads, dim), (n, width) = _here(), q.shape, block_table.shape
+    here, (T, heads, dim), (n, width) = _gpu("q", q), q.shape, block_table.shape
     qs = _rows(here, "q", q, heads, cache.head_dim, (torch.bfloat16,))
     outs = _rows(here, "out", out, heads, dim, (torch.bfloat16,))
     if out.shape[0] != T:
         raise ValueError("out must have as many rows as q")
-    _ints(here, ("block_table", block_table, n * width), ("lens", lens, n), ("seq_start", seq_start, n + 1))
+    _ints(here, torch.int32, ("block_table", block_table, n * width), ("lens", lens, n), ("seq_start", seq_start, n + 1))
     for name, t, size in (("lse", lse, T * heads), ("slopes", slopes, heads)):
         if t is not None and (t.dtype is not torch.float32 or t.numel() != size or t.get_device() != here or not t.is_contiguous()):
             _refuse(here, name, t, "fp32", size)
     if ws is not None and (ws.get_device() != here or not ws.is_contiguous()):
         _refuse(here, "ws", ws, "")
-    args = MbdKvAttnArgs(heads, n, width, T, max_new, window, dim ** -0.5 if scale is None else scale, softcap,
-                         None if slopes is None else slopes.data_ptr(), qs, outs)
-    check(lib().mbd_kv_attn(cache.ref(), ctypes.byref(args), q.data_ptr(), seq_start.data_ptr(), lens.data_ptr(), block_table.data_ptr(),
-                            out.data_ptr(), None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
-                            0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), "mbd_kv_attn")
+    args = _ATTN_ARGS.pack(heads, n, width, T, max_new, window, dim ** -0.5 if scale is None else scale, softcap,
+                           0 if slopes is None else slopes.data_ptr(), qs, outs)
+    st = lib().mbd_kv_attn(cache._ref, args, q.data_ptr(), seq_start.data_ptr(), lens.data_ptr(), block_table.data_ptr(), out.data_ptr(),
+                           None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
+                           _queue(stream, here))
+    check(st, "mbd_kv_attn")
 
 
 def mbd_probe_stream_read(src, sink, blocks: int, threads: int, stream=None) -> None:

@@ -88,7 +88,8 @@ SIGNATURES = {
                                 c_void_p]),
     "mbd_kv_gather": (c_int32, [POINTER(MbdKvCache), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p]),
     "mbd_kv_attn_workspace_bytes": (c_int32, [POINTER(MbdKvCache), c_int32, c_int32, c_int32, c_int32, POINTER(c_uint64)]),
-    "mbd_kv_attn": (c_int32, [POINTER(MbdKvCache), POINTER(MbdKvAttnArgs)] + [c_void_p] * 7 + [c_uint64, c_void_p]),
+    # the arguments by address: the binding packs an MbdKvAttnArgs as bytes
+    "mbd_kv_attn": (c_int32, [POINTER(MbdKvCache), c_void_p] + [c_void_p] * 7 + [c_uint64, c_void_p]),
     "mbd_probe_stream_read": (c_int32, [c_void_p, c_uint64, c_void_p, c_int32, c_int32, c_void_p]),
     "mbd_status_str": (c_char_p, [c_int32]),
     "mbd_last_error": (c_char_p, []),

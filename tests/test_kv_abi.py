@@ -138,3 +138,12 @@ def test_binding_checks():
         mbd.KvPool(16, torch.zeros((2, 4), dtype=torch.int32), torch.zeros(9, dtype=torch.int32))
     with pytest.raises(ValueError, match="n_seqs"):
         mbd.KvPool(16, torch.zeros(4, dtype=torch.int32), torch.zeros(9, dtype=torch.int32))
+
+
+def test_packed_attention_arguments():
+    """The bytes that the binding packs are an mbd_kv_attn_args."""
+    vals = (8, 2, 4, 2, 1, 3, 0.5, 2.0, 0x1230, 1024, 2048)
+    raw = mbd._ATTN_ARGS.pack(*vals)
+    a = mbd.MbdKvAttnArgs.from_buffer_copy(raw)
+    assert len(raw) == ctypes.sizeof(mbd.MbdKvAttnArgs)
+    assert tuple(getattr(a, n) for n, _ in mbd.MbdKvAttnArgs._fields_) == vals
