@@ -456,7 +456,7 @@ typedef struct {
  * overwritten; may be NULL where that is 0.  Calls that share a workspace must not
  * overlap.  Errors: EINVAL, ESHAPE (T above 2^24, max_blocks * block_size above 2^30,
  * n_seqs * max_blocks * block_size / 16 of 2^31 or more, KV heads times tiles of query
- * rows above 65535), EALIGN, EHIP. */
+ * rows of 2^24 or more), EALIGN, EHIP. */
 mbd_status mbd_kv_attn_workspace_bytes(const mbd_kv_cache* cache, int32_t n_heads, int32_t n_seqs,
                                        int32_t max_new, int32_t max_blocks, uint64_t* bytes);
 mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, const uint16_t* q,

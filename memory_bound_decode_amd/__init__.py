@@ -246,7 +246,7 @@ def _rows(here, name, t, heads, dim, dtypes):
         raise ValueError("%s: one token's heads must be dense" % name)
     if t.get_device() != here:
         _refuse(here, name, t, "")
-    return s0 if n > 1 else max(s0, heads * dim)
+    return s0 if n > 1 else heads * dim
 
 
 def _queue(stream, here):

@@ -30,9 +30,11 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// A request that is cut into parts, for what joins them; parts = 0 behind the last.
+// A tile of a request's query rows whose tokens are cut into parts, for what joins them;
+// parts = 0 behind the last.
 struct Split {
-    int32_t parts, slot, row0, rows;     // slot: of its first partial result
+    int32_t parts, slot, stride;         // slot of its first partial result, slots from one to the next
+    int32_t row0, r0, rows;              // the request's first row of q; the tile's first row, and how many
 };
 
 struct AttnArgs {
@@ -46,8 +48,8 @@ struct AttnArgs {
     const float* slopes;
     int64_t q_stride, out_stride;
     uint32_t per_group;                  // ceil(2^32 / group)
-    int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, places, n_splits;
-    bool by_seq;
+    int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, row_shift, places, unit, n_splits;
+    bool split;                          // whether requests may be cut into parts
     float to_score, softcap;             // product to score in the log2 domain (or over the cap); the cap there
 };
 
@@ -91,85 +93,96 @@ __device__ __forceinline__ int wave_scan(int v) {
     return plus_dpp<0x143, 0xc>(v);    // row_bcast 31 into rows 2 and 3
 }
 
-// The lengths are known on the device alone, so every wave cuts the work up itself: all
-// tiles over the places that the chip has for workgroups is a chunk, a request is cut into
-// ceil(tiles / chunk) even parts, and a workgroup's part follows from the prefix sums of
-// their counts.  One round of workgroups: two or four rounds of shorter ones, which end
-// more evenly, lost more on the way to their first product (32 requests of 32768 tokens
-// 201 and 207 us against 193, one of 131072 64 and 77 against 57).
+// The lengths are known on the device alone, so every wave cuts the work up itself.  The
+// work of a request is its tiles of tokens times its tiles of query rows; all of it over the
+// places that the chip has for a head's workgroups is a chunk of tokens, a request is cut into
+// ceil(tokens / chunk) even parts, and the workgroup's (request, part, row tile) follows from
+// the prefix sums of their counts.  One round of workgroups: two or four rounds of shorter
+// ones, which end more evenly, lost more on the way to their first product (32 requests of
+// 32768 tokens 201 and 207 us against 193, one of 131072 64 and 77 against 57).
 __device__ __forceinline__ int tiles_of(const Seq& s) { return s.n_new < 1 ? 0 : max(s.hi - s.lo, 1); }
+__device__ __forceinline__ int row_tiles_of(const AttnArgs& a, const Seq& s) { return (s.rows + (1 << a.row_shift) - 1) >> a.row_shift; }
 
-// A workgroup's part of a request, or (by_seq) all of one.
 struct Item {
-    int32_t seq, part, parts, slot;      // slot: of the request's first partial result
-    int32_t split;                       // split requests before it
+    int32_t seq, parts, index;           // index: among the request's, row tiles fastest
+    int32_t slot, split;                 // of the request's first partial result; split row tiles before it
 };
 
 __device__ __forceinline__ int32_t even_part(int tiles, int parts) {     // tiles of a part, whole steps
     return ((tiles - 1) / parts + kStep) / kStep * kStep;
 }
 
-// Item `want` (seq is -1 if there is none), its request, and how many requests are split.
+// Item `want` (seq is -1 if there is none), its request, and how many row tiles are split.
 __device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, Seq* sq, int* splits) {
     const int lane = threadIdx.x & 63;
     const int per = (a.n_seqs + 63) / 64;
     const int i0 = lane * per, i1 = min(i0 + per, a.n_seqs);
     const Seq mine = load_seq(a, min(i0, a.n_seqs - 1));        // up to 64 requests: one a lane, read once
-    const int n0 = i0 < a.n_seqs ? tiles_of(mine) : 0;
-    int tiles = n0, used = n0 > 0;
+    const int n0 = i0 < a.n_seqs ? tiles_of(mine) : 0, rt0 = n0 ? row_tiles_of(a, mine) : 0;
+    // in units that keep the sum within 32 bits, rounded up
+    auto work_of = [&](int n, int rt) { return int((uint64_t(uint32_t(n)) * uint32_t(rt) + (uint64_t(1) << a.unit) - 1) >> a.unit); };
+    int work = work_of(n0, rt0), used = rt0;
     for (int i = i0 + 1; i < i1; ++i) {
-        const int n = tiles_of(load_seq(a, i));
-        tiles += n;
-        used += n > 0;
+        const Seq s = load_seq(a, i);
+        const int n = tiles_of(s), rt = n ? row_tiles_of(a, s) : 0;
+        work += work_of(n, rt);
+        used += rt;
     }
-    tiles = max(__builtin_amdgcn_readlane(wave_scan(tiles), 63), 1);
+    work = max(__builtin_amdgcn_readlane(wave_scan(work), 63), 1);
     used = __builtin_amdgcn_readlane(wave_scan(used), 63);
-    // ceil(tiles_i / chunk) add up to between tiles / chunk and that + used: the smallest
-    // of three chunks whose parts fit the places, of which the last always does (unless
-    // there are more requests than places: those stay whole)
-    uint32_t chunk = 0;
-    int items = 0, slots = 0, cut = 0, p0 = 0;     // parts, those of split requests, split requests
+    // With chunks of work / room, the parts times row tiles add up to between room and
+    // room + used: the smallest of three chunks whose items fit the places, of which the
+    // last always does, unless there are as many row tiles as places (then only what is
+    // longer than a place's share is cut).  No chunk is below work / places, so the items
+    // of split requests number less than twice the places.
+    uint32_t chunk = 0x7fffffff;
+    int items = 0, slots = 0, cut = 0, p0 = 0;     // items, those of split requests, split row tiles
     auto parts_of = [&](int n) { return int((uint32_t(n) + chunk - 1) / chunk); };
 #pragma unroll 1
     for (int tries = 0; tries < 3; ++tries) {
-        const int room = a.places - (tries * used + 1) / 2;
-        chunk = max(room > 0 ? uint32_t(tiles - 1) / uint32_t(room) + 1 : uint32_t(tiles), uint32_t(kMinPart));
-        p0 = parts_of(n0);
-        items = p0;
-        cut = p0 > 1;
-        slots = p0 > 1 ? p0 : 0;
-        for (int i = i0 + 1; i < i1; ++i) {
-            const int p = parts_of(tiles_of(load_seq(a, i)));
-            items += p;
-            cut += p > 1;
-            slots += p > 1 ? p : 0;
+        if (a.split) {
+            const int room = a.places - (tries * used + 1) / 2;
+            const uint64_t share = uint64_t(uint32_t(work - 1) / uint32_t(room > 0 ? room : a.places) + 1) << a.unit;
+            chunk = uint32_t(min(max(share, uint64_t(kMinPart)), uint64_t(1) << 30));
         }
-        if (__builtin_amdgcn_readlane(wave_scan(items), 63) <= a.places) break;
+        p0 = parts_of(n0);
+        items = p0 * rt0;
+        cut = p0 > 1 ? rt0 : 0;
+        slots = p0 > 1 ? items : 0;
+        for (int i = i0 + 1; i < i1; ++i) {
+            const Seq s = load_seq(a, i);
+            const int n = tiles_of(s), p = parts_of(n), rt = n ? row_tiles_of(a, s) : 0;
+            items += p * rt;
+            cut += p > 1 ? rt : 0;
+            slots += p > 1 ? p * rt : 0;
+        }
+        if (!a.split || __builtin_amdgcn_readlane(wave_scan(items), 63) <= a.places) break;
     }
     const int cut_end = wave_scan(cut);
     int item0 = wave_scan(items) - items, slot0 = wave_scan(slots) - slots, cut0 = cut_end - cut;
     Item it{-1, 0, 0, 0, 0};
     Seq s = mine;
-    auto look = [&](int i, int p, const Seq& is) {
-        if (want >= item0 && want < item0 + p) {
-            it = {i, want - item0, p, slot0, cut0};
+    auto look = [&](int i, int p, int rt, const Seq& is) {
+        if (want >= item0 && want < item0 + p * rt) {
+            it = {i, p, want - item0, slot0, cut0};
             s = is;
         }
-        item0 += p;
-        cut0 += p > 1;
-        slot0 += p > 1 ? p : 0;
+        item0 += p * rt;
+        cut0 += p > 1 ? rt : 0;
+        slot0 += p > 1 ? p * rt : 0;
     };
-    if (i0 < a.n_seqs) look(i0, p0, mine);
+    look(i0, p0, rt0, mine);
     for (int i = i0 + 1; i < i1; ++i) {
         const Seq is = load_seq(a, i);
-        look(i, parts_of(tiles_of(is)), is);
+        const int n = tiles_of(is);
+        look(i, parts_of(n), n ? row_tiles_of(a, is) : 0, is);
     }
     const uint64_t who = __ballot(it.seq >= 0);
     const int l = who ? __builtin_ctzll(who) : 0;
     auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
     *sq = {of(s.row0), of(s.n_new), of(s.rows), of(s.p0), of(s.lo), of(s.hi), of(s.len)};
     *splits = __builtin_amdgcn_readlane(cut_end, 63);
-    return {who ? of(it.seq) : -1, of(it.part), of(it.parts), of(it.slot), of(it.split)};
+    return {who ? of(it.seq) : -1, of(it.parts), of(it.index), of(it.slot), of(it.split)};
 }
 
 // Maximum over the four lanes of a query row (lane % 16): the rows of 16 lanes swap places.
@@ -245,37 +258,27 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, n = lane & 15;
     const int in_block = (1 << a.shift) - 1;
-    // By request: heads side by side, so that a head's row tiles share an XCD's L2 and every
-    // XCD has all requests; a request's last rows, which see most, first.
-    int head = blockIdx.x, r0 = (gridDim.y - 1 - blockIdx.y) * ROWS;
-    Item it{int32_t(blockIdx.z), 0, 1, 0, 0};
+    // Heads side by side: workgroups go round the XCDs, so that of 8 heads each has an XCD, in
+    // whose L2 a request's row tiles find each other's codes.
+    const int want = blockIdx.x / uint32_t(a.n_kv), head = blockIdx.x - want * a.n_kv;
     Seq sq;
-    if (a.by_seq) sq = load_seq(a, it.seq);
-    else {
-        head = blockIdx.y % a.n_kv;
-        r0 = blockIdx.y / a.n_kv * ROWS;
-        int splits;
-        it = find_item(a, blockIdx.x, &sq, &splits);
-        if (blockIdx.y == 0 && threadIdx.x == 0) {
-            const int w = blockIdx.x;
-            if (w >= splits && w < a.n_splits) a.splits[w] = Split{0, 0, 0, 0};
-            if (it.seq >= 0 && it.parts > 1 && it.part == 0) a.splits[it.split] = Split{it.parts, it.slot, sq.row0, sq.rows};
-        }
-    }
-    if (it.seq < 0 || r0 >= sq.rows) return;
-    // the same in all lanes, which the compiler cannot see of loaded values: scalar registers
-    auto same = [](int32_t& v) { v = __builtin_amdgcn_readfirstlane(v); };
-    same(sq.row0), same(sq.n_new), same(sq.rows), same(sq.p0), same(sq.lo), same(sq.hi), same(sq.len);
-    same(it.seq), same(it.part), same(it.parts), same(it.slot);
+    int splits;
+    const Item it = find_item(a, want, &sq, &splits);
+    if (head == 0 && threadIdx.x == 0 && want >= splits && want < a.n_splits) a.splits[want] = Split{0, 0, 0, 0, 0, 0};
+    if (it.seq < 0) return;
+    const int row_tiles = row_tiles_of(a, sq), part = it.index / row_tiles;
+    const int row_tile = row_tiles - 1 - (it.index - part * row_tiles);       // the last rows, which see most, first
+    const int r0 = row_tile * ROWS, slot = it.slot + row_tile;
     const int rows = min(ROWS, sq.rows - r0);
     // what the first and the last row see bounds what any row sees
     const int pos_first = sq.p0 + token_of(a, r0), pos_last = sq.p0 + token_of(a, r0 + rows - 1);
     const int all_end = pos_first + 1, all_begin = a.window > 0 ? max(pos_last, 0) - a.window + 1 : 0;
     int t0 = sq.lo, t1 = min(sq.hi, (max(pos_last + 1, 0) + kTok - 1) / kTok);
     if (it.parts > 1) {
-        const int part = even_part(tiles_of(sq), it.parts);
-        t0 += it.part * part;
-        t1 = min(t1, t0 + part);
+        const int size = even_part(tiles_of(sq), it.parts);
+        t0 += part * size;
+        t1 = min(t1, t0 + size);
+        if (head == 0 && threadIdx.x == 0 && part == 0) a.splits[it.split + row_tile] = Split{it.parts, slot, row_tiles, sq.row0, r0, rows};
     }
     if (a.window > 0) t0 = max(t0, max(max(pos_first, 0) - a.window + 1, 0) / kTok);
 
@@ -473,9 +476,6 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
         *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
         if (d == 0 && a.lse) a.lse[int64_t(sq.row0 + j) * (a.n_kv * a.group) + qh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
     };
-    auto row_of = [&](int part) { return (int64_t(it.slot + part) * gridDim.y + blockIdx.y) * ROWS; };
-
-
     // Join the waves: a common maximum a row, then sums slab by slab through LDS.
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -520,7 +520,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
             if (it.parts == 1) {
                 put(r, 64 * c + d, o, m, l);
             } else {
-                const int64_t to = row_of(it.part) + r;
+                const int64_t to = ((slot + int64_t(part) * row_tiles) * a.n_kv + head) * ROWS + r;
                 *reinterpret_cast<f32x4*>(a.part_o + to * D + 64 * c + d) = o;
                 if (c == 0 && d == 0) *reinterpret_cast<f32x2*>(a.part_ml + to * 2) = f32x2{m, l};
             }
@@ -528,8 +528,8 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
     }
 }
 
-// The parts of the split requests: a workgroup for each four query rows of a request and
-// head, WAVES waves a row; lanes over channels, waves over parts.
+// The parts of the split row tiles: a workgroup for each four query rows of a tile and head,
+// WAVES waves a row; lanes over channels, waves over parts.
 // A second launch: joining in the last workgroup to arrive needs partial results that
 // pass the XCDs' L2s and a counter, which took longer (one request of 2048 tokens 10.5
 // against 8.9 us, one of 131072 84 against 57).
@@ -541,11 +541,11 @@ __global__ __launch_bounds__(64 * kJoinRows * WAVES) void join_kernel(AttnArgs a
     __shared__ float joined[kJoinRows][WAVES][D], top[kJoinRows][WAVES], sum[kJoinRows][WAVES];
     const int lane = threadIdx.x & 63, row = threadIdx.x / (64 * WAVES), wave = (threadIdx.x >> 6) % WAVES;
     const Split sp = a.splits[blockIdx.x];
-    const int head = blockIdx.y % a.n_kv, in_tile = blockIdx.z * kJoinRows + row;
-    const int r = blockIdx.y / a.n_kv * rows_of_tile + in_tile;
-    if (sp.parts == 0 || r - row >= sp.rows) return;
-    const bool mine = in_tile < rows_of_tile && r < sp.rows;
-    auto row_of = [&](int p) { return (int64_t(sp.slot + p) * gridDim.y + blockIdx.y) * rows_of_tile + (mine ? in_tile : 0); };
+    const int head = blockIdx.y, in_tile = blockIdx.z * kJoinRows + row;
+    if (sp.parts == 0 || in_tile - row >= sp.rows) return;
+    const bool mine = in_tile < sp.rows;
+    const int r = sp.r0 + in_tile;
+    auto row_of = [&](int p) { return ((sp.slot + int64_t(p) * sp.stride) * a.n_kv + head) * rows_of_tile + (mine ? in_tile : 0); };
     float m = -INFINITY, l = 0.f, o[DQ] = {};
     for (int p0 = wave; p0 < sp.parts; p0 += kJoinAhead * WAVES) {
         f32x2 ml[kJoinAhead];
@@ -613,11 +613,11 @@ __global__ __launch_bounds__(64 * kJoinRows * WAVES) void join_kernel(AttnArgs a
 
 // How a call is laid out; the same for the workspace's size and the launch.
 struct Plan {
-    int32_t group, nt, row_tiles, places;
-    bool by_seq;
-    uint32_t grid_x, grid_y;
-    uint64_t parts;          // partial results, of nt * 16 rows for every grid_y
-    uint64_t splits;         // requests that they can come from
+    int32_t group, nt, row_tiles, places, unit;
+    bool split;
+    int64_t longest;         // parts of a request at most
+    uint64_t parts;          // partial results of a head, of nt * 16 rows
+    uint64_t splits;         // row tiles that they can come from
     uint64_t bytes;
 };
 
@@ -634,30 +634,28 @@ static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs
     const int32_t rows = max_new * p->group;
     p->nt = rows <= 16 ? 1 : 2;
     p->row_tiles = (rows + 16 * p->nt - 1) / (16 * p->nt);
-    const int64_t y = int64_t(c->n_heads) * p->row_tiles;
-    if (y > 65535) return fail(MBD_ESHAPE, "KV heads times query row tiles above 65535");
-    p->grid_y = uint32_t(y);
-    const int64_t room = kCus * per_cu(c->head_dim / 64, p->nt);
-    const int64_t longest = (seq_tiles + kMinPart - 1) / kMinPart;         // parts of one request at most
-    p->places = int32_t(std::max<int64_t>(1, room / y));
-    p->by_seq = longest < 2 || p->places < 2 || (p->row_tiles > 1 && y * n_seqs >= room);
-    p->grid_x = uint32_t(p->by_seq ? n_seqs : std::min<int64_t>(std::max(p->places, n_seqs), n_seqs * longest));
-    p->parts = p->by_seq ? 0 : std::min<int64_t>(p->places, p->grid_x);    // more requests than places: none is split
-    p->splits = std::min<int64_t>(n_seqs, p->parts / 2);
-    p->bytes = p->parts * p->grid_y * (16u * p->nt) * (c->head_dim + 2) * sizeof(float) + p->splits * sizeof(Split);
+    const int64_t tiles = int64_t(n_seqs) * p->row_tiles;                  // of query rows
+    p->unit = 0;
+    while (((seq_tiles * p->row_tiles) >> p->unit) + 1 >= (int64_t(1) << 31) / n_seqs) ++p->unit;
+    p->places = int32_t(std::max<int64_t>(1, kCus * per_cu(c->head_dim / 64, p->nt) / c->n_heads));
+    p->longest = (seq_tiles + kMinPart - 1) / kMinPart;
+    p->split = p->longest > 1 && p->places > 1;
+    p->parts = p->split ? std::min<int64_t>(2 * p->places, tiles * p->longest) : 0;
+    p->splits = std::min<int64_t>(p->parts / 2, tiles);
+    p->bytes = p->parts * c->n_heads * (16u * p->nt) * (c->head_dim + 2) * sizeof(float) + p->splits * sizeof(Split);
     return MBD_OK;
 }
 
 template <bool E4M3, int DQ, int NT>
-static void launch(const AttnArgs& a, const Plan& p, bool ext, hipStream_t s) {
-    const dim3 grid = p.by_seq ? dim3(a.n_kv, p.row_tiles, a.n_seqs) : dim3(p.grid_x, p.grid_y), block(64 * kWaves);
+static void launch(const AttnArgs& a, const Plan& p, int64_t items, bool ext, hipStream_t s) {
+    const dim3 grid(unsigned(items) * unsigned(a.n_kv)), block(64 * kWaves);
     if (ext) hipLaunchKernelGGL((attn_kernel<E4M3, DQ, NT, true>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((attn_kernel<E4M3, DQ, NT, false>), grid, block, 0, s, a);
-    if (p.parts) {
+    if (a.n_splits) {
         const int rows = std::min(16 * NT, a.max_new * a.group);
-        const dim3 joins(unsigned(p.splits), p.grid_y, unsigned((rows + kJoinRows - 1) / kJoinRows));
-        // few requests can have many parts each: more waves over them
-        if (p.parts > 8 * p.splits)
+        const dim3 joins(unsigned(a.n_splits), unsigned(a.n_kv), unsigned((rows + kJoinRows - 1) / kJoinRows));
+        // few row tiles can have many parts each: more waves over them
+        if (a.n_seqs * int64_t(p.row_tiles) * 8 < p.places)
             hipLaunchKernelGGL((join_kernel<DQ, 4>), joins, dim3(64 * kJoinRows * 4), 0, s, a, 16 * NT);
         else
             hipLaunchKernelGGL((join_kernel<DQ, 1>), joins, dim3(64 * kJoinRows), 0, s, a, 16 * NT);
@@ -665,17 +663,17 @@ static void launch(const AttnArgs& a, const Plan& p, bool ext, hipStream_t s) {
 }
 
 template <bool E4M3, int DQ>
-static void launch_rows(const AttnArgs& a, const Plan& p, bool ext, hipStream_t s) {
-    if (p.nt == 1) return launch<E4M3, DQ, 1>(a, p, ext, s);
-    launch<E4M3, DQ, 2>(a, p, ext, s);
+static void launch_rows(const AttnArgs& a, const Plan& p, int64_t items, bool ext, hipStream_t s) {
+    if (p.nt == 1) return launch<E4M3, DQ, 1>(a, p, items, ext, s);
+    launch<E4M3, DQ, 2>(a, p, items, ext, s);
 }
 
 template <bool E4M3>
-static void launch_dim(const AttnArgs& a, const Plan& p, int dq, bool ext, hipStream_t s) {
-    if (dq == 1) launch_rows<E4M3, 1>(a, p, ext, s);
-    else if (dq == 2) launch_rows<E4M3, 2>(a, p, ext, s);
-    else if (dq == 3) launch_rows<E4M3, 3>(a, p, ext, s);
-    else launch_rows<E4M3, 4>(a, p, ext, s);
+static void launch_dim(const AttnArgs& a, const Plan& p, int64_t items, int dq, bool ext, hipStream_t s) {
+    if (dq == 1) launch_rows<E4M3, 1>(a, p, items, ext, s);
+    else if (dq == 2) launch_rows<E4M3, 2>(a, p, items, ext, s);
+    else if (dq == 3) launch_rows<E4M3, 3>(a, p, items, ext, s);
+    else launch_rows<E4M3, 4>(a, p, items, ext, s);
 }
 
 }  // namespace kv
@@ -716,6 +714,10 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     if (!kv::aligned(seq_start, 4) || !kv::aligned(lens, 4) || !kv::aligned(block_table, 4) || !kv::aligned(lse, 4) ||
         !kv::aligned(args->slopes, 4))
         return fail(MBD_EALIGN, "int32 and fp32 arrays must be 4-byte aligned");
+    // a head's items: places, and the row tiles that the sums may pass them by; T bounds those
+    const int64_t used = std::min<int64_t>(int64_t(args->n_seqs) * p.row_tiles, int64_t(args->T) * p.group / (16 * p.nt) + args->n_seqs);
+    const int64_t items = p.split ? std::min(p.places + used, used * p.longest) : used;
+    if (items * cache->n_heads >= (int64_t(1) << 24)) return fail(MBD_ESHAPE, "KV heads times tiles of query rows is 2^24 or more");
     if (args->T == 0) return MBD_OK;
     if (!q || !out) return fail(MBD_EINVAL, "NULL argument");
     if (!kv::aligned(q, 16) || !kv::aligned(out, 16)) return fail(MBD_EALIGN, "q and out must be 16-byte aligned");
@@ -735,8 +737,8 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     a.out = out;
     a.lse = lse;
     a.part_o = static_cast<float*>(ws);
-    a.part_ml = a.part_o + p.parts * p.grid_y * (16u * p.nt) * cache->head_dim;
-    a.splits = reinterpret_cast<kv::Split*>(a.part_ml + p.parts * p.grid_y * (16u * p.nt) * 2);
+    a.part_ml = a.part_o + p.parts * cache->n_heads * (16u * p.nt) * cache->head_dim;
+    a.splits = reinterpret_cast<kv::Split*>(a.part_ml + p.parts * cache->n_heads * (16u * p.nt) * 2);
     a.slopes = args->slopes;
     a.q_stride = args->q_stride;
     a.out_stride = args->out_stride;
@@ -750,15 +752,17 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     a.n_kv = cache->n_heads;
     a.group = p.group;
     a.per_group = uint32_t(((uint64_t(1) << 32) + p.group - 1) / p.group);
+    a.row_shift = p.nt == 1 ? 4 : 5;
     a.places = p.places;
-    a.n_splits = int32_t(p.splits);
-    a.by_seq = p.by_seq;
+    a.unit = p.unit;
+    a.n_splits = int32_t(std::min<int64_t>(p.splits, used));
+    a.split = p.split;
     a.to_score = args->softcap > 0 ? args->scale / args->softcap : kv::kLog2e * args->scale;
     a.softcap = args->softcap * kv::kLog2e;
     const bool ext = a.window > 0 || args->softcap > 0 || args->slopes;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    if (cache->fmt == MBD_KV_E4M3) kv::launch_dim<true>(a, p, cache->head_dim / 64, ext, s);
-    else kv::launch_dim<false>(a, p, cache->head_dim / 64, ext, s);
+    if (cache->fmt == MBD_KV_E4M3) kv::launch_dim<true>(a, p, items, cache->head_dim / 64, ext, s);
+    else kv::launch_dim<false>(a, p, items, cache->head_dim / 64, ext, s);
     return hip_check("attention launch");
 }
 

@@ -450,6 +450,20 @@ def test_attn_split_long(dev, fmt):
     _run_attn(dev, fmt, 64, 16, 2, 2, [6001, 50], [5, 2], softcap=30.0, window=4000)
 
 
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+def test_attn_prompts_beside_decodes(dev, fmt):
+    """One call with prompt slices, verify steps and single tokens of long contexts: row tiles
+    and parts of requests in one row of work, some of it joined."""
+    _run_attn(dev, fmt, 128, 64, 2, 4, [260, 9000, 33, 5000, 64], [130, 1, 5, 1, 64], pad=2)
+    _run_attn(dev, fmt, 64, 16, 1, 40, [50, 3000, 3000], [9, 4, 1], window=2500)
+
+
+def test_attn_row_tiles_beyond_places(dev):
+    """More tiles of query rows than the chip has places for a head's workgroups, next to a
+    request that is still cut."""
+    _run_attn(dev, E4M3, 256, 32, 4, 16, [9000] + [24] * 70, [1] + [24] * 70)
+
+
 def test_attn_wide_cap_is_no_cap(dev):
     """A cap far above every score leaves them as they are: cap tanh(u / cap) = u - u^3 / (3 cap^2) + ..,
     so with |u| < 100 and a cap of 1e6 within 1e-6, far inside the tolerance of the uncapped call."""

@@ -83,7 +83,7 @@ BAD_ARGS = [(dict(n_heads=7), "ESHAPE"), (dict(n_heads=0), "ESHAPE"), (dict(n_se
             (dict(T=-1), "ESHAPE"), (dict(T=(1 << 24) + 1), "ESHAPE"), (dict(max_new=0), "ESHAPE"), (dict(max_new=1 << 22), "ESHAPE"),
             (dict(window=-1), "EINVAL"), (dict(scale=float("nan")), "EINVAL"), (dict(softcap=-1.0), "EINVAL"),
             (dict(softcap=float("inf")), "EINVAL"), (dict(softcap=float("nan")), "EINVAL"), (dict(n_heads=514), "ESHAPE"), (dict(q_stride=1016), "ESHAPE"), (dict(out_stride=1028), "ESHAPE"),
-            (dict(slopes=P + 2), "EALIGN")]
+            (dict(slopes=P + 2), "EALIGN"), (dict(n_heads=512, n_seqs=4096, max_new=1 << 15, T=1 << 24, q_stride=1 << 16, out_stride=1 << 16), "ESHAPE")]
 
 
 @pytest.mark.parametrize("change,status", BAD_ARGS)
@@ -122,7 +122,8 @@ def test_workspace_sizes(L):
     assert ask(8, 2, 0, 512) == ask(9, 2, 1, 512) == ask(8, 0, 1, 512) == ask(8, 2, 1, 0) == mbd.MBD_ESHAPE
     assert ask(8, 2, 1, 1) == mbd.MBD_OK and need.value == 0                        # 16 tokens: never split
     assert ask(8, 4096, 1, 32768) == mbd.MBD_OK and 0 < need.value < 1 << 30
-    assert ask(8, 1, 8192, 1024) == mbd.MBD_OK and need.value == 0                  # prompts alone fill the chip
+    assert ask(8, 64, 8192, 32768) == mbd.MBD_OK and need.value < 1 << 27           # does not grow with the rows
+    assert ask(8, 1, 1 << 21, 1 << 20) == mbd.MBD_OK and need.value < 1 << 27
 
 
 def test_binding_checks():
