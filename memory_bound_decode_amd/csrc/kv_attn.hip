@@ -48,7 +48,7 @@ struct AttnArgs {
     const float* slopes;
     int64_t q_stride, out_stride;
     uint32_t per_group;                  // ceil(2^32 / group)
-    int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, row_shift, places, unit, n_splits;
+    int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, row_shift, places, unit, n_splits, n_parts;
     bool split;                          // whether requests may be cut into parts
     float to_score, softcap;             // product to score in the log2 domain (or over the cap); the cap there
 };
@@ -247,7 +247,7 @@ __device__ __forceinline__ float lane_float(float v, int l) {
 
 // Workgroups a CU (waves a SIMD) that a variant's registers are held to: enough loads in
 // flight for the memory, and as many shares as there are places for them.
-constexpr int per_cu(int dq, int nt) { return nt == 1 ? (dq <= 2 ? 4 : dq == 3 ? 3 : 2) : (dq == 1 ? 3 : dq == 2 ? 2 : 1); }
+constexpr int per_cu(int dq, int nt) { return nt == 1 ? (dq <= 2 ? 4 : dq == 3 ? 3 : 2) : (dq == 1 ? 4 : dq == 2 ? 3 : 2); }
 
 // DQ = head_dim / 64, NT = tiles of 16 query rows, EXT: cap, window or distance bias.
 template <bool E4M3, int DQ, int NT, bool EXT>
@@ -293,7 +293,11 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
     };
     int32_t next_id = look_up(0);
 
-    bf16x8 qf[NT][2 * DQ];
+    // Two row tiles' queries would hold as many registers as a third wave a SIMD needs: they lie
+    // in LDS, in the lanes' order, and every wave reads them there.
+    constexpr bool kQueryLds = NT > 1;
+    __shared__ u32x4 queries[kQueryLds ? NT * 2 * DQ : 1][64];
+    u32x4 held[kQueryLds ? 1 : NT][kQueryLds ? 1 : 2 * DQ];
     int pos[NT];
     float slope[NT];
 #pragma unroll
@@ -307,11 +311,18 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
         const uint16_t* row = a.q + int64_t(sq.row0 + j) * a.q_stride + int64_t(qh) * D + 16 * g;
 #pragma unroll
         for (int c = 0; c < 2 * DQ; ++c) {
+            if (kQueryLds && c % kWaves != wave) continue;
             u32x4 w = {0, 0, 0, 0};
             if (in) w = *reinterpret_cast<const u32x4*>(row + 64 * (c / 2) + 8 * (c % 2));
-            qf[t][c] = __builtin_bit_cast(bf16x8, w);
+            if constexpr (kQueryLds) queries[t * 2 * DQ + c][lane] = w;
+            else held[t][c] = w;
         }
     }
+    if (kQueryLds) __syncthreads();
+    auto query = [&](int t, int c) {
+        if constexpr (kQueryLds) return __builtin_bit_cast(bf16x8, queries[t * 2 * DQ + c][lane]);
+        else return __builtin_bit_cast(bf16x8, held[t][c]);
+    };
 
     f32x4 acc[DQ][4][NT];
     float top[NT], sum[NT];          // base of the weights (log2 domain); this lane's share of their sum
@@ -345,8 +356,10 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
     };
 
     // The next step's keys are asked for as soon as this one's are used up, and so the values:
-    // each load has the other product and the softmax to arrive in, and needs no second buffer.
+    // each load has the other product and the softmax to arrive in.  A second buffer, asked for a
+    // whole step ahead, measured the same (prompt slices 55 us) and costs a wave a SIMD.
     auto step = [&](int tile, int l, int next_tile, bool more) {
+        if (kQueryLds) asm volatile("" ::: "memory");      // the queries are read again in each step
         f32x4 s[kStep][NT];
         bool whole = tile * kTok >= all_begin && (tile + kStep) * kTok <= all_end;
         float ks[kStep], vs[kStep];
@@ -368,7 +381,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
                     const bf16x8 kf = operand<E4M3>(kc[h][c][2 * e], kc[h][c][2 * e + 1]);
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
-                        s[h][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[t][2 * c + e], s[h][t], 0, 0, 0);
+                        s[h][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, query(t, 2 * c + e), s[h][t], 0, 0, 0);
                 }
         }
         keep_order();
@@ -542,7 +555,12 @@ __global__ __launch_bounds__(64 * kJoinRows * WAVES) void join_kernel(AttnArgs a
     const int lane = threadIdx.x & 63, row = threadIdx.x / (64 * WAVES), wave = (threadIdx.x >> 6) % WAVES;
     const Split sp = a.splits[blockIdx.x];
     const int head = blockIdx.y, in_tile = blockIdx.z * kJoinRows + row;
-    if (sp.parts == 0 || in_tile - row >= sp.rows) return;
+    // the attention kernel's own words, unless another call shares the workspace at the same time:
+    // then results are lost, but nothing is read or written out of range
+    if (sp.parts < 2 || in_tile - row >= sp.rows) return;
+    if (sp.rows > rows_of_tile || sp.slot < 0 || sp.stride < 1 || sp.slot + int64_t(sp.parts - 1) * sp.stride >= a.n_parts || sp.row0 < 0 ||
+        sp.r0 < 0 || sp.r0 >= (1 << 24) || int64_t(sp.row0) + token_of(a, sp.r0 + sp.rows - 1) >= a.T)
+        return;
     const bool mine = in_tile < sp.rows;
     const int r = sp.r0 + in_tile;
     auto row_of = [&](int p) { return ((sp.slot + int64_t(p) * sp.stride) * a.n_kv + head) * rows_of_tile + (mine ? in_tile : 0); };
@@ -756,6 +774,7 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     a.places = p.places;
     a.unit = p.unit;
     a.n_splits = int32_t(std::min<int64_t>(p.splits, used));
+    a.n_parts = int32_t(p.parts);
     a.split = p.split;
     a.to_score = args->softcap > 0 ? args->scale / args->softcap : kv::kLog2e * args->scale;
     a.softcap = args->softcap * kv::kLog2e;
