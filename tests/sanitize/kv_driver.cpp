@@ -65,6 +65,7 @@ void refusals() {
     expect(mbd_kv_attn_workspace_bytes(&c, 8, 2, 1, 4, nullptr), MBD_EINVAL, "workspace to nowhere");
     expect(mbd_kv_attn(nullptr, &a, q, i, i, i, q, nullptr, nullptr, 0, nullptr), MBD_EINVAL, "no cache");
     expect(mbd_kv_attn(&c, nullptr, q, i, i, i, q, nullptr, nullptr, 0, nullptr), MBD_EINVAL, "no arguments");
+    a.max_blocks = 512;                                             // long enough to be cut into parts
     expect(mbd_kv_attn(&c, &a, q, i, i, i, q, nullptr, nullptr, 0, nullptr), MBD_EINVAL, "no workspace");
     a.scale = std::nanf("");
     expect(mbd_kv_attn(&c, &a, q, i, i, i, q, nullptr, nullptr, 0, nullptr), MBD_EINVAL, "scale NaN");
