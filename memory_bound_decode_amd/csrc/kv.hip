@@ -59,6 +59,7 @@ __device__ __forceinline__ int owner(const int32_t* start, int n, int32_t x) {
 __device__ __forceinline__ int32_t capped(int64_t v) { return v > 0x7fffffff ? 0x7fffffff : int32_t(v); }
 
 constexpr int kMapTokens = 1024;   // of one workgroup of slot_map_kernel
+constexpr int kBatch = 4;
 
 __device__ __forceinline__ void map_token(const SlotArgs& a, const int32_t* start, const int32_t* from, int32_t e) {
     const int i = owner(start, a.n, e);
@@ -81,6 +82,7 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(SlotArgs a) {
     __shared__ int64_t sums[2][kSlotThreads / 64][2];
     __shared__ int32_t start[kMaxSeqs + 1], back_at[kMaxSeqs + 1], take_at[kMaxSeqs + 1];
     __shared__ int32_t from[kMaxSeqs];       // position of the first new token, -1: not served
+    __shared__ int32_t first_new[kMaxSeqs];  // the first column that is not held
     __shared__ int32_t taken_all;
     const int t = threadIdx.x, n = a.n;
     const int per = (n + int(blockDim.x) - 1) / int(blockDim.x);
@@ -138,6 +140,7 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(SlotArgs a) {
             if (want[j] > 0) atomicMax(&taken_all, int32_t(at_need));
             const bool ended = add[j] < 0 && st[j] == 0;
             from[i] = add[j] > 0 && st[j] == 0 ? len[j] : -1;
+            first_new[i] = held[j];
             a.status[i] = st[j];
             a.lens_out[i] = ended ? 0 : st[j] == 0 ? len[j] + max(add[j], 0) : len[j];
             a.held_out[i] = ended ? 0 : held[j] + int32_t(want[j]);
@@ -153,16 +156,38 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(SlotArgs a) {
     __syncthreads();
     const int32_t taken = taken_all;
     if (t == 0) *a.n_free_out = int32_t(top) - taken;
-    for (int32_t e = t; e < int32_t(top) - n_free; e += blockDim.x) {
-        const int i = owner(back_at, n, e);
-        a.free_blocks[n_free + e] = a.table[int64_t(i) * a.max_blocks + (e - back_at[i])];
+    // Entries behind the sums, a batch of each thread's at a time: their reads are in flight together.
+    const int32_t step = blockDim.x;
+    for (int32_t e0 = t; e0 < int32_t(top) - n_free; e0 += kBatch * step) {
+        int32_t id[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int32_t e = e0 + k * step;
+            if (e < int32_t(top) - n_free) {
+                const int i = owner(back_at, n, e);
+                id[k] = a.table[int64_t(i) * a.max_blocks + (e - back_at[i])];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (e0 + k * step < int32_t(top) - n_free) a.free_blocks[n_free + e0 + k * step] = id[k];
     }
     __syncthreads();
-    for (int32_t e = t; e < taken; e += blockDim.x) {
-        const int i = owner(take_at, n, e);
-        // the first column that is not held: lens_out, held_out may be lens, held
-        const int64_t blocks = a.held_out[i] - (take_at[i + 1] - take_at[i]);
-        a.table[int64_t(i) * a.max_blocks + blocks + (e - take_at[i])] = a.free_blocks[int32_t(top) - 1 - e];
+    for (int32_t e0 = t; e0 < taken; e0 += kBatch * step) {
+        int32_t id[kBatch];
+        int64_t to[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int32_t e = e0 + k * step;
+            if (e < taken) {
+                id[k] = a.free_blocks[int32_t(top) - 1 - e];
+                const int i = owner(take_at, n, e);
+                to[k] = int64_t(i) * a.max_blocks + first_new[i] + (e - take_at[i]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (e0 + k * step < taken) a.table[to[k]] = id[k];
     }
     __syncthreads();
     if (!a.map_here) return;

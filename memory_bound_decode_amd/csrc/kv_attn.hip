@@ -132,9 +132,10 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, Seq* 
     used = __builtin_amdgcn_readlane(wave_scan(used), 63);
     // With chunks of work / room, the parts times row tiles add up to between room and
     // room + used: the smallest of three chunks whose items fit the places, of which the
-    // last always does, unless there are as many row tiles as places (then only what is
-    // longer than a place's share is cut).  No chunk is below work / places, so the items
-    // of split requests number less than twice the places.
+    // last always does, unless there are as many row tiles as places: then only what is longer
+    // than two places' share is cut (prompt slices cut at one share each: 58 us, 12 of them the
+    // join; not cut 51).  No chunk is below work / places, so the items of split requests
+    // number less than twice the places.
     uint32_t chunk = 0x7fffffff;
     int items = 0, slots = 0, cut = 0, p0 = 0;     // items, those of split requests, split row tiles
     auto parts_of = [&](int n) { return int((uint32_t(n) + chunk - 1) / chunk); };
@@ -142,7 +143,7 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, Seq* 
     for (int tries = 0; tries < 3; ++tries) {
         if (a.split) {
             const int room = a.places - (tries * used + 1) / 2;
-            const uint64_t share = uint64_t(uint32_t(work - 1) / uint32_t(room > 0 ? room : a.places) + 1) << a.unit;
+            const uint64_t share = uint64_t(uint32_t(work - 1) / uint32_t(room > 0 ? room : (a.places + 1) / 2) + 1) << a.unit;
             chunk = uint32_t(min(max(share, uint64_t(kMinPart)), uint64_t(1) << 30));
         }
         p0 = parts_of(n0);
@@ -554,79 +555,83 @@ __global__ __launch_bounds__(64 * kJoinRows * WAVES) void join_kernel(AttnArgs a
     __shared__ float joined[kJoinRows][WAVES][D], top[kJoinRows][WAVES], sum[kJoinRows][WAVES];
     const int lane = threadIdx.x & 63, row = threadIdx.x / (64 * WAVES), wave = (threadIdx.x >> 6) % WAVES;
     const Split sp = a.splits[blockIdx.x];
-    const int head = blockIdx.y, in_tile = blockIdx.z * kJoinRows + row;
+    const int head = blockIdx.y;
     // the attention kernel's own words, unless another call shares the workspace at the same time:
     // then results are lost, but nothing is read or written out of range
-    if (sp.parts < 2 || in_tile - row >= sp.rows) return;
+    if (sp.parts < 2) return;
     if (sp.rows > rows_of_tile || sp.slot < 0 || sp.stride < 1 || sp.slot + int64_t(sp.parts - 1) * sp.stride >= a.n_parts || sp.row0 < 0 ||
         sp.r0 < 0 || sp.r0 >= (1 << 24) || int64_t(sp.row0) + token_of(a, sp.r0 + sp.rows - 1) >= a.T)
         return;
-    const bool mine = in_tile < sp.rows;
-    const int r = sp.r0 + in_tile;
-    auto row_of = [&](int p) { return ((sp.slot + int64_t(p) * sp.stride) * a.n_kv + head) * rows_of_tile + (mine ? in_tile : 0); };
-    float m = -INFINITY, l = 0.f, o[DQ] = {};
-    for (int p0 = wave; p0 < sp.parts; p0 += kJoinAhead * WAVES) {
-        f32x2 ml[kJoinAhead];
-        float x[kJoinAhead][DQ];
+    for (int pass = blockIdx.z; pass * kJoinRows < sp.rows; pass += gridDim.z) {
+        const int in_tile = pass * kJoinRows + row;
+        if (pass != int(blockIdx.z)) __syncthreads();          // the last pass's sums are read
+        const bool mine = in_tile < sp.rows;
+        const int r = sp.r0 + in_tile;
+        auto row_of = [&](int p) { return ((sp.slot + int64_t(p) * sp.stride) * a.n_kv + head) * rows_of_tile + (mine ? in_tile : 0); };
+        float m = -INFINITY, l = 0.f, o[DQ] = {};
+        for (int p0 = wave; p0 < sp.parts; p0 += kJoinAhead * WAVES) {
+            f32x2 ml[kJoinAhead];
+            float x[kJoinAhead][DQ];
 #pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k) {
-            const int64_t at = row_of(min(p0 + k * WAVES, sp.parts - 1));
-            ml[k] = *reinterpret_cast<const f32x2*>(a.part_ml + at * 2);
+            for (int k = 0; k < kJoinAhead; ++k) {
+                const int64_t at = row_of(min(p0 + k * WAVES, sp.parts - 1));
+                ml[k] = *reinterpret_cast<const f32x2*>(a.part_ml + at * 2);
 #pragma unroll
-            for (int c = 0; c < DQ; ++c) x[k][c] = a.part_o[at * D + 64 * c + lane];
-        }
-        float most = m;
-#pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k)
-            if (p0 + k * WAVES < sp.parts) most = fmaxf(most, ml[k][0]);
-        const float base = most == -INFINITY ? 0.f : most, f0 = __builtin_amdgcn_exp2f(m - base);
-        m = most;
-        l *= f0;
-#pragma unroll
-        for (int c = 0; c < DQ; ++c) o[c] *= f0;
-#pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k)
-            if (p0 + k * WAVES < sp.parts) {
-                const float f = __builtin_amdgcn_exp2f(ml[k][0] - base);
-                l += ml[k][1] * f;
-#pragma unroll
-                for (int c = 0; c < DQ; ++c) o[c] += x[k][c] * f;
+                for (int c = 0; c < DQ; ++c) x[k][c] = a.part_o[at * D + 64 * c + lane];
             }
-    }
-    if (WAVES > 1 && lane == 0) top[row][wave] = m;
-    if (WAVES > 1) {
-        __syncthreads();
-        float most = top[row][0];
+            float most = m;
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) most = fmaxf(most, top[row][w]);
-        const float f = __builtin_amdgcn_exp2f(m - (most == -INFINITY ? 0.f : most));
-        m = most;
-        l *= f;
+            for (int k = 0; k < kJoinAhead; ++k)
+                if (p0 + k * WAVES < sp.parts) most = fmaxf(most, ml[k][0]);
+            const float base = most == -INFINITY ? 0.f : most, f0 = __builtin_amdgcn_exp2f(m - base);
+            m = most;
+            l *= f0;
 #pragma unroll
-        for (int c = 0; c < DQ; ++c) o[c] *= f;
-    }
-    if (lane == 0) sum[row][wave] = l;
+            for (int c = 0; c < DQ; ++c) o[c] *= f0;
 #pragma unroll
-    for (int c = 0; c < DQ; ++c) joined[row][wave][64 * c + lane] = o[c];
-    __syncthreads();
-    if (!mine) return;
-    l = 0.f;
+            for (int k = 0; k < kJoinAhead; ++k)
+                if (p0 + k * WAVES < sp.parts) {
+                    const float f = __builtin_amdgcn_exp2f(ml[k][0] - base);
+                    l += ml[k][1] * f;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) l += sum[row][w];
-    const int j = token_of(a, r), qh = head * a.group + (r - j * a.group);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t token = sp.row0 + j;
-    const int first = (threadIdx.x % (64 * WAVES)) * 2;
-    for (int d = first; d < D; d += 128 * WAVES) {
-        float x0 = 0.f, x1 = 0.f;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-            x0 += joined[row][w][d];
-            x1 += joined[row][w][d + 1];
+                    for (int c = 0; c < DQ; ++c) o[c] += x[k][c] * f;
+                }
         }
-        *reinterpret_cast<uint32_t*>(a.out + token * a.out_stride + int64_t(qh) * D + d) = pack_bf16(x0 * inv, x1 * inv);
+        if (WAVES > 1 && lane == 0) top[row][wave] = m;
+        if (WAVES > 1) {
+            __syncthreads();
+            float most = top[row][0];
+#pragma unroll
+            for (int w = 1; w < WAVES; ++w) most = fmaxf(most, top[row][w]);
+            const float f = __builtin_amdgcn_exp2f(m - (most == -INFINITY ? 0.f : most));
+            m = most;
+            l *= f;
+#pragma unroll
+            for (int c = 0; c < DQ; ++c) o[c] *= f;
+        }
+        if (lane == 0) sum[row][wave] = l;
+#pragma unroll
+        for (int c = 0; c < DQ; ++c) joined[row][wave][64 * c + lane] = o[c];
+        __syncthreads();
+        if (!mine) continue;
+        l = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) l += sum[row][w];
+        const int j = token_of(a, r), qh = head * a.group + (r - j * a.group);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t token = sp.row0 + j;
+        const int first = (threadIdx.x % (64 * WAVES)) * 2;
+        for (int d = first; d < D; d += 128 * WAVES) {
+            float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) {
+                x0 += joined[row][w][d];
+                x1 += joined[row][w][d + 1];
+            }
+            *reinterpret_cast<uint32_t*>(a.out + token * a.out_stride + int64_t(qh) * D + d) = pack_bf16(x0 * inv, x1 * inv);
+        }
+        if (first == 0 && a.lse) a.lse[token * (a.n_kv * a.group) + qh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
     }
-    if (first == 0 && a.lse) a.lse[token * (a.n_kv * a.group) + qh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
 // How a call is laid out; the same for the workspace's size and the launch.
@@ -671,7 +676,8 @@ static void launch(const AttnArgs& a, const Plan& p, int64_t items, bool ext, hi
     else hipLaunchKernelGGL((attn_kernel<E4M3, DQ, NT, false>), grid, block, 0, s, a);
     if (a.n_splits) {
         const int rows = std::min(16 * NT, a.max_new * a.group);
-        const dim3 joins(unsigned(a.n_splits), unsigned(a.n_kv), unsigned((rows + kJoinRows - 1) / kJoinRows));
+        // (at most four workgroups a tile: where few tiles are split, most find nothing to do)
+        const dim3 joins(unsigned(a.n_splits), unsigned(a.n_kv), unsigned(std::min((rows + kJoinRows - 1) / kJoinRows, 4)));
         // few row tiles can have many parts each: more waves over them
         if (a.n_seqs * int64_t(p.row_tiles) * 8 < p.places)
             hipLaunchKernelGGL((join_kernel<DQ, 4>), joins, dim3(64 * kJoinRows * 4), 0, s, a, 16 * NT);
