@@ -4,6 +4,8 @@
 // weights those are the cached keys and values, halved here against bf16.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "kv_common.h"
 
 namespace mbd {
@@ -515,10 +517,10 @@ __device__ __forceinline__ int run_length(const AppendArgs& a, const Look& k, in
 // a run.  The waves of a workgroup take neighbouring heads, which lie side by side.
 template <bool E4M3, class T>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
-    const int hw = blockIdx.y * 4 + (threadIdx.x >> 6);
+    const int hw = blockIdx.x * 4 + (threadIdx.x >> 6);
     if (hw >= 2 * a.n_heads) return;
     const int head = hw % a.n_heads;
-    const int32_t t0 = int32_t(blockIdx.x);
+    const int32_t t0 = int32_t(blockIdx.y);
     const Look k = look_at(a, t0);
     if (!k.starts) return;
     const int32_t first = __builtin_amdgcn_readfirstlane(k.slot);
@@ -535,22 +537,24 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(sizeof(T) =
     __shared__ uint32_t lds[4];
     constexpr int kept = 2;            // fewer registers, more workgroups in flight
     const int wave = threadIdx.x >> 6;
-    const int head = blockIdx.y % a.n_heads;
-    const bool values = int(blockIdx.y) >= a.n_heads;
-    const int32_t t0 = int32_t(blockIdx.x) * a.window;
-    const Look k = look_at(a, t0);                     // the same in every wave
-    uint64_t todo = k.starts;
-    for (int turn = 0; todo; ++turn) {
-        const int l = __builtin_ctzll(todo);
-        todo &= todo - 1;
-        const int32_t first = __builtin_amdgcn_readlane(k.slot, l), token = t0 + l;
-        const int fill = first & ((1 << a.shift) - 1), end = fill + run_length(a, k, t0, l, first);
-        if (((end - 1) / kTok + 1 - fill / kTok) * a.head_dim > 64 * kept) {
-            if (values) append_run<E4M3, true, T, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
-            else append_run<E4M3, false, T, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
-        } else if (turn % 4 == wave) {
-            if (values) append_run<E4M3, true, T, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
-            else append_run<E4M3, false, T, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
+    const int head = blockIdx.x % uint32_t(a.n_heads);
+    const bool values = int(blockIdx.x) >= a.n_heads;
+    for (int64_t at = int64_t(blockIdx.y) * a.window; at < a.T; at += int64_t(gridDim.y) * a.window) {
+        const int32_t t0 = int32_t(at);
+        const Look k = look_at(a, t0);                     // the same in every wave
+        uint64_t todo = k.starts;
+        for (int turn = 0; todo; ++turn) {
+            const int l = __builtin_ctzll(todo);
+            todo &= todo - 1;
+            const int32_t first = __builtin_amdgcn_readlane(k.slot, l), token = t0 + l;
+            const int fill = first & ((1 << a.shift) - 1), end = fill + run_length(a, k, t0, l, first);
+            if (((end - 1) / kTok + 1 - fill / kTok) * a.head_dim > 64 * kept) {
+                if (values) append_run<E4M3, true, T, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
+                else append_run<E4M3, false, T, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
+            } else if (turn % 4 == wave) {
+                if (values) append_run<E4M3, true, T, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
+                else append_run<E4M3, false, T, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
+            }
         }
     }
 }
@@ -572,49 +576,54 @@ __device__ __forceinline__ void store4(uint16_t* p, const f32x4 v) {
 
 constexpr int kGatherTokens = 4;   // tokens of one thread
 
-// A thread writes four neighbouring channels, so that a workgroup's stores are whole
-// rows.  The four tokens of a value word are read by four threads: the repeats hit L1.
+// A thread writes four neighbouring channels, so that a workgroup's stores are whole rows of a
+// head, and neighbouring workgroups take a token's other heads: the outputs fill front to back
+// (32768 tokens of 8 heads x 128 to fp32 in 50 us, 6.7 TB/s; with the tokens of one head side
+// by side 63-75).  They are not read again here: streamed past the caches (77 us if kept).
+// The four tokens of a value word are read by four threads: the repeats hit L1.
 template <bool E4M3, class T>
 __global__ __launch_bounds__(256) void gather_kernel(GatherArgs a) {
     const int quads = a.head_dim / 4, rows = 256 / quads;
     const int row = threadIdx.x / quads, quad = threadIdx.x - row * quads;
     if (row >= rows) return;
-    const int head = blockIdx.y, D = a.head_dim;
-    const int32_t t0 = int32_t(blockIdx.x) * rows * kGatherTokens + row;
-    int32_t slot[kGatherTokens];
-    uint32_t kw[kGatherTokens];
-    u32x4 vw[kGatherTokens];
-    float ks[kGatherTokens], vs[kGatherTokens];
+    const int head = blockIdx.x, D = a.head_dim;
+    for (int64_t group = blockIdx.y; group * rows * kGatherTokens < a.T; group += gridDim.y) {
+        const int32_t t0 = int32_t(group) * rows * kGatherTokens + row;
+        int32_t slot[kGatherTokens];
+        uint32_t kw[kGatherTokens];
+        u32x4 vw[kGatherTokens];
+        float ks[kGatherTokens], vs[kGatherTokens];
 #pragma unroll
-    for (int i = 0; i < kGatherTokens; ++i) {
-        const int32_t t = t0 + i * rows;
-        slot[i] = t < a.T ? a.slots[t] : -1;
-        if (slot[i] >= a.n_slots) slot[i] = -1;
+        for (int i = 0; i < kGatherTokens; ++i) {
+            const int32_t t = t0 + i * rows;
+            slot[i] = t < a.T ? a.slots[t] : -1;
+            if (slot[i] >= a.n_slots) slot[i] = -1;
+        }
+        const int slab = quad / 16, m = quad % 16;
+#pragma unroll
+        for (int i = 0; i < kGatherTokens; ++i)
+            if (slot[i] >= 0) {
+                const int64_t bh = int64_t(slot[i] >> a.shift) * a.n_heads + head;
+                const int place = slot[i] & ((1 << a.shift) - 1), tok = place % kTok;
+                const int64_t tile = ((bh * D) << a.shift) + int64_t(place / kTok) * kTok * D + slab * 1024;
+                kw[i] = *reinterpret_cast<const uint32_t*>(a.codes[0] + tile + (m / 4) * 256 + tok * 16 + (m % 4) * 4);
+                vw[i] = *reinterpret_cast<const u32x4*>(a.codes[1] + tile + (tok / 4) * 256 + m * 16);
+                ks[i] = a.scales[0][bh];
+                vs[i] = a.scales[1][bh];
+            }
+#pragma unroll
+        for (int i = 0; i < kGatherTokens; ++i)
+            if (slot[i] >= 0) {
+                const int64_t at = (int64_t(t0 + i * rows) * a.n_heads + head) * D + quad * 4;
+                const int sh = (slot[i] & 3) * 8;
+                store4(static_cast<T*>(a.out[0]) + at, f32x4{code_value<E4M3, 0>(kw[i]) * ks[i], code_value<E4M3, 1>(kw[i]) * ks[i],
+                                                             code_value<E4M3, 2>(kw[i]) * ks[i], code_value<E4M3, 3>(kw[i]) * ks[i]});
+                f32x4 v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = code_value<E4M3, 0>(vw[i][j] >> sh) * vs[i];
+                store4(static_cast<T*>(a.out[1]) + at, v);
+            }
     }
-    const int slab = quad / 16, m = quad % 16;
-#pragma unroll
-    for (int i = 0; i < kGatherTokens; ++i)
-        if (slot[i] >= 0) {
-            const int64_t bh = int64_t(slot[i] >> a.shift) * a.n_heads + head;
-            const int place = slot[i] & ((1 << a.shift) - 1), tok = place % kTok;
-            const int64_t tile = ((bh * D) << a.shift) + int64_t(place / kTok) * kTok * D + slab * 1024;
-            kw[i] = *reinterpret_cast<const uint32_t*>(a.codes[0] + tile + (m / 4) * 256 + tok * 16 + (m % 4) * 4);
-            vw[i] = *reinterpret_cast<const u32x4*>(a.codes[1] + tile + (tok / 4) * 256 + m * 16);
-            ks[i] = a.scales[0][bh];
-            vs[i] = a.scales[1][bh];
-        }
-#pragma unroll
-    for (int i = 0; i < kGatherTokens; ++i)
-        if (slot[i] >= 0) {
-            const int64_t at = (int64_t(t0 + i * rows) * a.n_heads + head) * D + quad * 4;
-            const int sh = (slot[i] & 3) * 8;
-            store4(static_cast<T*>(a.out[0]) + at, f32x4{code_value<E4M3, 0>(kw[i]) * ks[i], code_value<E4M3, 1>(kw[i]) * ks[i],
-                                                         code_value<E4M3, 2>(kw[i]) * ks[i], code_value<E4M3, 3>(kw[i]) * ks[i]});
-            f32x4 v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = code_value<E4M3, 0>(vw[i][j] >> sh) * vs[i];
-            store4(static_cast<T*>(a.out[1]) + at, v);
-        }
 }
 
 // Host checks of the token-wise calls.
@@ -677,7 +686,7 @@ mbd_status mbd_kv_append(const mbd_kv_cache* cache, const void* k, const void* v
         return fail(MBD_ESHAPE, "token strides must be multiples of 8 and at least n_heads * head_dim");
     if (T == 0) return MBD_OK;
     // A wave a token until that is twice the chip's waves, then workgroups over windows that
-    // keep it full: 13 prompts of 16.4k tokens together took 88 us with a wave a run.
+    // keep it full: 13 prompts of 19.5k tokens together took 88 us with a wave a run.
     const int64_t waves = int64_t(T) * 2 * cache->n_heads;
     int32_t window = 1;
     while (window < 64 && waves / window > 4096) window *= 2;
@@ -686,7 +695,7 @@ mbd_status mbd_kv_append(const mbd_kv_cache* cache, const void* k, const void* v
     kv::AppendArgs a{{static_cast<uint8_t*>(cache->k_codes), static_cast<uint8_t*>(cache->v_codes)}, {cache->k_scale, cache->v_scale},
                      {k, v}, {k_stride, v_stride}, slots, int32_t(cache->n_blocks * cache->block_size), T, window, cache->n_heads,
                      cache->head_dim, kv::log2_of(cache->block_size)};
-    const dim3 grid(unsigned((T + window - 1) / window), unsigned(few ? (2 * cache->n_heads + 3) / 4 : 2 * cache->n_heads));
+    const dim3 grid(unsigned(few ? (2 * cache->n_heads + 3) / 4 : 2 * cache->n_heads), unsigned(std::min((T + window - 1) / window, 65535)));
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool wide = dtype == MBD_F32;
     const auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a); };
@@ -710,7 +719,7 @@ mbd_status mbd_kv_gather(const mbd_kv_cache* cache, const int32_t* slots, int32_
                      {cache->k_scale, cache->v_scale}, {k_out, v_out}, slots, int32_t(cache->n_blocks * cache->block_size), T,
                      cache->n_heads, cache->head_dim, kv::log2_of(cache->block_size)};
     const int per = 256 / (cache->head_dim / 4) * kv::kGatherTokens;
-    const dim3 grid(unsigned((T + per - 1) / per), unsigned(cache->n_heads));
+    const dim3 grid(unsigned(cache->n_heads), unsigned(std::min((T + per - 1) / per, 65535)));
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const bool e4m3 = cache->fmt == MBD_KV_E4M3, wide = dtype == MBD_F32;
     if (e4m3 && wide) hipLaunchKernelGGL((kv::gather_kernel<true, float>), grid, dim3(256), 0, s, a);
