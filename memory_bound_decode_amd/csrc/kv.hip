@@ -79,7 +79,9 @@ __device__ __forceinline__ void map_token(const SlotArgs& a, const int32_t* star
 // come back and in the blocks that are taken is a prefix sum over the requests; the
 // entries behind each sum are then written flat over the threads, each finding its
 // request by bisection of the sums in LDS.  A decode step's work is a few KB, so the time
-// is that of the dependent loads (lengths, free stack, tables) and of two scans.
+// is that of the dependent loads (lengths, free stack, tables) and of two scans: 4.6 us for 32
+// requests.  250 requests with 30 prompts (66k tokens, 4k new blocks) take 10.7 us, and 5.9 more
+// for their slot map over the chip, which one workgroup would write in 50.
 __global__ __launch_bounds__(kSlotThreads) void slots_kernel(SlotArgs a) {
     __shared__ int64_t sums[2][kSlotThreads / 64][2];
     __shared__ int32_t start[kMaxSeqs + 1], back_at[kMaxSeqs + 1], take_at[kMaxSeqs + 1];
@@ -514,7 +516,9 @@ __device__ __forceinline__ int run_length(const AppendArgs& a, const Look& k, in
 }
 
 // Few tokens: a wave for each (token, head, keys or values), busy where the token begins
-// a run.  The waves of a workgroup take neighbouring heads, which lie side by side.
+// a run.  The waves of a workgroup take neighbouring heads, which lie side by side.  Bound by
+// its chain of loads (slots -> values, old codes, scale): one token 4.8 us, a verify step of 48
+// requests x 0..9 tokens (fp32, 236 rows) 7.6 us.
 template <bool E4M3, class T>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
     const int hw = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -531,7 +535,9 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 
 // Many tokens: a workgroup for each (window of tokens, head, keys or values).  Long runs
 // are taken by the whole workgroup, so that prompts are read once and all their loads are
-// in flight together; short ones (a wave's units at most) by one wave each.
+// in flight together; short ones (a wave's units at most) by one wave each.  13 prompts of
+// 19.5k tokens (8 heads x 128, bf16 to int8, 120 MB) take 33 us, 3.6 TB/s: the vector units work
+// half of that, the rest is the chain of a workgroup's loads.
 template <bool E4M3, class T>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 6 : 4))) void append_window_kernel(AppendArgs a) {
     __shared__ uint32_t lds[4];
