@@ -434,7 +434,7 @@ typedef struct {
     int32_t max_new;      /* most new tokens of one request, >= 1: 1 for decode, N+1 to
                              verify N drafts, more for prompts                          */
     int32_t window;       /* >= 0                                                       */
-    float scale, softcap; /* finite; softcap in [0, 2^64]                               */
+    float scale, softcap; /* scale in [-2^64, 2^64]; softcap 0, or 2^-64 to 2^64        */
     const float* slopes;  /* device fp32 [n_heads], or NULL                             */
     int64_t q_stride;     /* elements from one token's row to the next, a multiple of 8 */
     int64_t out_stride;   /*   and at least n_heads * head_dim                          */
@@ -456,7 +456,7 @@ typedef struct {
  * overwritten; may be NULL where that is 0.  Calls that share a workspace must not
  * overlap.  Errors: EINVAL, ESHAPE (T above 2^24, max_blocks * block_size above 2^30,
  * n_seqs * max_blocks * block_size / 16 of 2^31 or more, KV heads times tiles of query
- * rows of 2^24 or more), EALIGN, EHIP. */
+ * rows of 2^24 or more, n_seqs times those of max_new above 2^28), EALIGN, EHIP. */
 mbd_status mbd_kv_attn_workspace_bytes(const mbd_kv_cache* cache, int32_t n_heads, int32_t n_seqs,
                                        int32_t max_new, int32_t max_blocks, uint64_t* bytes);
 mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, const uint16_t* q,

@@ -286,6 +286,8 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
     const int all_end = pos_first + 1, all_begin = a.window > 0 ? max(pos_last, 0) - a.window + 1 : 0;
     int t0 = sq.lo, t1 = min(sq.hi, (max(pos_last + 1, 0) + kTok - 1) / kTok);
     if (it.parts > 1) {
+        // (starts that fall, which no request can have, could count rows twice; in range all the same)
+        if (it.split + row_tile >= a.n_splits || slot + int64_t(it.parts - 1) * row_tiles >= a.n_parts) return;
         const int size = even_part(tiles_of(sq), it.parts);
         t0 += part * size;
         t1 = min(t1, t0 + size);
@@ -669,6 +671,7 @@ static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs
     p->nt = rows <= 16 ? 1 : 2;
     p->row_tiles = (rows + 16 * p->nt - 1) / (16 * p->nt);
     const int64_t tiles = int64_t(n_seqs) * p->row_tiles;                  // of query rows
+    if (tiles > (int64_t(1) << 28)) return fail(MBD_ESHAPE, "n_seqs times tiles of max_new tokens' query rows above 2^28");
     p->unit = 0;
     while (((seq_tiles * p->row_tiles) >> p->unit) + 1 >= (int64_t(1) << 31) / n_seqs) ++p->unit;
     p->places = int32_t(std::max<int64_t>(1, kCus * per_cu(c->head_dim / 64, p->nt) / c->n_heads));
@@ -740,8 +743,9 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     if (st != MBD_OK) return st;
     if (args->T < 0 || args->T > (1 << 24)) return fail(MBD_ESHAPE, "T %d outside [0, 2^24]", args->T);
     if (args->window < 0) return fail(MBD_EINVAL, "window %d below 0", args->window);
-    if (!std::isfinite(args->scale) || !(args->softcap >= 0 && args->softcap <= 0x1p64f))
-        return fail(MBD_EINVAL, "scale must be finite, softcap in [0, 2^64]");
+    if (!(std::fabs(args->scale) <= 0x1p64f)) return fail(MBD_EINVAL, "scale outside [-2^64, 2^64]");
+    if (args->softcap != 0 && !(args->softcap >= 0x1p-64f && args->softcap <= 0x1p64f))
+        return fail(MBD_EINVAL, "softcap is neither 0 nor in [2^-64, 2^64]");
     const int64_t row = int64_t(args->n_heads) * cache->head_dim;
     if (args->q_stride < row || args->out_stride < row || args->q_stride % 8 || args->out_stride % 8)
         return fail(MBD_ESHAPE, "row strides must be multiples of 8 and at least n_heads * head_dim");

@@ -82,7 +82,8 @@ BAD_ARGS = [(dict(n_heads=7), "ESHAPE"), (dict(n_heads=0), "ESHAPE"), (dict(n_se
             (dict(max_blocks=0), "ESHAPE"), (dict(max_blocks=(1 << 26) + 1), "ESHAPE"), (dict(max_blocks=1 << 26, n_seqs=32), "ESHAPE"),
             (dict(T=-1), "ESHAPE"), (dict(T=(1 << 24) + 1), "ESHAPE"), (dict(max_new=0), "ESHAPE"), (dict(max_new=1 << 22), "ESHAPE"),
             (dict(window=-1), "EINVAL"), (dict(scale=float("nan")), "EINVAL"), (dict(softcap=-1.0), "EINVAL"),
-            (dict(softcap=float("inf")), "EINVAL"), (dict(softcap=float("nan")), "EINVAL"), (dict(n_heads=514), "ESHAPE"), (dict(q_stride=1016), "ESHAPE"), (dict(out_stride=1028), "ESHAPE"),
+            (dict(softcap=float("inf")), "EINVAL"), (dict(softcap=float("nan")), "EINVAL"), (dict(n_heads=514), "ESHAPE"), (dict(softcap=1e-30), "EINVAL"), (dict(scale=float("inf")), "EINVAL"),
+            (dict(scale=-1e30), "EINVAL"), (dict(n_seqs=4096, max_new=1 << 20, n_heads=8), "ESHAPE"), (dict(q_stride=1016), "ESHAPE"), (dict(out_stride=1028), "ESHAPE"),
             (dict(slopes=P + 2), "EALIGN"), (dict(n_heads=512, n_seqs=4096, max_new=1 << 15, T=1 << 24, q_stride=1 << 16, out_stride=1 << 16), "ESHAPE")]
 
 
