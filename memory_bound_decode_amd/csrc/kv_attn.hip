@@ -28,11 +28,10 @@
 namespace mbd {
 namespace kv {
 
-constexpr int kWaves = 4;              // waves of a workgroup; each takes every fourth step
 constexpr int kStep = 2;               // tiles of one step: 32 tokens, the k of an MFMA
 constexpr int kRefill = 64 / kStep;    // steps whose block ids and scales one lane each holds
 constexpr int kMaxSeqs = 4096;
-constexpr int kMinPart = kWaves * kStep;    // tiles: the least part of a request, a step a wave
+constexpr int kMaxWaves = 4;           // most waves of a workgroup; they take its steps in turn
 constexpr int kCus = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -56,7 +55,7 @@ struct AttnArgs {
     const float* slopes;
     int64_t q_stride, out_stride;
     uint32_t per_group;                  // ceil(2^32 / group)
-    int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, row_shift, places, unit, n_splits, n_parts;
+    int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, row_shift, min_part, places, unit, n_splits, n_parts;
     bool split;                          // whether requests may be cut into parts
     float to_score, softcap;             // product to score in the log2 domain (or over the cap); the cap there
 };
@@ -152,7 +151,7 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, Seq* 
         if (a.split) {
             const int room = a.places - (tries * used + 1) / 2;
             const uint64_t share = uint64_t(uint32_t(work - 1) / uint32_t(room > 0 ? room : (a.places + 1) / 2) + 1) << a.unit;
-            chunk = uint32_t(min(max(share, uint64_t(kMinPart)), uint64_t(1) << 30));
+            chunk = uint32_t(min(max(share, uint64_t(a.min_part)), uint64_t(1) << 30));
         }
         p0 = parts_of(n0);
         items = p0 * rt0;
@@ -260,12 +259,17 @@ __device__ __forceinline__ float lane_float(float v, int l) {
 // for the 1.08 GB of the largest decode step.)
 constexpr int per_cu(int dq, int nt) { return nt == 1 ? (dq <= 2 ? 4 : dq == 3 ? 3 : 2) : (dq == 1 ? 4 : dq == 2 ? 3 : 2); }
 
-// DQ = head_dim / 64, NT = tiles of 16 query rows, EXT: cap, window or distance bias.
-template <bool E4M3, int DQ, int NT, bool EXT>
-__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per_cu(DQ, NT)))) void attn_kernel(AttnArgs a) {
+// DQ = head_dim / 64, NT = tiles of 16 query rows, EXT: cap, window or distance bias, WAVES: four
+// to a part, or one, which waits for no other and finds its share alone, where the requests
+// outnumber the places that parts of four waves have.  Four waves against one there:
+// 1000 requests of up to 600 tokens (64 / 4 heads x 128, e4m3) 374 and 169 us, 256 of up to 1000
+// (32 / 8 x 128, int8) 72 and 66, 160 of up to 8192 250 and 246, 40 of up to 600 with 32 / 32 heads
+// 27.5 and 28.8.
+template <bool E4M3, int DQ, int NT, bool EXT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_cu(DQ, NT)))) void attn_kernel(AttnArgs a) {
     constexpr int D = 64 * DQ, ROWS = 16 * NT, PITCH = 68;
-    __shared__ float merge[kWaves][ROWS][PITCH];     // pitch: rows 4 banks apart
-    __shared__ float merge_m[kWaves][ROWS], merge_l[kWaves][ROWS];
+    __shared__ float merge[WAVES][ROWS][PITCH];     // pitch: rows 4 banks apart
+    __shared__ float merge_m[WAVES][ROWS], merge_l[WAVES][ROWS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, n = lane & 15;
     const int in_block = (1 << a.shift) - 1;
@@ -296,8 +300,8 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
     if (a.window > 0) t0 = max(t0, max(max(pos_first, 0) - a.window + 1, 0) / kTok);
 
     const int steps = (max(t1 - t0, 0) + kStep - 1) / kStep;
-    const int mine = steps > wave ? (steps - wave + kWaves - 1) / kWaves : 0;
-    auto tile_of = [&](int k) { return t0 + kStep * (wave + kWaves * k); };
+    const int mine = steps > wave ? (steps - wave + WAVES - 1) / WAVES : 0;
+    auto tile_of = [&](int k) { return t0 + kStep * (wave + WAVES * k); };
     // lane l looks up tile l % 2 of step k0 + l / 2; the first look is on its way before the queries
     const int32_t* table = a.table + int64_t(it.seq) * a.max_blocks;
     auto look_up = [&](int k0) {
@@ -324,7 +328,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
         const uint16_t* row = a.q + int64_t(sq.row0 + j) * a.q_stride + int64_t(qh) * D + 16 * g;
 #pragma unroll
         for (int c = 0; c < 2 * DQ; ++c) {
-            if (kQueryLds && c % kWaves != wave) continue;
+            if (kQueryLds && c % WAVES != wave) continue;
             u32x4 w = {0, 0, 0, 0};
             if (in) w = *reinterpret_cast<const u32x4*>(row + 64 * (c / 2) + 8 * (c % 2));
             if constexpr (kQueryLds) queries[t * 2 * DQ + c][lane] = w;
@@ -519,7 +523,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
     for (int t = 0; t < NT; ++t) {
         float m = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) m = fmaxf(m, merge_m[w][16 * t + n]);
+        for (int w = 0; w < WAVES; ++w) m = fmaxf(m, merge_m[w][16 * t + n]);
         f[t] = __builtin_amdgcn_exp2f(top[t] - (m == -INFINITY ? 0.f : m));
     }
 #pragma unroll
@@ -532,15 +536,15 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(per
                 *reinterpret_cast<f32x4*>(&merge[wave][16 * t + n][16 * g + 4 * i]) =
                     f32x4{acc[c][0][t][i], acc[c][1][t][i], acc[c][2][t][i], acc[c][3][t][i]} * f[t];
         __syncthreads();
-        for (int e = threadIdx.x; e < rows * 16; e += 64 * kWaves) {
+        for (int e = threadIdx.x; e < rows * 16; e += 64 * WAVES) {
             const int r = e >> 4, d = (e & 15) * 4;
             float m = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) m = fmaxf(m, merge_m[w][r]);
+            for (int w = 0; w < WAVES; ++w) m = fmaxf(m, merge_m[w][r]);
             const float base = m == -INFINITY ? 0.f : m;
             f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
+            for (int w = 0; w < WAVES; ++w) {
                 l += merge_l[w][r] * __builtin_amdgcn_exp2f(merge_m[w][r] - base);
                 o += *reinterpret_cast<const f32x4*>(&merge[w][r][d]);
             }
@@ -649,7 +653,7 @@ __global__ __launch_bounds__(64 * kJoinRows * WAVES) void join_kernel(AttnArgs a
 
 // How a call is laid out; the same for the workspace's size and the launch.
 struct Plan {
-    int32_t group, nt, row_tiles, places, unit;
+    int32_t group, nt, waves, row_tiles, places, unit;
     bool split;
     int64_t longest;         // parts of a request at most
     uint64_t parts;          // partial results of a head, of nt * 16 rows
@@ -674,8 +678,11 @@ static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs
     if (tiles > (int64_t(1) << 28)) return fail(MBD_ESHAPE, "n_seqs times tiles of max_new tokens' query rows above 2^28");
     p->unit = 0;
     while (((seq_tiles * p->row_tiles) >> p->unit) + 1 >= (int64_t(1) << 31) / n_seqs) ++p->unit;
-    p->places = int32_t(std::max<int64_t>(1, kCus * per_cu(c->head_dim / 64, p->nt) / c->n_heads));
-    p->longest = (seq_tiles + kMinPart - 1) / kMinPart;
+    const int waves = kCus * per_cu(c->head_dim / 64, p->nt) * kMaxWaves;  // that the chip holds
+    p->waves = p->nt == 1 && tiles > std::max(1, waves / kMaxWaves / c->n_heads) ? 1 : kMaxWaves;
+    p->places = std::max(1, waves / p->waves / c->n_heads);
+    const int64_t least = p->waves * kStep;                                // tiles of a part: a step a wave
+    p->longest = (seq_tiles + least - 1) / least;
     p->split = p->longest > 1 && p->places > 1;
     p->parts = p->split ? std::min<int64_t>(2 * p->places, tiles * p->longest) : 0;
     p->splits = std::min<int64_t>(p->parts / 2, tiles);
@@ -683,11 +690,11 @@ static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs
     return MBD_OK;
 }
 
-template <bool E4M3, int DQ, int NT>
+template <bool E4M3, int DQ, int NT, int WAVES>
 static void launch(const AttnArgs& a, const Plan& p, int64_t items, bool ext, hipStream_t s) {
-    const dim3 grid(unsigned(items) * unsigned(a.n_kv)), block(64 * kWaves);
-    if (ext) hipLaunchKernelGGL((attn_kernel<E4M3, DQ, NT, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((attn_kernel<E4M3, DQ, NT, false>), grid, block, 0, s, a);
+    const dim3 grid(unsigned(items) * unsigned(a.n_kv)), block(64 * WAVES);
+    if (ext) hipLaunchKernelGGL((attn_kernel<E4M3, DQ, NT, true, WAVES>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((attn_kernel<E4M3, DQ, NT, false, WAVES>), grid, block, 0, s, a);
     if (a.n_splits) {
         const int rows = std::min(16 * NT, a.max_new * a.group);
         // (at most four workgroups a tile: where few tiles are split, most find nothing to do)
@@ -702,8 +709,9 @@ static void launch(const AttnArgs& a, const Plan& p, int64_t items, bool ext, hi
 
 template <bool E4M3, int DQ>
 static void launch_rows(const AttnArgs& a, const Plan& p, int64_t items, bool ext, hipStream_t s) {
-    if (p.nt == 1) return launch<E4M3, DQ, 1>(a, p, items, ext, s);
-    launch<E4M3, DQ, 2>(a, p, items, ext, s);
+    if (p.nt == 2) launch<E4M3, DQ, 2, 4>(a, p, items, ext, s);
+    else if (p.waves == 4) launch<E4M3, DQ, 1, 4>(a, p, items, ext, s);
+    else launch<E4M3, DQ, 1, 1>(a, p, items, ext, s);
 }
 
 template <bool E4M3>
@@ -792,6 +800,7 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     a.group = p.group;
     a.per_group = uint32_t(((uint64_t(1) << 32) + p.group - 1) / p.group);
     a.row_shift = p.nt == 1 ? 4 : 5;
+    a.min_part = p.waves * kv::kStep;
     a.places = p.places;
     a.unit = p.unit;
     a.n_splits = int32_t(std::min<int64_t>(p.splits, used));

@@ -484,6 +484,22 @@ def test_attn_many_requests(dev):
     _run_attn(dev, INT8, 64, 16, 1, 2, list(np.random.default_rng(1).integers(1, 60, 300)), [1] * 300)
 
 
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("hkv,group,new,opts", [
+    (16, 2, 1, {}), (16, 5, 3, {}), (16, 1, 1, dict(softcap=9.0, window=200, alibi=True))])
+def test_attn_more_requests_than_places(dev, fmt, dim, hkv, group, new, opts):
+    """So many requests that one wave works on each part; a long one among them is cut, some see nothing."""
+    n = 70
+    lens = list(np.random.default_rng(2).integers(new, 100, n))
+    lens[1] = 1500
+    _run_attn(dev, fmt, dim, 16, hkv, group, lens, [i % (new + 1) if i else 0 for i in range(n - 1)] + [new], **opts)
+
+
+def test_attn_more_heads_than_places(dev):
+    _run_attn(dev, INT8, 64, 16, 1100, 1, [20, 40, 3], [1, 0, 1])
+
+
 def test_attn_large_scores(dev):
     """Scores far apart: running maxima that move late, weights that underflow."""
     _run_attn(dev, INT8, 128, 16, 1, 4, [900], [3], scale=8.0)
