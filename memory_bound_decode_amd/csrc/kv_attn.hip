@@ -122,19 +122,27 @@ __device__ __forceinline__ int32_t even_part(int tiles, int parts) {     // tile
 // Item `want` (seq is -1 if there is none), its request, and how many row tiles are split.
 __device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, Seq* sq, int* splits) {
     const int lane = threadIdx.x & 63;
-    const int per = (a.n_seqs + 63) / 64;
-    const int i0 = lane * per, i1 = min(i0 + per, a.n_seqs);
-    const Seq mine = load_seq(a, min(i0, a.n_seqs - 1));        // up to 64 requests: one a lane, read once
-    const int n0 = i0 < a.n_seqs ? tiles_of(mine) : 0, rt0 = n0 ? row_tiles_of(a, mine) : 0;
+    // Request 64 j + l is lane l's in round j: a round's loads are whole lines.  (With a run of
+    // neighbours a lane each load met 64 lines, and 1000 requests of up to 600 tokens took 169 us
+    // against 103.)
+    const Seq first = load_seq(a, min(lane, a.n_seqs - 1));     // round 0, read once
+    const int n0 = lane < a.n_seqs ? tiles_of(first) : 0, rt0 = n0 ? row_tiles_of(a, first) : 0;
+    // f(tiles, row tiles) of the lane's requests; the loads of four rounds are in flight at once
+    auto each = [&](auto&& f) {
+        f(n0, rt0);
+#pragma unroll 4
+        for (int i = 64 + lane; i < a.n_seqs; i += 64) {
+            const Seq s = load_seq(a, i);
+            const int n = tiles_of(s);
+            f(n, n ? row_tiles_of(a, s) : 0);
+        }
+    };
     // in units that keep the sum within 32 bits, rounded up
-    auto work_of = [&](int n, int rt) { return int((uint64_t(uint32_t(n)) * uint32_t(rt) + (uint64_t(1) << a.unit) - 1) >> a.unit); };
-    int work = work_of(n0, rt0), used = rt0;
-    for (int i = i0 + 1; i < i1; ++i) {
-        const Seq s = load_seq(a, i);
-        const int n = tiles_of(s), rt = n ? row_tiles_of(a, s) : 0;
-        work += work_of(n, rt);
+    int work = 0, used = 0;
+    each([&](int n, int rt) {
+        work += int((uint64_t(uint32_t(n)) * uint32_t(rt) + (uint64_t(1) << a.unit) - 1) >> a.unit);
         used += rt;
-    }
+    });
     work = max(__builtin_amdgcn_readlane(wave_scan(work), 63), 1);
     used = __builtin_amdgcn_readlane(wave_scan(used), 63);
     // With chunks of work / room, the parts times row tiles add up to between room and
@@ -144,7 +152,7 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, Seq* 
     // join; not cut 51).  No chunk is below work / places, so the items of split requests
     // number less than twice the places.
     uint32_t chunk = 0x7fffffff;
-    int items = 0, slots = 0, cut = 0, p0 = 0;     // items, those of split requests, split row tiles
+    int cut = 0;                                   // split row tiles
     auto parts_of = [&](int n) { return int((uint32_t(n) + chunk - 1) / chunk); };
 #pragma unroll 1
     for (int tries = 0; tries < 3; ++tries) {
@@ -153,44 +161,39 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, Seq* 
             const uint64_t share = uint64_t(uint32_t(work - 1) / uint32_t(room > 0 ? room : (a.places + 1) / 2) + 1) << a.unit;
             chunk = uint32_t(min(max(share, uint64_t(a.min_part)), uint64_t(1) << 30));
         }
-        p0 = parts_of(n0);
-        items = p0 * rt0;
-        cut = p0 > 1 ? rt0 : 0;
-        slots = p0 > 1 ? items : 0;
-        for (int i = i0 + 1; i < i1; ++i) {
-            const Seq s = load_seq(a, i);
-            const int n = tiles_of(s), p = parts_of(n), rt = n ? row_tiles_of(a, s) : 0;
+        int items = 0;
+        cut = 0;
+        each([&](int n, int rt) {
+            const int p = parts_of(n);
             items += p * rt;
             cut += p > 1 ? rt : 0;
-            slots += p > 1 ? p * rt : 0;
-        }
+        });
         if (!a.split || __builtin_amdgcn_readlane(wave_scan(items), 63) <= a.places) break;
     }
-    const int cut_end = wave_scan(cut);
-    int item0 = wave_scan(items) - items, slot0 = wave_scan(slots) - slots, cut0 = cut_end - cut;
-    Item it{-1, 0, 0, 0, 0};
-    Seq s = mine;
-    auto look = [&](int i, int p, int rt, const Seq& is) {
-        if (want >= item0 && want < item0 + p * rt) {
-            it = {i, p, want - item0, slot0, cut0};
-            s = is;
+    *splits = __builtin_amdgcn_readlane(wave_scan(cut), 63);
+
+    Seq s = first;
+    int items = 0, slots = 0, cuts = 0;            // of earlier rounds
+#pragma unroll 1
+    for (int round = 0; round < a.n_seqs; round += 64) {
+        Seq next = s;
+        if (round + 64 < a.n_seqs) next = load_seq(a, min(round + 64 + lane, a.n_seqs - 1));
+        const int n = round + lane < a.n_seqs ? tiles_of(s) : 0, rt = n ? row_tiles_of(a, s) : 0, p = parts_of(n);
+        const int mine = p * rt, my_slots = p > 1 ? mine : 0, my_cuts = p > 1 ? rt : 0;
+        const int end = items + wave_scan(mine), slots_end = slots + wave_scan(my_slots), cuts_end = cuts + wave_scan(my_cuts);
+        const uint64_t who = __ballot(want >= end - mine && want < end);
+        if (who) {
+            const int l = __builtin_ctzll(who);
+            auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+            *sq = {of(s.row0), of(s.n_new), of(s.rows), of(s.p0), of(s.lo), of(s.hi), of(s.len)};
+            return {round + l, of(p), want - of(end - mine), of(slots_end - my_slots), of(cuts_end - my_cuts)};
         }
-        item0 += p * rt;
-        cut0 += p > 1 ? rt : 0;
-        slot0 += p > 1 ? p * rt : 0;
-    };
-    look(i0, p0, rt0, mine);
-    for (int i = i0 + 1; i < i1; ++i) {
-        const Seq is = load_seq(a, i);
-        const int n = tiles_of(is);
-        look(i, parts_of(n), n ? row_tiles_of(a, is) : 0, is);
+        items = __builtin_amdgcn_readlane(end, 63);
+        slots = __builtin_amdgcn_readlane(slots_end, 63);
+        cuts = __builtin_amdgcn_readlane(cuts_end, 63);
+        s = next;
     }
-    const uint64_t who = __ballot(it.seq >= 0);
-    const int l = who ? __builtin_ctzll(who) : 0;
-    auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-    *sq = {of(s.row0), of(s.n_new), of(s.rows), of(s.p0), of(s.lo), of(s.hi), of(s.len)};
-    *splits = __builtin_amdgcn_readlane(cut_end, 63);
-    return {who ? of(it.seq) : -1, of(it.parts), of(it.index), of(it.slot), of(it.split)};
+    return {-1, 0, 0, 0, 0};
 }
 
 // Maximum over the four lanes of a query row (lane % 16): the rows of 16 lanes swap places.
@@ -262,9 +265,9 @@ constexpr int per_cu(int dq, int nt) { return nt == 1 ? (dq <= 2 ? 4 : dq == 3 ?
 // DQ = head_dim / 64, NT = tiles of 16 query rows, EXT: cap, window or distance bias, WAVES: four
 // to a part, or one, which waits for no other and finds its share alone, where the requests
 // outnumber the places that parts of four waves have.  Four waves against one there:
-// 1000 requests of up to 600 tokens (64 / 4 heads x 128, e4m3) 374 and 169 us, 256 of up to 1000
-// (32 / 8 x 128, int8) 72 and 66, 160 of up to 8192 250 and 246, 40 of up to 600 with 32 / 32 heads
-// 27.5 and 28.8.
+// 1000 requests of up to 600 tokens (64 / 4 heads x 128, e4m3) 166 and 103 us, 256 of up to 1000
+// (32 / 8 x 128, int8) 69 and 64, 160 of up to 8192 250 and 245, 40 of up to 600 with 32 / 32 heads
+// 27.7 and 28.8.
 template <bool E4M3, int DQ, int NT, bool EXT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_cu(DQ, NT)))) void attn_kernel(AttnArgs a) {
     constexpr int D = 64 * DQ, ROWS = 16 * NT, PITCH = 68;
