@@ -496,6 +496,14 @@ def test_attn_more_requests_than_places(dev, fmt, dim, hkv, group, new, opts):
     _run_attn(dev, fmt, dim, 16, hkv, group, lens, [i % (new + 1) if i else 0 for i in range(n - 1)] + [new], **opts)
 
 
+def test_attn_most_requests(dev):
+    """4096 requests, the most, of which three in four are not in the step."""
+    n = 4096
+    lens = list(np.random.default_rng(3).integers(1, 5, n))
+    lens[-1], lens[2000] = 700, 100
+    _run_attn(dev, E4M3, 64, 16, 1, 1, lens, [int(i % 4 == 3) for i in range(n)])
+
+
 def test_attn_more_heads_than_places(dev):
     _run_attn(dev, INT8, 64, 16, 1100, 1, [20, 40, 3], [1, 0, 1])
 
