@@ -122,12 +122,12 @@ __device__ __forceinline__ int32_t even_part(int tiles, int parts) {     // tile
 // Item `want` (seq is -1 if there is none), its request, and how many row tiles are split.
 __device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, Seq* sq, int* splits) {
     const int lane = threadIdx.x & 63;
-    // Request 64 j + l is lane l's in round j: a round's loads are whole lines.  (With a run of
+    // Request 64 j + l is lane l's in turn j: a turn's loads are whole lines.  (With a run of
     // neighbours a lane each load met 64 lines, and 1000 requests of up to 600 tokens took 169 us
     // against 103.)
-    const Seq first = load_seq(a, min(lane, a.n_seqs - 1));     // round 0, read once
+    const Seq first = load_seq(a, min(lane, a.n_seqs - 1));     // turn 0, read once
     const int n0 = lane < a.n_seqs ? tiles_of(first) : 0, rt0 = n0 ? row_tiles_of(a, first) : 0;
-    // f(tiles, row tiles) of the lane's requests; the loads of four rounds are in flight at once
+    // f(tiles, row tiles) of the lane's requests; the loads of four turns are in flight at once
     auto each = [&](auto&& f) {
         f(n0, rt0);
 #pragma unroll 4
@@ -173,12 +173,12 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, Seq* 
     *splits = __builtin_amdgcn_readlane(wave_scan(cut), 63);
 
     Seq s = first;
-    int items = 0, slots = 0, cuts = 0;            // of earlier rounds
+    int items = 0, slots = 0, cuts = 0;            // of earlier turns
 #pragma unroll 1
-    for (int round = 0; round < a.n_seqs; round += 64) {
+    for (int turn = 0; turn < a.n_seqs; turn += 64) {
         Seq next = s;
-        if (round + 64 < a.n_seqs) next = load_seq(a, min(round + 64 + lane, a.n_seqs - 1));
-        const int n = round + lane < a.n_seqs ? tiles_of(s) : 0, rt = n ? row_tiles_of(a, s) : 0, p = parts_of(n);
+        if (turn + 64 < a.n_seqs) next = load_seq(a, min(turn + 64 + lane, a.n_seqs - 1));
+        const int n = turn + lane < a.n_seqs ? tiles_of(s) : 0, rt = n ? row_tiles_of(a, s) : 0, p = parts_of(n);
         const int mine = p * rt, my_slots = p > 1 ? mine : 0, my_cuts = p > 1 ? rt : 0;
         const int end = items + wave_scan(mine), slots_end = slots + wave_scan(my_slots), cuts_end = cuts + wave_scan(my_cuts);
         const uint64_t who = __ballot(want >= end - mine && want < end);
@@ -186,7 +186,7 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, Seq* 
             const int l = __builtin_ctzll(who);
             auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
             *sq = {of(s.row0), of(s.n_new), of(s.rows), of(s.p0), of(s.lo), of(s.hi), of(s.len)};
-            return {round + l, of(p), want - of(end - mine), of(slots_end - my_slots), of(cuts_end - my_cuts)};
+            return {turn + l, of(p), want - of(end - mine), of(slots_end - my_slots), of(cuts_end - my_cuts)};
         }
         items = __builtin_amdgcn_readlane(end, 63);
         slots = __builtin_amdgcn_readlane(slots_end, 63);
