@@ -228,6 +228,12 @@ def _refuse(here, name, t, dtype, n=None):
     raise ValueError("%s must be a contiguous %s tensor%s" % (name, dtype, "" if n is None else " of %d values" % n))
 
 
+def _held(here, name, held):
+    """A cache's or pool's memory is where it was built, whatever GPU is current now."""
+    if held.gpu != here:
+        raise ValueError("the %s is on cuda:%d, not on the current GPU" % (name, held.gpu))
+
+
 def _ints(here, i32, *checks):
     """(name, tensor, values) each: contiguous int32 on GPU ``here``."""
     for name, t, n in checks:
@@ -271,7 +277,7 @@ class KvCache:
             if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
                 raise ValueError("codes are contiguous uint8 tensors of one shape, scales contiguous fp32 [n_blocks][n_heads]")
         for t in (k_codes, v_codes, k_scale, v_scale):
-            _gpu("the cache", t)
+            self.gpu = _gpu("the cache", t)
         self.tensors = dict(k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale)
         self.fmt, self.block_size, self.n_heads, self.head_dim = fmt, block_size, k_codes.shape[1], head_dim
         self.n_blocks = k_codes.shape[0]
@@ -297,7 +303,8 @@ class KvPool:
         if block_table.dim() != 2 or free_blocks.dim() != 1:
             raise ValueError("block_table must be [n_seqs][max_blocks], free_blocks [n_blocks]")
         import torch
-        _ints(_gpu("block_table", block_table), torch.int32, ("block_table", block_table, block_table.numel()),
+        self.gpu = _gpu("block_table", block_table)
+        _ints(self.gpu, torch.int32, ("block_table", block_table, block_table.numel()),
               ("free_blocks", free_blocks, free_blocks.numel()))
         self.block_table, self.free_blocks, self.block_size = block_table, free_blocks, block_size
         self.n_seqs, self.max_blocks = block_table.shape
@@ -315,6 +322,7 @@ def mbd_kv_slots(pool: KvPool, new_tokens, lens, held, n_free, seq_start, slots,
     one value for each row of the step's token batch, positions may be None."""
     import torch
     n, T, here, i32 = pool.n_seqs, slots.numel(), _gpu("slots", slots), torch.int32
+    _held(here, "pool", pool)
     _ints(here, i32, ("new_tokens", new_tokens, n), ("lens", lens, n), ("held", held, n), ("n_free", n_free, 1), ("seq_start", seq_start, n + 1),
           ("slots", slots, T), ("lens_out", lens_out, n), ("held_out", held_out, n), ("n_free_out", n_free_out, 1), ("status", status, n))
     if positions is not None:
@@ -329,6 +337,7 @@ def mbd_kv_append(cache: KvCache, k, v, slots, stream=None) -> None:
     """Quantise k, v [T][n_heads][head_dim] (bf16 or fp32; rows may be slices) into their slots."""
     import torch
     here, heads, dim, T, dt = _gpu("k", k), cache.n_heads, cache.head_dim, k.shape[0], k.dtype
+    _held(here, "cache", cache)
     ks, vs = _rows(here, "k", k, heads, dim, (torch.bfloat16, torch.float32)), _rows(here, "v", v, heads, dim, (dt,))
     if v.shape[0] != T:
         raise ValueError("k and v must have as many tokens")
@@ -342,6 +351,7 @@ def mbd_kv_gather(cache: KvCache, slots, k_out, v_out, stream=None) -> None:
     """Dense keys and values [T][n_heads][head_dim] (bf16 or fp32) of the tokens in ``slots``."""
     import torch
     here, heads, dim, T, dt = _gpu("k_out", k_out), cache.n_heads, cache.head_dim, k_out.shape[0], k_out.dtype
+    _held(here, "cache", cache)
     _rows(here, "k_out", k_out, heads, dim, (torch.bfloat16, torch.float32))
     _rows(here, "v_out", v_out, heads, dim, (dt,))
     if v_out.shape[0] != T or not k_out.is_contiguous() or not v_out.is_contiguous():
@@ -371,6 +381,7 @@ def mbd_kv_attn(cache: KvCache, q, seq_start, lens, block_table, out, ws=None, m
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q must be [T][n_heads][head_dim], block_table [n_seqs][max_blocks]")
     here, (T, heads, dim), (n, width) = _gpu("q", q), q.shape, block_table.shape
+    _held(here, "cache", cache)
     qs = _rows(here, "q", q, heads, cache.head_dim, (torch.bfloat16,))
     outs = _rows(here, "out", out, heads, dim, (torch.bfloat16,))
     if out.shape[0] != T:

@@ -149,3 +149,57 @@ def test_packed_attention_arguments():
     a = mbd.MbdKvAttnArgs.from_buffer_copy(raw)
     assert len(raw) == ctypes.sizeof(mbd.MbdKvAttnArgs)
     assert tuple(getattr(a, n) for n, _ in mbd.MbdKvAttnArgs._fields_) == vals
+
+
+class _On(torch.Tensor):
+    """A CPU tensor that says it is on a GPU; its memory is never reached."""
+    gpu = 0
+
+    def get_device(self):
+        return self.gpu
+
+
+def _on(gpu, shape, dtype=torch.int32):
+    t = torch.zeros(shape, dtype=dtype).as_subclass(_On)
+    t.gpu = gpu
+    return t
+
+
+def test_cache_and_pool_of_another_gpu(monkeypatch):
+    """A cache or a pool built on GPU 0 is refused with GPU 1 current, before the library is called."""
+    current = [0]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+
+    def cache(gpu):
+        current[0] = gpu
+        codes, scale = _on(gpu, (4, 2, 16 * 64), torch.uint8), _on(gpu, (4, 2), torch.float32)
+        return mbd.KvCache(mbd.MBD_KV_INT8, 16, 64, codes, codes, scale, scale)
+
+    def pool(gpu):
+        current[0] = gpu
+        return mbd.KvPool(16, _on(gpu, (2, 4)), _on(gpu, 9))
+
+    here, other, tables = cache(1), cache(0), pool(0)
+    current[0] = 1
+
+    def no_library():
+        raise AssertionError("the library was called")
+
+    monkeypatch.setattr(mbd, "lib", no_library)
+    x, ints = _on(1, (3, 2, 64), torch.bfloat16), lambda *n: _on(1, n)
+    calls = {
+        "append": lambda c: mbd.mbd_kv_append(c, x, x, ints(3), stream=0),
+        "gather": lambda c: mbd.mbd_kv_gather(c, ints(3), x, x, stream=0),
+        "attn": lambda c: mbd.mbd_kv_attn(c, x, ints(3), ints(2), ints(2, 4), x, stream=0),
+    }
+    for name, call in calls.items():
+        with pytest.raises(ValueError, match="the cache is on"):
+            call(other)
+        with pytest.raises(AssertionError, match="library was called"):
+            call(here)                                   # the same call with a cache of its GPU goes through
+    slots = lambda p: mbd.mbd_kv_slots(p, ints(2), ints(2), ints(2), ints(1), ints(3), ints(5), None, ints(2), ints(2), ints(1), ints(2), stream=0)
+    with pytest.raises(ValueError, match="the pool is on"):
+        slots(tables)
+    own = pool(1)
+    with pytest.raises(AssertionError, match="library was called"):
+        slots(own)
