@@ -434,7 +434,8 @@ typedef struct {
     int32_t max_new;      /* most new tokens of one request, >= 1: 1 for decode, N+1 to
                              verify N drafts, more for prompts                          */
     int32_t window;       /* >= 0                                                       */
-    float scale, softcap; /* scale in [-2^64, 2^64]; softcap 0, or 2^-64 to 2^64        */
+    float scale, softcap; /* scale in [-2^64, 2^64]; softcap 0, or 2^-64 to 2^64 and
+                             |scale| / softcap at most 2^126                            */
     const float* slopes;  /* device fp32 [n_heads], or NULL                             */
     int64_t q_stride;     /* elements from one token's row to the next, a multiple of 8 */
     int64_t out_stride;   /*   and at least n_heads * head_dim                          */
@@ -450,8 +451,10 @@ typedef struct {
  * aligned: as the x of mbd_gemv where out_stride = n_heads * head_dim.  lse fp32
  * [T][n_heads], natural logarithm of the softmax's sum, or NULL.  Rows of no request,
  * and a request's rows past its first max_new, stay as they were.  Sums and
- * statistics are fp32; softmax weights times value scales enter the second product
- * as bf16.  The order of every sum depends on the arguments alone.
+ * statistics are fp32 (so a product q . k of codes, an uncapped score times log2(e), and
+ * 2^8 times the sum of a channel's |v| over the tokens a query sees have to stay below
+ * 2^127); softmax weights times value scales enter the second product as bf16, each off
+ * by at most 2^-8 of itself.  The order of every sum depends on the arguments alone.
  * ws: device workspace of mbd_kv_attn_workspace_bytes, 16-byte aligned, contents
  * overwritten; may be NULL where that is 0.  Calls that share a workspace must not
  * overlap.  Errors: EINVAL, ESHAPE (T above 2^24, max_blocks * block_size above 2^30,

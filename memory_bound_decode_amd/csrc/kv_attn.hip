@@ -21,6 +21,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "kv_common.h"
@@ -58,6 +59,7 @@ struct AttnArgs {
     int32_t n_blocks, n_seqs, max_blocks, T, max_new, window, shift, n_kv, group, row_shift, min_part, places, unit, n_splits, n_parts;
     bool split;                          // whether requests may be cut into parts
     float to_score, softcap;             // product to score in the log2 domain (or over the cap); the cap there
+    int32_t most_ks;                     // largest key scale whose product with to_score is finite, as bits
 };
 
 // Token of a query row: r / group, exact for r * group below 2^32.
@@ -386,7 +388,9 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
         float ks[kStep], vs[kStep];
 #pragma unroll
         for (int h = 0; h < kStep; ++h) {
-            ks[h] = lane_float(my_ks, l + h) * a.to_score;
+            // the factor stays finite: past fp32 a zero score would become 0 * inf, where any other only
+            // meets the cap (scales are not negative, so their bits compare as they do)
+            ks[h] = __int_as_float(min(__builtin_amdgcn_readlane(__float_as_int(my_ks), l + h), a.most_ks)) * a.to_score;
             vs[h] = lane_float(my_vs, l + h);
             whole = whole && __builtin_amdgcn_readlane(my_id, l + h) >= 0;
 #pragma unroll
@@ -757,6 +761,8 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     if (!(std::fabs(args->scale) <= 0x1p64f)) return fail(MBD_EINVAL, "scale outside [-2^64, 2^64]");
     if (args->softcap != 0 && !(args->softcap >= 0x1p-64f && args->softcap <= 0x1p64f))
         return fail(MBD_EINVAL, "softcap is neither 0 nor in [2^-64, 2^64]");
+    if (args->softcap > 0 && std::fabs(args->scale) / double(args->softcap) > 0x1p126)
+        return fail(MBD_EINVAL, "|scale| / softcap above 2^126");
     const int64_t row = int64_t(args->n_heads) * cache->head_dim;
     if (args->q_stride < row || args->out_stride < row || args->q_stride % 8 || args->out_stride % 8)
         return fail(MBD_ESHAPE, "row strides must be multiples of 8 and at least n_heads * head_dim");
@@ -810,6 +816,9 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     a.n_parts = int32_t(p.parts);
     a.split = p.split;
     a.to_score = args->softcap > 0 ? args->scale / args->softcap : kv::kLog2e * args->scale;
+    // (the margin is for this rounding and the product's)
+    const float most = float(double(FLT_MAX) * (1 - 0x1p-22) / std::max(double(std::fabs(a.to_score)), 1.0));
+    a.most_ks = __builtin_bit_cast(int32_t, most);
     a.softcap = args->softcap * kv::kLog2e;
     const bool ext = a.window > 0 || args->softcap > 0 || args->slopes;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -697,3 +697,38 @@ def test_attn_bad_device_data(dev):
         torch.cuda.synchronize()
         assert torch.isfinite(out.float()).all()
     c.check(cache)
+
+
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("scale,softcap,key_scale", [(2.0 ** 64, 0.0, 2.0 ** 100), (2.0 ** 64, 2.0 ** -62, 2.0 ** 20), (-2.0 ** 64, 1.0, 2.0 ** 100),
+                                                     (2.0 ** 10, 2.0, 2.0 ** 120)])
+def test_attn_factors_past_fp32(dev, fmt, scale, softcap, key_scale):
+    """The factor of a block's scores (key scale x scale / cap) passes fp32: a zero score is 0 all the
+    same, any other meets the cap.  One query channel at most is not zero, so that every product
+    is exact and no rounding decides a score's sign; without a cap the queries are zero."""
+    mbd = _mbd()
+    print("case far factors", fmt, scale, softcap, key_scale, flush=True)
+    dim, bs, length, n = 64, 16, 40, 2
+    c = Cache(fmt, 4, 1, dim, bs, dev)
+    c.fill(np.arange(4))
+    c.ks[:] = key_scale
+    c.k[1], c.ks[1] = 0, 0                              # a block of zero tokens
+    table, start, lens = np.array([[2, 1, 0], [3, -1, -1]]), np.array([0, 1, 2]), np.array([length, 9])
+    q = np.zeros((n, 2, dim))
+    if softcap:
+        q[:, 0, 5] = 1.0
+    cache = c.device()
+    out = torch.full((n, 2, dim), 7.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((n, 2), 7.0, device=dev)
+    ws = torch.empty(max(16, mbd.mbd_kv_attn_workspace_bytes(cache, 2, n, 1, 3)), dtype=torch.uint8, device=dev)
+    mbd.mbd_kv_attn(cache, torch.from_numpy(q).to(torch.bfloat16).to(dev), _ints(start, dev), _ints(lens, dev), _ints(table, dev), out, ws, scale=scale,
+                    softcap=softcap, lse=lse)
+    torch.cuda.synchronize()
+    args = [q, start, lens, table, kv.decode(c.k, fmt), kv.decode(c.v, fmt), c.ks, c.vs, bs, scale, softcap]
+    ref, ref_lse, _ = kv.attention(*args)
+    weight, _, _ = _abs_attention(args, np.abs(kv.decode(c.v, fmt)))
+    # scores are 0 or +-cap, up to the cap's own rounding: the bounds of _tolerances without their products
+    du = 2.0 ** -20 * softcap
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 * 1.01 + 2 * du + 2.0 ** -17) * weight
+    assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+    np.testing.assert_allclose(lse.double().cpu().numpy(), ref_lse, atol=du + 2.0 ** -19, rtol=2.0 ** -21)

@@ -203,3 +203,13 @@ def test_cache_and_pool_of_another_gpu(monkeypatch):
     own = pool(1)
     with pytest.raises(AssertionError, match="library was called"):
         slots(own)
+
+
+def test_scale_over_cap_out_of_range(L):
+    """|scale| / softcap above 2^126, where fp32 cannot hold the factor of a score, is refused; the largest below is not."""
+    call = lambda scale, cap: L.mbd_kv_attn(ctypes.byref(_cache()), ctypes.byref(_args(scale=scale, softcap=cap, T=0)), None, P, P, P, None, None,
+                                            None, 0, None)
+    for scale, cap in ((2.0 ** 64, 2.0 ** -64), (-2.0 ** 64, 2.0 ** -63), (2.0 ** 63, 2.0 ** -64)):
+        assert call(scale, cap) == mbd.MBD_EINVAL
+    for scale, cap in ((2.0 ** 64, 2.0 ** -62), (-2.0 ** 62, 2.0 ** -64), (0.0, 2.0 ** -64), (2.0 ** 64, 0.0), (2.0 ** -64, 2.0 ** 64)):
+        assert call(scale, cap) == mbd.MBD_OK
