@@ -259,7 +259,7 @@ __device__ __forceinline__ uint32_t encode(const float v[4]) {
 }
 
 // Sixteen values x over a scale, as the codes of one unit.  r is the scale's reciprocal,
-// correctly rounded.  E4M3: the scale is a power of two, the product is the quotient.  INT8:
+// correctly rounded.  E4M3: where the scale is a power of two, the product is the quotient.  INT8:
 // Markstein's theorem (IBM J. Res. Dev. 34, 1990): for such an r and a q within an ulp of
 // x / s, q + r (x - q s) with fused operations rounds correctly; three operations where a
 // division without r takes ten and more.  Adding 1.5 * 2^23 then rounds to a whole number,
@@ -430,7 +430,8 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
     const bool grew = wanted > old_scale;
     const float now = grew ? wanted : old_scale, div = now > 0.f ? now : 1.f;
     const float r = 1.f / div, ratio = old_scale / div;
-    const bool any_values = !finite || !(div >= 0x1p-100f);    // a smaller scale's remainders lose bits
+    // a smaller scale's remainders lose bits; an e4m3 scale of a cache filled elsewhere may be no power of two
+    const bool any_values = !finite || !(div >= 0x1p-100f) || (E4M3 && (__float_as_uint(div) & 0x7fffffu));
     if (tid == 0 && (grew || fill == 0)) a.scales[V][bh] = now;
     for (int c0 = 0; c0 < chunks; c0 += round) {
         if (!once) load(c0);

@@ -732,3 +732,40 @@ def test_attn_factors_past_fp32(dev, fmt, scale, softcap, key_scale):
     tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 * 1.01 + 2 * du + 2.0 ** -17) * weight
     assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
     np.testing.assert_allclose(lse.double().cpu().numpy(), ref_lse, atol=du + 2.0 ** -19, rtol=2.0 ** -21)
+
+
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("heads", [2, 700])
+def test_append_ties_over_any_stored_scale(dev, fmt, heads):
+    """Blocks whose stored scale is no power of two (a cache filled by another program), appended to
+    with values in the middle between two codes: the code comes from the fp32 quotient, to even.
+    With many heads the call is large enough for the kernel over windows of tokens."""
+    mbd = _mbd()
+    print("case stored scales", fmt, heads, flush=True)
+    blocks, dim, bs = 12, 64, 16
+    c = Cache(fmt, blocks, heads, dim, bs, dev, seed=heads)
+    c.fill(np.arange(blocks))
+    c.ks[:] = np.float32(np.exp2(c.rng.uniform(-9, 3, c.ks.shape)))
+    c.vs[:] = np.float32(np.exp2(c.rng.uniform(-9, 3, c.vs.shape)))
+    fill = c.rng.integers(1, bs - 1, blocks)
+    live = fill + c.rng.integers(1, bs - fill + 1)
+    _live_only(c, fill)
+    slots = np.concatenate([b * bs + np.arange(fill[b], live[b]) for b in range(blocks)])
+    block = slots // bs
+    values = kv.decode(np.arange(127), fmt) if fmt == E4M3 else np.arange(128.0)
+    mids = (values[1:] + values[:-1]) / 2
+    pick = lambda: c.rng.choice(mids, (len(slots), heads, dim)) * c.rng.choice([-1, 1], (len(slots), heads, dim))
+    k, v = (np.float32(pick() * s[block][..., None].astype(np.float64)) for s in (c.ks, c.vs))
+    v[::3] *= np.float32(1.7)                           # some blocks' scales grow, by what is no power of two
+    cache = c.device()
+    mbd.mbd_kv_append(cache, torch.from_numpy(k).to(dev), torch.from_numpy(v).to(dev), _ints(slots, dev))
+    torch.cuda.synchronize()
+    kv.append(c.k, c.ks, k, slots, fmt)
+    kv.append(c.v, c.vs, v, slots, fmt)
+    got = {n: t.cpu().numpy() for n, t in cache.tensors.items()}
+    np.testing.assert_array_equal(got["k_scale"], c.ks)
+    np.testing.assert_array_equal(got["v_scale"], c.vs)
+    gk, gv = kv.unpack(got["k_codes"], bs, dim, False), kv.unpack(got["v_codes"], bs, dim, True)
+    for b in range(blocks):
+        np.testing.assert_array_equal(gk[b, :, :live[b]], c.k[b, :, :live[b]], err_msg="keys of block %d" % b)
+        np.testing.assert_array_equal(gv[b, :, :live[b]], c.v[b, :, :live[b]], err_msg="values of block %d" % b)
