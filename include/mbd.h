@@ -456,8 +456,9 @@ typedef struct {
  * 2^127); softmax weights times value scales enter the second product as bf16, each off
  * by at most 2^-8 of itself.  The order of every sum depends on the arguments alone.
  * ws: device workspace of mbd_kv_attn_workspace_bytes, 16-byte aligned, contents
- * overwritten; may be NULL where that is 0.  Calls that share a workspace must not
- * overlap.  Errors: EINVAL, ESHAPE (T above 2^24, max_blocks * block_size above 2^30,
+ * overwritten; may be NULL where that is 0.  One made for the most n_seqs, max_new and
+ * max_blocks of a program serves its smaller calls of the same heads too.  Calls that share a
+ * workspace must not overlap.  Errors: EINVAL, ESHAPE (T above 2^24, max_blocks * block_size above 2^30,
  * n_seqs * max_blocks * block_size / 16 of 2^31 or more, KV heads times tiles of query
  * rows of 2^24 or more, n_seqs times those of max_new above 2^28), EALIGN, EHIP. */
 mbd_status mbd_kv_attn_workspace_bytes(const mbd_kv_cache* cache, int32_t n_heads, int32_t n_seqs,

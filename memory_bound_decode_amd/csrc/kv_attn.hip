@@ -668,6 +668,22 @@ struct Plan {
     uint64_t bytes;
 };
 
+// Workgroups of a head that the chip holds.
+static int places_of(const mbd_kv_cache* c, int nt, int waves) {
+    return std::max(1, kCus * per_cu(c->head_dim / 64, nt) * kMaxWaves / waves / c->n_heads);
+}
+
+// The parts and their memory, for tiles of p->nt * 16 query rows and parts of p->waves waves.
+static void lay_out(const mbd_kv_cache* c, int64_t tiles, int64_t seq_tiles, Plan* p) {
+    p->places = places_of(c, p->nt, p->waves);
+    const int64_t least = p->waves * kStep;                                // tiles of a part: a step a wave
+    p->longest = (seq_tiles + least - 1) / least;
+    p->split = p->longest > 1 && p->places > 1;
+    p->parts = p->split ? std::min<int64_t>(2 * p->places, tiles * p->longest) : 0;
+    p->splits = std::min<int64_t>(p->parts / 2, tiles);
+    p->bytes = p->parts * c->n_heads * (16u * p->nt) * (c->head_dim + 2) * sizeof(float) + p->splits * sizeof(Split);
+}
+
 static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs, int32_t max_new, int32_t max_blocks, Plan* p) {
     if (n_heads < 1 || n_heads % c->n_heads) return fail(MBD_ESHAPE, "n_heads %d is not a multiple of the cache's %d", n_heads, c->n_heads);
     if (n_seqs < 1 || n_seqs > kMaxSeqs) return fail(MBD_ESHAPE, "n_seqs %d outside [1, %d]", n_seqs, kMaxSeqs);
@@ -685,16 +701,28 @@ static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs
     if (tiles > (int64_t(1) << 28)) return fail(MBD_ESHAPE, "n_seqs times tiles of max_new tokens' query rows above 2^28");
     p->unit = 0;
     while (((seq_tiles * p->row_tiles) >> p->unit) + 1 >= (int64_t(1) << 31) / n_seqs) ++p->unit;
-    const int waves = kCus * per_cu(c->head_dim / 64, p->nt) * kMaxWaves;  // that the chip holds
-    p->waves = p->nt == 1 && tiles > std::max(1, waves / kMaxWaves / c->n_heads) ? 1 : kMaxWaves;
-    p->places = std::max(1, waves / p->waves / c->n_heads);
-    const int64_t least = p->waves * kStep;                                // tiles of a part: a step a wave
-    p->longest = (seq_tiles + least - 1) / least;
-    p->split = p->longest > 1 && p->places > 1;
-    p->parts = p->split ? std::min<int64_t>(2 * p->places, tiles * p->longest) : 0;
-    p->splits = std::min<int64_t>(p->parts / 2, tiles);
-    p->bytes = p->parts * c->n_heads * (16u * p->nt) * (c->head_dim + 2) * sizeof(float) + p->splits * sizeof(Split);
+    p->waves = p->nt == 1 && tiles > places_of(c, 1, kMaxWaves) ? 1 : kMaxWaves;
+    lay_out(c, tiles, seq_tiles, p);
     return MBD_OK;
+}
+
+// The workspace that this call and every one with fewer requests, tokens or blocks needs: up to
+// 16 query rows parts are of one wave or of four, above that of two row tiles, and the places,
+// which bound the partial results, are most numerous where the rows are few.
+static uint64_t largest_workspace(const mbd_kv_cache* c, int32_t n_seqs, int32_t max_blocks, const Plan& own) {
+    const int64_t seq_tiles = int64_t(max_blocks) * (c->block_size / kTok);
+    uint64_t bytes = own.bytes;
+    if (own.group > 16) return bytes;          // a single token has two row tiles
+    Plan p{};
+    p.nt = 1;
+    for (int waves : {kMaxWaves, 1}) {
+        const int64_t fours = places_of(c, 1, kMaxWaves);
+        if (waves == 1 && n_seqs <= fours) break;
+        p.waves = waves;
+        lay_out(c, waves == 1 ? n_seqs : std::min<int64_t>(n_seqs, fours), seq_tiles, &p);
+        bytes = std::max(bytes, p.bytes);
+    }
+    return bytes;
 }
 
 template <bool E4M3, int DQ, int NT, int WAVES>
@@ -742,7 +770,7 @@ mbd_status mbd_kv_attn_workspace_bytes(const mbd_kv_cache* cache, int32_t n_head
     kv::Plan p;
     mbd_status st = kv::check_cache(cache, false);
     if (st == MBD_OK) st = kv::plan_of(cache, n_heads, n_seqs, max_new, max_blocks, &p);
-    if (st == MBD_OK) *bytes = p.bytes;
+    if (st == MBD_OK) *bytes = kv::largest_workspace(cache, n_seqs, max_blocks, p);
     return st;
 }
 

@@ -213,3 +213,24 @@ def test_scale_over_cap_out_of_range(L):
         assert call(scale, cap) == mbd.MBD_EINVAL
     for scale, cap in ((2.0 ** 64, 2.0 ** -62), (-2.0 ** 62, 2.0 ** -64), (0.0, 2.0 ** -64), (2.0 ** 64, 0.0), (2.0 ** -64, 2.0 ** 64)):
         assert call(scale, cap) == mbd.MBD_OK
+
+
+def test_workspace_for_the_largest_step_serves_all(L):
+    """A workspace made for the most requests, tokens and blocks is enough for every smaller call."""
+    def size(c, *a):
+        need = ctypes.c_uint64()
+        assert L.mbd_kv_attn_workspace_bytes(ctypes.byref(c), *a, ctypes.byref(need)) == mbd.MBD_OK
+        return need.value
+
+    grew = 0
+    for heads, group, dim in ((8, 4, 128), (1, 1, 64), (2, 16, 256), (16, 1, 192), (4, 17, 64), (128, 1, 128), (1100, 2, 64)):
+        c = _cache(n_heads=heads, head_dim=dim, block_size=64)
+        steps = [(n, new, cols) for n in (1, 2, 7, 16, 17, 40, 65, 130, 200, 257, 1000, 1025, 4096) for new in (1, 2, 4, 5, 9, 16, 17, 64, 300)
+                 for cols in (1, 2, 5, 128, 3000)]
+        sizes = {s: size(c, heads * group, *s) for s in steps}
+        for big, most in sizes.items():
+            for small, need in sizes.items():
+                if all(a <= b for a, b in zip(small, big)):
+                    assert need <= most, (heads, group, dim, small, need, big, most)
+                    grew += need < most
+    assert grew
