@@ -769,3 +769,73 @@ def test_append_ties_over_any_stored_scale(dev, fmt, heads):
     for b in range(blocks):
         np.testing.assert_array_equal(gk[b, :, :live[b]], c.k[b, :, :live[b]], err_msg="keys of block %d" % b)
         np.testing.assert_array_equal(gv[b, :, :live[b]], c.v[b, :, :live[b]], err_msg="values of block %d" % b)
+
+
+WINDOW_APPENDS = [  # heads, dim, bs, (cached, new) of each request; all large enough for the kernel over windows of tokens
+    (40, 64, 16, [(0, 70), (5, 40), (16, 33), (31, 1), (0, 16), (15, 50)]),
+    (24, 128, 16, [(3, 200), (0, 97), (15, 1), (9, 7), (32, 64)]),
+    (17, 192, 32, [(30, 150), (7, 3), (0, 260), (31, 2), (17, 88)]),
+    (16, 256, 64, [(63, 300), (1, 62), (0, 129), (20, 44)]),
+    (12, 128, 128, [(0, 400), (100, 250), (127, 2), (64, 64)]),
+    (10, 64, 256, [(0, 600), (200, 300), (16, 128), (255, 1), (17, 239)]),
+    (9, 256, 256, [(3, 900), (40, 216), (128, 1)]),
+    (9, 192, 64, [(13, 1000), (0, 5), (60, 4)]),
+    (66, 64, 256, [(3, 700), (250, 300), (0, 40), (16, 1)]),       # windows of 64 tokens, the widest
+    (70, 128, 16, [(7, 900), (0, 33), (31, 1), (5, 60)]),
+]
+
+
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("special", [False, True])
+@pytest.mark.parametrize("heads,dim,bs,requests", WINDOW_APPENDS)
+def test_append_prompts(dev, fmt, dtype, special, heads, dim, bs, requests):
+    """Prompts: runs that a whole workgroup takes, over windows of tokens, beside short ones; they begin and
+    end inside tiles, over codes of before whose scale grows or stays, go past a window and past 128 tokens of
+    a block, with rows of no slot between requests and, if special, infinities and NaN."""
+    mbd = _mbd()
+    print("case prompts", fmt, dtype, special, heads, dim, bs, requests, flush=True)
+    ends = np.array([a + b for a, b in requests])
+    held = -(-ends // bs)
+    blocks = int(held.sum()) + 2
+    c = Cache(fmt, blocks, heads, dim, bs, dev, seed=heads + bs)
+    order, at = c.rng.permutation(blocks), 0
+    slots, before, live = [], np.zeros(blocks, int), np.zeros(blocks, int)
+    for i, (cached, new) in enumerate(requests):
+        table = order[at:at + held[i]]
+        at += held[i]
+        place = np.arange(cached + new)
+        to = table[place // bs] * bs + place % bs
+        for s, p in zip(to, place):
+            live[s // bs] = s % bs + 1
+            if p < cached:
+                before[s // bs] = s % bs + 1
+        slots += list(to[cached:]) + ([-1] if i % 2 else [])
+    slots = np.array(slots + [blocks * bs, -2 ** 31])
+    T, row = len(slots), heads * dim
+    assert T * 2 * heads > 16384
+    c.fill(np.flatnonzero(before))
+    c.ks[::2] *= np.float32(0.25)                       # every other block's keys, and the others' values, outgrow their scale
+    c.vs[1::2] *= np.float32(0.25)
+    _live_only(c, before)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x = torch.from_numpy(c.rng.standard_normal((T, 2 * row + 8)) * c.rng.choice([0.3, 1.0], (T, 1))).to(dt)
+    if special:
+        for value in (float("inf"), float("-inf"), float("nan")):
+            x[torch.from_numpy(c.rng.integers(0, T, 40)), torch.from_numpy(c.rng.integers(0, 2 * row, 40))] = value
+        x[2:5, :dim] = float("inf")
+    cache, d = c.device(), x.to(dev)
+    mbd.mbd_kv_append(cache, d[:, :row].unflatten(1, (heads, dim)), d[:, row:2 * row].unflatten(1, (heads, dim)), _ints(slots, dev))
+    torch.cuda.synchronize()
+    xn = x.double().numpy()
+    kv.append(c.k, c.ks, xn[:, :row].reshape(T, heads, dim), slots, fmt)
+    kv.append(c.v, c.vs, xn[:, row:2 * row].reshape(T, heads, dim), slots, fmt)
+    got = {n: t.cpu().numpy() for n, t in cache.tensors.items()}
+    used = live > 0
+    np.testing.assert_array_equal(got["k_scale"][used], c.ks[used])
+    np.testing.assert_array_equal(got["v_scale"][used], c.vs[used])
+    assert np.isnan(got["k_scale"][~used]).all() and np.isnan(got["v_scale"][~used]).all()
+    gk, gv = kv.unpack(got["k_codes"], bs, dim, False), kv.unpack(got["v_codes"], bs, dim, True)
+    for b in range(blocks):
+        np.testing.assert_array_equal(gk[b, :, :live[b]], c.k[b, :, :live[b]], err_msg="keys of block %d" % b)
+        np.testing.assert_array_equal(gv[b, :, :live[b]], c.v[b, :, :live[b]], err_msg="values of block %d" % b)
