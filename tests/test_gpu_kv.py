@@ -839,3 +839,107 @@ def test_append_prompts(dev, fmt, dtype, special, heads, dim, bs, requests):
     for b in range(blocks):
         np.testing.assert_array_equal(gk[b, :, :live[b]], c.k[b, :, :live[b]], err_msg="keys of block %d" % b)
         np.testing.assert_array_equal(gv[b, :, :live[b]], c.v[b, :, :live[b]], err_msg="values of block %d" % b)
+
+
+EVERY = [  # head_dim, KV heads, query heads a KV head, tokens, short requests beside, new tokens, window
+    (64, 8, 16, 20000, 0, 1, 0),         # parts of four waves
+    (128, 4, 8, 4097, 3, 1, 0),
+    (64, 16, 4, 4097, 69, 1, 0),         # more requests than places: parts of one wave
+    (128, 2, 16, 4100, 2, 5, 0),         # two row tiles
+    (256, 1, 16, 1500, 1, 3, 0),
+    (64, 4, 16, 6000, 2, 1, 2500),       # a window that begins inside a tile
+    (192, 1, 16, 3000, 1, 4, 1001),
+]
+
+
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("dim,hkv,group,length,others,new,window", EVERY)
+def test_attn_every_position(dev, fmt, dim, hkv, group, length, others, new, window):
+    """Every cached position counts once.  Keys and values hold their position's 15 bits as +-1.5, a query
+    the bits of the position that it looks for: its score is 24 * 15, any other's at least 48 lower, so
+    o is that position's value (the weight and the output each rounded by at most 2^-8) and lse its
+    score (a few fp32 roundings of 360 * log2(e)); a lost token moves lse by 48, one taken twice by log 2.
+    Queries of zero weigh all tokens alike: sums of ones are exact, lse is log(count) up to the
+    logarithm's and the product's roundings."""
+    mbd = _mbd()
+    print("case every position", fmt, dim, hkv, group, length, others, new, window, flush=True)
+    bs, hq, n = 32, hkv * group, others + 1
+    mid = others // 2
+    lens, fresh = np.full(n, 3), np.ones(n, int)
+    lens[mid], fresh[mid] = length, new
+    held = -(-lens // bs)
+    c = Cache(fmt, int(held.sum()), hkv, dim, bs, dev)
+    order = c.rng.permutation(int(held.sum()))
+    table, at = np.full((n, held.max()), -1), 0
+    for i in range(n):
+        table[i, :held[i]] = order[at:at + held[i]]
+        at += held[i]
+    c.ks[:] = c.vs[:] = 2.0 ** -6
+    bits = lambda p: ((np.asarray(p)[..., None] >> np.arange(15)) & 1) * 2 - 1
+    for i in range(n):
+        place = np.arange(held[i] * bs)
+        live = place < lens[i]
+        plus, minus = (int(kv.encode(np.array([96.0 * s]), fmt)[0]) for s in (1, -1))
+        codes = np.zeros((len(place), dim), np.uint8)
+        codes[:, :15] = np.where(bits(place) > 0, plus, minus)
+        for store in (c.k, c.v):
+            store[table[i, place[live] // bs], :, place[live] % bs] = codes[live][:, None]
+    cache = c.device()
+    start = np.concatenate([[0], np.cumsum(fresh)])
+    T, row0 = int(start[-1]), int(start[mid])
+    size = mbd.mbd_kv_attn_workspace_bytes(cache, hq, n, new, table.shape[1])
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device=dev) if size else None
+    q = torch.zeros((T, hq, dim), dtype=torch.bfloat16, device=dev)
+    out, lse = torch.zeros_like(q), torch.zeros((T, hq), device=dev)
+    ints = _ints(start, dev), _ints(lens, dev), _ints(table, dev)
+    call = lambda: mbd.mbd_kv_attn(cache, q, *ints, out, ws, max_new=new, scale=16.0, window=window, lse=lse)
+    call()
+    torch.cuda.synchronize()
+    pos = np.repeat(lens, fresh) - np.repeat(start[1:], fresh) + np.arange(T)
+    count = np.minimum(pos + 1, window) if window else pos + 1
+    np.testing.assert_allclose(lse.double().cpu().numpy(), np.repeat(np.log(count)[:, None], hq, 1), rtol=2.0 ** -21, atol=2.0 ** -24)
+    seen = np.arange(max(0, length - window) if window else 0, length - new + 1)     # by every row of the request
+    per = new * hq
+    tol_lse = 360 * 2.0 ** -21
+    for a in range(0, len(seen), per):
+        target = np.resize(seen[a:a + per], per).reshape(new, hq)
+        q[row0:row0 + new, :, :15] = torch.from_numpy(bits(target)).to(torch.bfloat16).to(dev)
+        call()
+        torch.cuda.synchronize()
+        o, l = out[row0:row0 + new].double().cpu().numpy(), lse[row0:row0 + new].double().cpu().numpy()
+        off = np.abs(o[..., :15] - 1.5 * bits(target))
+        assert off.max() <= 1.5 * (2.0 ** -7 + 2.0 ** -14), "position %d" % target.ravel()[off.max(-1).argmax()]
+        assert (o[..., 15:] == 0).all()
+        gap = np.abs(l - 360)
+        assert gap.max() <= tol_lse, "position %d" % target.ravel()[gap.argmax()]
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("dim,hkv,group,lens,new", [(128, 2, 4, [700, 40], [2, 1]), (64, 1, 8, [90, 2000, 33], [5, 9, 1]), (256, 2, 1, [50] * 3, [1] * 3)])
+def test_attn_bad_queries_stay_in_their_row(dev, dim, hkv, group, lens, new, bad):
+    """A query of NaN or infinities leaves every other row's output and lse as they are, bit for bit."""
+    mbd = _mbd()
+    print("case bad queries", dim, hkv, group, lens, new, bad, flush=True)
+    bs, hq, n = 16, hkv * group, len(lens)
+    held = -(-np.array(lens) // bs)
+    c = Cache(INT8, int(held.sum()), hkv, dim, bs, dev)
+    c.fill(np.arange(int(held.sum())))
+    table = np.full((n, held.max()), -1)
+    for i in range(n):
+        table[i, :held[i]] = held[:i].sum() + np.arange(held[i])
+    cache, start = c.device(), np.concatenate([[0], np.cumsum(new)])
+    T = int(start[-1])
+    q = torch.from_numpy(c.rng.standard_normal((T, hq, dim))).to(torch.bfloat16).to(dev)
+    out, lse = torch.zeros_like(q), torch.zeros((T, hq), device=dev)
+    ws = torch.empty(max(16, mbd.mbd_kv_attn_workspace_bytes(cache, hq, n, max(new), table.shape[1])), dtype=torch.uint8, device=dev)
+    call = lambda: mbd.mbd_kv_attn(cache, q, _ints(start, dev), _ints(lens, dev), _ints(table, dev), out, ws, max_new=max(new), lse=lse)
+    call()
+    want, want_lse = out.clone(), lse.clone()
+    keep = torch.ones((T, hq), dtype=torch.bool, device=dev)
+    for row, head, channel in ((0, 0, 0), (T - 1, hq - 1, dim - 1), (T // 2, hq // 2, slice(None))):
+        q[row, head, channel] = bad
+        keep[row, head] = False
+    call()
+    torch.cuda.synchronize()
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], want_lse[keep])
+    assert not torch.isfinite(out[~keep].float()).all(-1).any()
