@@ -13,7 +13,6 @@ namespace kv {
 
 // ---------------------------------------------------------------- slots
 
-constexpr int kMaxSeqs = 4096;
 constexpr int kSlotThreads = 1024;
 constexpr int kPer = kMaxSeqs / kSlotThreads;   // requests of one thread, neighbours
 

@@ -31,7 +31,6 @@ namespace kv {
 
 constexpr int kStep = 2;               // tiles of one step: 32 tokens, the k of an MFMA
 constexpr int kRefill = 64 / kStep;    // steps whose block ids and scales one lane each holds
-constexpr int kMaxSeqs = 4096;
 constexpr int kMaxWaves = 4;           // most waves of a workgroup; they take its steps in turn
 constexpr int kCus = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;

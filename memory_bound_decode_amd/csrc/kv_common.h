@@ -9,7 +9,8 @@
 namespace mbd {
 namespace kv {
 
-constexpr int kTok = 16;   // tokens of one code tile
+constexpr int kTok = 16;         // tokens of one code tile
+constexpr int kMaxSeqs = 4096;   // requests of a call
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
