@@ -691,12 +691,15 @@ mbd_status mbd_kv_append(const mbd_kv_cache* cache, const void* k, const void* v
     if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8)
         return fail(MBD_ESHAPE, "token strides must be multiples of 8 and at least n_heads * head_dim");
     if (T == 0) return MBD_OK;
-    // A wave a token until that is twice the chip's waves, then workgroups over windows that
-    // keep it full: 13 prompts of 19.5k tokens together took 88 us with a wave a run.
+    // A wave a token up to 4096 waves: above, those that find no run cost more than windows do
+    // (8 heads x 128, waves against windows: 256 requests x 1 token 17.8 and 21.3 us, 128 x 4 21.3 and
+    // 15.2, 128 x 8 fp32 50 and 19, one prompt of 512 12.9 and 10.8).  A window takes the runs that begin in it,
+    // so narrow ones start workgroups that find none; they widen down to 2048 workgroups: one prompt of
+    // 4096 tokens 20.0 us, with 4096 of them 25.4; 512 requests x 8 46.0 and 45.3, with 1024 49.3.
     const int64_t waves = int64_t(T) * 2 * cache->n_heads;
     int32_t window = 1;
-    while (window < 64 && waves / window > 4096) window *= 2;
-    const bool few = waves <= 16384;
+    while (window < 64 && waves / window > 2048) window *= 2;
+    const bool few = waves <= 4096;
     if (few) window = 1;
     kv::AppendArgs a{{static_cast<uint8_t*>(cache->k_codes), static_cast<uint8_t*>(cache->v_codes)}, {cache->k_scale, cache->v_scale},
                      {k, v}, {k_stride, v_stride}, slots, int32_t(cache->n_blocks * cache->block_size), T, window, cache->n_heads,
