@@ -671,8 +671,12 @@ mbd_status mbd_kv_slots(const mbd_kv_pool* pool, const int32_t* new_tokens, cons
     if (!kv::aligned(slots, 4) || !kv::aligned(positions, 4)) return fail(MBD_EALIGN, "int32 arrays must be 4-byte aligned");
     kv::SlotArgs a{new_tokens, lens, held, n_free, pool->block_table, pool->free_blocks, seq_start, slots, positions, lens_out, held_out,
                    n_free_out, status, pool->n_seqs, kv::log2_of(pool->block_size), pool->max_blocks, pool->n_blocks, T,
-                   T <= 2 * kv::kSlotThreads};
-    // a step that decodes has few entries behind its sums: fewer waves meet at the barriers sooner
+                   T <= 8192};
+    // Up to 8192 tokens the one workgroup writes the slot map in less time than a second launch takes:
+    // 64 requests with 2168, 4281 and 8976 tokens 8.9, 10.2 and 13.3 us against 12.0, 12.1 and 12.1, two
+    // with 6001 and 12001 8.6 and 10.8 against 9.8 and 9.9, 4000 that decode 30 against 46.
+    // A step that decodes has few entries behind its sums: fewer waves meet at the barriers sooner
+    // (32 requests 5.1 us, with 1024 threads 7.0; 64 with 525 tokens 7.7 either way, with 1228 9.0 and 8.3).
     const int threads = pool->n_seqs <= 256 && T <= 256 ? 256 : kv::kSlotThreads;
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     hipLaunchKernelGGL(kv::slots_kernel, dim3(1), dim3(threads), 0, s, a);

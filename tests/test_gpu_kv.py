@@ -943,3 +943,30 @@ def test_attn_bad_queries_stay_in_their_row(dev, dim, hkv, group, lens, new, bad
     torch.cuda.synchronize()
     assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], want_lse[keep])
     assert not torch.isfinite(out[~keep].float()).all(-1).any()
+
+
+@pytest.mark.parametrize("seed,n,bs,width,prompt_hi", [(10, 700, 16, 40, 300), (11, 90, 64, 30, 1500), (12, 1500, 32, 12, 90)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_slots_of_many_tokens(dev, seed, n, bs, width, prompt_hi, in_place):
+    """Steps whose slot map one workgroup writes, or the whole chip, just below and above where that changes."""
+    mbd = _mbd()
+    new, lens, held, table, free, n_free = _requests(seed, n, bs, width, prompt_hi)
+    total = int(np.maximum(new, 0).sum())
+    assert total > 8192
+    for T in (8192, 8193, total + 5):
+        print("case slots of many tokens", seed, n, bs, width, in_place, T, flush=True)
+        ref_table, ref_free = table.copy(), free.copy()
+        ref = kv.slots(new, lens, held, ref_table, ref_free, n_free, bs, T)
+        pool = mbd.KvPool(bs, _ints(table, dev), _ints(free, dev))
+        d = {k: _ints(v, dev) for k, v in dict(new=new, lens=lens, held=held, n_free=[n_free]).items()}
+        o = {k: torch.full((s,), -55, dtype=torch.int32, device=dev) for k, s in dict(
+            seq_start=n + 1, slots=T, positions=T, lens_out=n, held_out=n, n_free_out=1, status=n).items()}
+        if in_place:
+            o["lens_out"], o["held_out"], o["n_free_out"] = d["lens"], d["held"], d["n_free"]
+        mbd.mbd_kv_slots(pool, d["new"], d["lens"], d["held"], d["n_free"], o["seq_start"], o["slots"], o["positions"], o["lens_out"],
+                         o["held_out"], o["n_free_out"], o["status"])
+        torch.cuda.synchronize()
+        for name, want in ref.items():
+            np.testing.assert_array_equal(o[name].cpu().numpy(), np.atleast_1d(want), err_msg="%s, T %d" % (name, T))
+        np.testing.assert_array_equal(pool.block_table.cpu().numpy(), ref_table)
+        np.testing.assert_array_equal(pool.free_blocks.cpu().numpy(), ref_free)
