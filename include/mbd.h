@@ -447,20 +447,22 @@ typedef struct {
  * lens[i] - n_i + j, its own key and value already appended.  lens is taken as at most
  * max_blocks * block_size, seq_start as within [0, T].  Block ids outside the cache
  * are left out, as if masked.  A query that sees nothing (position below 0, all
- * blocks left out) gets o = 0, lse = -inf.  out bf16 [T][n_heads][head_dim], 16-byte
- * aligned: as the x of mbd_gemv where out_stride = n_heads * head_dim.  lse fp32
- * [T][n_heads], natural logarithm of the softmax's sum, or NULL.  Rows of no request,
- * and a request's rows past its first max_new, stay as they were.  Sums and
- * statistics are fp32 (so a product q . k of codes, an uncapped score times log2(e), and
- * 2^8 times the sum of a channel's |v| over the tokens a query sees have to stay below
- * 2^127); softmax weights times value scales enter the second product as bf16, each off
+ * blocks left out) gets o = 0, lse = -inf.  Rows of a request that mbd_kv_slots did not
+ * serve are taken as its last cached tokens: they mean nothing, their caller drops them.
+ * out bf16 [T][n_heads][head_dim], 16-byte aligned: as the x of mbd_gemv where out_stride
+ * = n_heads * head_dim.  lse fp32 [T][n_heads], natural logarithm of the softmax's sum, or
+ * NULL.  Rows of no request, and a request's rows past its first max_new, stay as they
+ * were.  Sums and statistics are fp32 (so a product q . k of codes, an uncapped score times
+ * log2(e), and 2^8 times the sum of a channel's |v| over the tokens a query sees have to
+ * stay below 2^127); softmax weights times value scales enter the second product as bf16, each off
  * by at most 2^-8 of itself.  The order of every sum depends on the arguments alone.
  * ws: device workspace of mbd_kv_attn_workspace_bytes, 16-byte aligned, contents
  * overwritten; may be NULL where that is 0.  One made for the most n_seqs, max_new and
- * max_blocks of a program serves its smaller calls of the same heads too.  Calls that share a
- * workspace must not overlap.  Errors: EINVAL, ESHAPE (T above 2^24, max_blocks * block_size above 2^30,
- * n_seqs * max_blocks * block_size / 16 of 2^31 or more, KV heads times tiles of query
- * rows of 2^24 or more, n_seqs times those of max_new above 2^28), EALIGN, EHIP. */
+ * max_blocks of a program serves its smaller calls of the same heads too.  Calls that
+ * share a workspace must not overlap.  Errors: EINVAL, ESHAPE (T above 2^24, max_blocks *
+ * block_size above 2^30, n_seqs * max_blocks * block_size / 16 of 2^31 or more, KV heads
+ * times tiles of query rows of 2^24 or more, n_seqs times those of max_new above 2^28),
+ * EALIGN, EHIP. */
 mbd_status mbd_kv_attn_workspace_bytes(const mbd_kv_cache* cache, int32_t n_heads, int32_t n_seqs,
                                        int32_t max_new, int32_t max_blocks, uint64_t* bytes);
 mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, const uint16_t* q,

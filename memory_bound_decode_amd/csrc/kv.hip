@@ -79,7 +79,7 @@ __device__ __forceinline__ void map_token(const SlotArgs& a, const int32_t* star
 // entries behind each sum are then written flat over the threads, each finding its
 // request by bisection of the sums in LDS.  A decode step's work is a few KB, so the time
 // is that of the dependent loads (lengths, free stack, tables) and of two scans: 4.6 us for 32
-// requests.  250 requests with 30 prompts (66k tokens, 4k new blocks) take 10.7 us, and 5.9 more
+// requests.  250 requests with 30 prompts (66k tokens, 4k new blocks) take 10.7 us, and 6.0 more
 // for their slot map over the chip, which one workgroup would write in 50.
 __global__ __launch_bounds__(kSlotThreads) void slots_kernel(SlotArgs a) {
     __shared__ int64_t sums[2][kSlotThreads / 64][2];
@@ -517,8 +517,8 @@ __device__ __forceinline__ int run_length(const AppendArgs& a, const Look& k, in
 
 // Few tokens: a wave for each (token, head, keys or values), busy where the token begins
 // a run.  The waves of a workgroup take neighbouring heads, which lie side by side.  Bound by
-// its chain of loads (slots -> values, old codes, scale): one token 4.8 us, a verify step of 48
-// requests x 0..9 tokens (fp32, 236 rows) 7.6 us.
+// its chain of loads (slots -> values, old codes, scale): one token 5.2 us, a verify step of 48
+// requests x 0..9 tokens (fp32, 236 rows) 7.7 us.
 template <bool E4M3, class T>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
     const int hw = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -536,8 +536,8 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // Many tokens: a workgroup for each (window of tokens, head, keys or values).  Long runs
 // are taken by the whole workgroup, so that prompts are read once and all their loads are
 // in flight together; short ones (a wave's units at most) by one wave each.  13 prompts of
-// 19.5k tokens (8 heads x 128, bf16 to int8, 120 MB) take 33 us, 3.6 TB/s: the vector units work
-// half of that, the rest is the chain of a workgroup's loads.
+// 19.5k tokens (8 heads x 128, bf16 to int8, 120 MB) take 33.6 us, 3.6 TB/s, from fp32 (200 MB) 48.6
+// us, 4.1 TB/s: the vector units work 42% of that, the rest is the chain of a workgroup's loads.
 template <bool E4M3, class T>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 6 : 4))) void append_window_kernel(AppendArgs a) {
     __shared__ uint32_t lds[4];
@@ -584,8 +584,9 @@ constexpr int kGatherTokens = 4;   // tokens of one thread
 
 // A thread writes four neighbouring channels, so that a workgroup's stores are whole rows of a
 // head, and neighbouring workgroups take a token's other heads: the outputs fill front to back
-// (32768 tokens of 8 heads x 128 to fp32 in 50 us, 6.7 TB/s; with the tokens of one head side
-// by side 63-75).  They are not read again here: streamed past the caches (77 us if kept).
+// (32768 tokens of 8 heads x 128 to fp32, 336 MB, four fifths of it writes, in 49 us, 6.9 TB/s, what a
+// plain fill reaches; to bf16, 201 MB, 31 us; with the tokens of one head side by side 63-75 for
+// 49).  They are not read again here: streamed past the caches (77 us if kept).
 // The four tokens of a value word are read by four threads: the repeats hit L1.
 template <bool E4M3, class T>
 __global__ __launch_bounds__(256) void gather_kernel(GatherArgs a) {

@@ -12,12 +12,13 @@
 // factor of the 16 x 16 scores, or of the weights.
 //
 // A decode step is bound by the codes it streams: 32 requests of 32768 tokens (64 / 4 heads
-// x 128, int8, 1.08 GB) take 178 us, 6.0 of the 6.3 TB/s that a plain read reaches, and 5 us to
-// join the parts; 32 requests of 1 to 8192 tokens (32 / 8 heads, e4m3, 277 MB) 48 + 5 us, 5.8 TB/s.
+// x 128, int8, 1.08 GB) take 180 us, 6.0 of the 6.5 TB/s that a plain read of 4 GiB reaches, and 5 us
+// to join the parts; 32 requests of 1 to 8192 tokens (32 / 8 heads, e4m3, 277 MB) 49 + 5 us, 5.6 TB/s.
 // Short calls are bound by the way to the first product (lengths -> table -> scales and codes,
 // a memory latency each): one request of 2048 tokens takes 6 + 4 us.  Many query rows are bound
-// by the vector units (scores and unpacking take three times the matrix units' cycles): four
-// prompt slices of 90 to 300 tokens, 22.5 GFLOP, 50 us.
+// by the vector units (scores and unpacking take three times the matrix units' cycles) and by how
+// the row tiles fill the chip: four prompt slices of 90 to 300 tokens, 22.5 GFLOP, are 113 row tiles
+// a head on 96 places and take 58 + 5 us, 52 in a row of such calls.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -106,8 +107,8 @@ __device__ __forceinline__ int wave_scan(int v) {
 // places that the chip has for a head's workgroups is a chunk of tokens, a request is cut into
 // ceil(tokens / chunk) even parts, and the workgroup's (request, part, row tile) follows from
 // the prefix sums of their counts.  One round of workgroups: two or four rounds of shorter
-// ones, which end more evenly, lost more on the way to their first product (32 requests of
-// 32768 tokens 201 and 207 us against 193, one of 131072 64 and 77 against 57).
+// ones, which end more evenly, lost more on the way to their first product (with an earlier form,
+// 32 requests of 32768 tokens 201 and 207 us against 193, one of 131072 64 and 77 against 57).
 __device__ __forceinline__ int tiles_of(const Seq& s) { return s.n_new < 1 ? 0 : max(s.hi - s.lo, 1); }
 __device__ __forceinline__ int row_tiles_of(const AttnArgs& a, const Seq& s) { return (s.rows + (1 << a.row_shift) - 1) >> a.row_shift; }
 
@@ -260,15 +261,18 @@ __device__ __forceinline__ float lane_float(float v, int l) {
 // Workgroups a CU (waves a SIMD) that a variant's registers are held to: enough loads in
 // flight for the memory, and as many parts as there are places for them.  (With a second
 // buffer for a step's codes int8 at head_dim 128 took 213 registers, two waves, and 212 us
-// for the 1.08 GB of the largest decode step.)
+// for the 1.08 GB of the largest decode step.  At head_dim 64 and one row tile the registers would let
+// in a fifth wave; counted as places they make shorter parts: 4 requests of 8000 tokens 18.1 us against
+// 15.7, a verify step of 8 x 5 15.4 against 13.9, 32 of up to 8192 32.4 against 32.3.)
 constexpr int per_cu(int dq, int nt) { return nt == 1 ? (dq <= 2 ? 4 : dq == 3 ? 3 : 2) : (dq == 1 ? 4 : dq == 2 ? 3 : 2); }
 
 // DQ = head_dim / 64, NT = tiles of 16 query rows, EXT: cap, window or distance bias, WAVES: four
 // to a part, or one, which waits for no other and finds its share alone, where the requests
 // outnumber the places that parts of four waves have.  Four waves against one there:
-// 1000 requests of up to 600 tokens (64 / 4 heads x 128, e4m3) 166 and 103 us, 256 of up to 1000
-// (32 / 8 x 128, int8) 69 and 64, 160 of up to 8192 250 and 245, 40 of up to 600 with 32 / 32 heads
-// 27.7 and 28.8.
+// 1000 requests of up to 600 tokens (64 / 4 heads x 128, e4m3) 167 and 103 us, 256 of up to 1000
+// (32 / 8 x 128, int8) 68 and 64.5, 160 of up to 8192 (e4m3) 241 and 237, 40 of up to 600 with 32 / 32
+// heads 27.9 and 28.8; with fewer requests, 100 of up to 600 (32 / 8) 22.8 and 25.7, 64 of 2000 to 4000
+// 79.4 and 78.7.
 template <bool E4M3, int DQ, int NT, bool EXT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_cu(DQ, NT)))) void attn_kernel(AttnArgs a) {
     constexpr int D = 64 * DQ, ROWS = 16 * NT, PITCH = 68;
@@ -463,8 +467,13 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
                     sum[t] += p[h][i];
                     p[h][i] *= vs[h];
                 }
-            // the weights' rounding to bf16 (at most 2^-9 of each) averages out over a row's
-            // tokens; their sum is taken before it
+            // The matrix unit takes bf16: a weight times its value scale is off by at most 2^-8 of
+            // itself, and so is o where one token has the weight, or where equal weights share a block's scale
+            // and so their rounding; over many tokens of unlike weights the errors mostly cancel (o off by
+            // 2.1e-3 to 2.3e-3 in the mean, its own rounding to bf16 among it, which alone is 1.65e-3).
+            // With what is left of each weight as a second operand that is all, for prompt slices of 61 us
+            // instead of 53, verify steps of 16 x 8 41 instead of 38, single tokens 0 to 2% more, and
+            // scratch memory in six variants.  The sums are of the weights before it.
             const u32x4 w = {pack_bf16(p[0][0], p[0][1]), pack_bf16(p[0][2], p[0][3]), pack_bf16(p[1][0], p[1][1]), pack_bf16(p[1][2], p[1][3])};
             pf[t] = __builtin_bit_cast(bf16x8, w);
         }
@@ -568,8 +577,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
 // The parts of the split row tiles: a workgroup for each four query rows of a tile and head,
 // WAVES waves a row; lanes over channels, waves over parts.
 // A second launch: joining in the last workgroup to arrive needs partial results that
-// pass the XCDs' L2s and a counter, which took longer (one request of 2048 tokens 10.5
-// against 8.9 us, one of 131072 84 against 57).
+// pass the XCDs' L2s and a counter, which took longer (with an earlier form of the kernel above, one
+// request of 2048 tokens 10.5 against 8.9 us, one of 131072 84 against 57).
 constexpr int kJoinRows = 4, kJoinAhead = 8;
 
 template <int DQ, int WAVES>
@@ -675,7 +684,9 @@ static int places_of(const mbd_kv_cache* c, int nt, int waves) {
 // The parts and their memory, for tiles of p->nt * 16 query rows and parts of p->waves waves.
 static void lay_out(const mbd_kv_cache* c, int64_t tiles, int64_t seq_tiles, Plan* p) {
     p->places = places_of(c, p->nt, p->waves);
-    const int64_t least = p->waves * kStep;                                // tiles of a part: a step a wave
+    // tiles of a part: a step a wave (with two, three: one request of 2048 tokens 11.4, 12.7 us against
+    // 10.2, a verify step of 8 x 5 13.5, 13.5 against 13.9, 8 of up to 4096 13.4, 13.7 against 13.9)
+    const int64_t least = p->waves * kStep;
     p->longest = (seq_tiles + least - 1) / least;
     p->split = p->longest > 1 && p->places > 1;
     p->parts = p->split ? std::min<int64_t>(2 * p->places, tiles * p->longest) : 0;
@@ -733,7 +744,9 @@ static void launch(const AttnArgs& a, const Plan& p, int64_t items, bool ext, hi
         const int rows = std::min(16 * NT, a.max_new * a.group);
         // (at most four workgroups a tile: where few tiles are split, most find nothing to do)
         const dim3 joins(unsigned(a.n_splits), unsigned(a.n_kv), unsigned(std::min((rows + kJoinRows - 1) / kJoinRows, 4)));
-        // few row tiles can have many parts each: more waves over them
+        // few row tiles can have many parts each: more waves over them (four against one, one request of
+        // 131072 tokens 58.8 and 69.3 us, 8 of up to 4096 13.9 and 14.8, one of 500 10.0 and 8.9; with more row
+        // tiles, 32 of up to 8192 54.9 and 53.7, a verify step of 8 x 5 15.3 and 14.2)
         if (a.n_seqs * int64_t(p.row_tiles) * 8 < p.places)
             hipLaunchKernelGGL((join_kernel<DQ, 4>), joins, dim3(64 * kJoinRows * 4), 0, s, a, 16 * NT);
         else
