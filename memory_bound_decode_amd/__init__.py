@@ -363,6 +363,7 @@ def mbd_kv_gather(cache: KvCache, slots, k_out, v_out, stream=None) -> None:
 
 
 def mbd_kv_attn_workspace_bytes(cache: KvCache, n_heads: int, n_seqs: int, max_new: int, max_blocks: int) -> int:
+    """Bytes of mbd_kv_attn's workspace for these sizes and all smaller ones."""
     b = ctypes.c_uint64(0)
     check(lib().mbd_kv_attn_workspace_bytes(cache.ref(), n_heads, n_seqs, max_new, max_blocks, ctypes.byref(b)),
           "mbd_kv_attn_workspace_bytes")
