@@ -321,11 +321,11 @@ mbd_status mbd_encode_cassandra(const uint16_t* w, const float* act_norm, int64_
                                 void* const* sec, void* ws, uint64_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------ KV cache
- * The other half of what a decode step reads: a paged cache of 8-bit keys and values.
- * A pool of n_blocks blocks holds block_size tokens each; a request's block table
- * names its blocks in order.  Each (block, KV head) has one fp32 scale for its keys
- * and one for its values; a value is code * scale.
+ * The other half of what a decode step reads: a paged cache of keys and values in 8 or
+ * 4 bits.  A pool of n_blocks blocks holds block_size tokens each; a request's block
+ * table names its blocks in order.  A value is code * scale.
  *
+ * 8 bits: each (block, KV head) has one fp32 scale for its keys and one for its values.
  * Formats, x the value to store, s the scale, amax the largest finite |x| among the
  * tokens that one call brings to a (block, head):
  *   MBD_KV_INT8  code = clamp(rne(x / s), -127, 127); wanted s = amax * (1/127), the
@@ -344,8 +344,25 @@ mbd_status mbd_encode_cassandra(const uint16_t* w, const float* act_norm, int64_
  * of (token t of the tile, channel d):
  *   keys    (d/64)*1024 + (d/16%4)*256 + t*16 + d%16
  *   values  (d/64)*1024 + (t/4)*256 + (d/4%16)*16 + d%4*4 + t%4
- * Scales: fp32 [n_blocks][n_heads].  None of it needs to be cleared before use.  */
-typedef enum { MBD_KV_INT8 = 1, MBD_KV_E4M3 = 2 } mbd_kv_format;
+ * Scales: fp32 [n_blocks][n_heads].  None of it needs to be cleared before use.
+ *
+ * 4 bits, MBD_KV_MXFP4: each 32 neighbouring channels of a token's head (channels 32 G to
+ * 32 G + 31 are group G) have a power of two as their scale, 2^e, kept as the byte e + 127;
+ * 4.25 bits a value.  e is the smallest whole number from -100 to 125 with amax <= 7 * 2^e,
+ * amax the group's largest finite |x|: what lies between 6 and 7 times 2^e becomes 6, by at
+ * most the half step that its neighbours are rounded by.  code = e2m1(x / 2^e): one of 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6, nearest, a tie to the even code, saturating at 6, bit 3 the sign of x.
+ * NaN is stored as 0; an infinity as the largest code.  A token's codes depend on that token
+ * alone, so any slots in any order can be appended, each at most once a call.
+ * Codes: uint8 [n_blocks][n_heads][block_size/16] tiles of 16 tokens x head_dim / 2 bytes, the
+ * even channel of a pair in the low half of its byte.  Byte of (token t, channel d):
+ *   keys    (d/32)*256 + t*16 + d%32/2
+ *   values  (d/128)*1024 + (t/4)*256 + (d%128/8)*16 + (t%4)*4 + d%8/2, or, where head_dim is
+ *           64 or 192, for its last 64 channels
+ *           (d/128)*1024 + (t/4)*128 + (d%64/4)*8 + (t%4)*2 + d%4/2
+ * Scales: uint8 [n_blocks][n_heads][block_size/16][head_dim/32][16], the byte of (group, token)
+ * of a tile.  None of it needs to be cleared before use.  */
+typedef enum { MBD_KV_INT8 = 1, MBD_KV_E4M3 = 2, MBD_KV_MXFP4 = 3 } mbd_kv_format;
 typedef enum { MBD_BF16 = 1, MBD_F32 = 2 } mbd_dtype;
 
 typedef struct {
@@ -356,8 +373,8 @@ typedef struct {
     int64_t n_blocks;     /* n_blocks * block_size < 2^31               */
     void* k_codes;        /* device, 16-byte aligned; offsets may pass  */
     void* v_codes;        /*   32 bits                                  */
-    float* k_scale;       /* device, 4-byte aligned                     */
-    float* v_scale;
+    void* k_scale;        /* device, 4-byte aligned: fp32, or uint8 for */
+    void* v_scale;        /*   MBD_KV_MXFP4                             */
 } mbd_kv_cache;
 
 /* Block tables of n_seqs requests over one pool, and its free blocks as a stack:
@@ -406,12 +423,38 @@ mbd_status mbd_kv_slots(const mbd_kv_pool* pool, const int32_t* new_tokens, cons
  * 16-byte aligned; k_stride, v_stride: elements from one token to the next, multiples
  * of 8, at least n_heads * head_dim (so both may be slices of one projection).  slots
  * [T] device int32: the slot of each token; a slot outside the cache skips its token.
- * The tokens that a call brings to one block stand next to each other in rising slots
+ * In 8 bits the tokens that a call brings to one block stand next to each other in rising slots
  * (as mbd_kv_slots writes them); otherwise that block's codes and scale are unspecified.
  * T = 0 does nothing; T is at most 2^24.  Errors: EINVAL, ESHAPE, EALIGN, EHIP. */
 mbd_status mbd_kv_append(const mbd_kv_cache* cache, const void* k, const void* v, int32_t dtype,
                          int64_t k_stride, int64_t v_stride, const int32_t* slots, int32_t T,
                          void* stream);
+
+/* Rotation of keys and queries by their tokens' positions, from a table that the caller keeps.
+ * Of each head the first rot_dim channels are turned in pairs (a, b), pair j by the angle
+ * whose cosine and sine stand at j and rot_dim/2 + j of the position's row:
+ *   a' = a cos - b sin,  b' = b cos + a sin     each product and sum rounded to fp32
+ * Pair j is channels (j, j + rot_dim/2), or (2j, 2j + 1) where interleaved is not 0. */
+typedef struct {
+    const float* table;   /* device fp32 [n_positions][rot_dim], 16-byte aligned         */
+    int32_t n_positions;  /* >= 1                                                        */
+    int32_t rot_dim;      /* a multiple of 8, 8 to head_dim                              */
+    int32_t interleaved;
+    int32_t n_q_heads;    /* heads of q, 1..65535; 0: no queries, q and q_out are unused */
+    const void* q;        /* device [T][n_q_heads][head_dim] of the keys' dtype          */
+    uint16_t* q_out;      /* device bf16 [T][n_q_heads][head_dim]                        */
+    int64_t q_stride;     /* elements from one token to the next: multiples of 8, at     */
+    int64_t q_out_stride; /*   least n_q_heads * head_dim; q and q_out 16-byte aligned   */
+} mbd_rope;
+
+/* mbd_kv_append with the keys turned on the way (the values are not), and the same tokens'
+ * queries turned into q_out, rounded to bf16 once (as mbd_kv_attn takes them).  positions [T]
+ * device int32, as mbd_kv_slots writes them.  A token whose position is outside the table is
+ * not stored, and its row of q_out stays as it was; a slot outside the cache skips the
+ * token's key and value alone.  q_out may not overlap q, k or v.  Errors as mbd_kv_append. */
+mbd_status mbd_kv_append_rope(const mbd_kv_cache* cache, const mbd_rope* rope, const void* k, const void* v,
+                              int32_t dtype, int64_t k_stride, int64_t v_stride, const int32_t* slots,
+                              const int32_t* positions, int32_t T, void* stream);
 
 /* Dense keys and values of cached tokens: k_out, v_out [T][n_heads][head_dim] of dtype,
  * 16-byte aligned: code * scale in fp32, then rounded to dtype.  Any slots in any order;
@@ -452,10 +495,12 @@ typedef struct {
  * out bf16 [T][n_heads][head_dim], 16-byte aligned: as the x of mbd_gemv where out_stride
  * = n_heads * head_dim.  lse fp32 [T][n_heads], natural logarithm of the softmax's sum, or
  * NULL.  Rows of no request, and a request's rows past its first max_new, stay as they
- * were.  Sums and statistics are fp32 (so a product q . k of codes, an uncapped score times
- * log2(e), and 2^8 times the sum of a channel's |v| over the tokens a query sees have to
- * stay below 2^127); softmax weights times value scales enter the second product as bf16, each off
- * by at most 2^-8 of itself.  The order of every sum depends on the arguments alone.
+ * were.  Sums and statistics are fp32 (so a product q . k of codes (in 4 bits, of keys), an
+ * uncapped score times log2(e), and 2^8 times the sum of a channel's |v| over the tokens a query
+ * sees have to stay below 2^127); softmax weights (in 8 bits times value scales) enter the second
+ * product as bf16, each off by at most 2^-8 of itself.  In 4 bits q enters the first product as
+ * the sum of two 8-bit floats, each channel off by at most 2^-21 of its row's largest.  The order
+ * of every sum depends on the arguments alone.
  * ws: device workspace of mbd_kv_attn_workspace_bytes, 16-byte aligned, contents
  * overwritten; may be NULL where that is 0.  One made for the most n_seqs, max_new and
  * max_blocks of a program serves its smaller calls of the same heads too.  Calls that

@@ -16,7 +16,7 @@ from ._native import (  # noqa: F401
     MBD_CASSANDRA, MBD_EALIGN, MBD_EFORMAT, MBD_EHIP, MBD_EINVAL, MBD_ENOMEM, MBD_ERANGE,
     MBD_CASSANDRA_MX, MBD_ESHAPE, MBD_INT4_G128, MBD_MX32, MBD_OK, MBD_TERNARY_B128, MBD_TERNARY_SKIP, MbdDWeights, MbdError,
     MbdEncodePlan, MbdPackParams, MbdSection, MbdStats, check, lib,
-    MBD_BF16, MBD_F32, MBD_KV_E4M3, MBD_KV_INT8, MbdKvAttnArgs, MbdKvCache, MbdKvPool,
+    MBD_BF16, MBD_F32, MBD_KV_E4M3, MBD_KV_INT8, MBD_KV_MXFP4, MbdKvAttnArgs, MbdKvCache, MbdKvPool, MbdRope,
 )
 
 SECTION_NAMES = {
@@ -264,18 +264,24 @@ def _queue(stream, here):
 
 
 class KvCache:
-    """An 8-bit paged KV cache over the caller's device tensors: codes uint8
-    [n_blocks][n_heads][block_size * head_dim] in the tile order of mbd.h, scales fp32
-    [n_blocks][n_heads].  Holds the tensors and the mbd_kv_cache that points at them."""
+    """A paged KV cache over the caller's device tensors, in the layouts of mbd.h.  8 bits: codes
+    uint8 [n_blocks][n_heads][block_size * head_dim], scales fp32 [n_blocks][n_heads].  MBD_KV_MXFP4:
+    codes uint8 [n_blocks][n_heads][block_size * head_dim / 2], scales uint8 [n_blocks][n_heads]
+    [block_size * head_dim / 32].  Holds the tensors and the mbd_kv_cache that points at them."""
 
     def __init__(self, fmt: int, block_size: int, head_dim: int, k_codes, v_codes, k_scale, v_scale):
         import torch
-        if k_codes.dim() != 3 or k_codes.shape[2] != block_size * head_dim:
-            raise ValueError("codes must be [n_blocks][n_heads][block_size * head_dim]")
+        mx = fmt == MBD_KV_MXFP4
+        per, what = (2, "block_size * head_dim / 2") if mx else (1, "block_size * head_dim")
+        if k_codes.dim() != 3 or k_codes.shape[2] * per != block_size * head_dim:
+            raise ValueError("codes must be [n_blocks][n_heads][%s]" % what)
+        scales = (*k_codes.shape[:2], block_size * head_dim // 32) if mx else k_codes.shape[:2]
+        scale_type = torch.uint8 if mx else torch.float32
         for t, shape, dtype in ((k_codes, k_codes.shape, torch.uint8), (v_codes, k_codes.shape, torch.uint8),
-                                (k_scale, k_codes.shape[:2], torch.float32), (v_scale, k_codes.shape[:2], torch.float32)):
+                                (k_scale, scales, scale_type), (v_scale, scales, scale_type)):
             if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-                raise ValueError("codes are contiguous uint8 tensors of one shape, scales contiguous fp32 [n_blocks][n_heads]")
+                raise ValueError("codes are contiguous uint8 tensors of one shape, scales contiguous " +
+                                 ("uint8 [n_blocks][n_heads][block_size * head_dim / 32]" if mx else "fp32 [n_blocks][n_heads]"))
         for t in (k_codes, v_codes, k_scale, v_scale):
             self.gpu = _gpu("the cache", t)
         self.tensors = dict(k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale)
@@ -288,8 +294,11 @@ class KvCache:
     @classmethod
     def empty(cls, fmt: int, n_blocks: int, n_heads: int, head_dim: int, block_size: int, device="cuda"):
         import torch
-        codes = [torch.empty((n_blocks, n_heads, block_size * head_dim), dtype=torch.uint8, device=device) for _ in range(2)]
-        scales = [torch.empty((n_blocks, n_heads), dtype=torch.float32, device=device) for _ in range(2)]
+        mx = fmt == MBD_KV_MXFP4
+        code_shape = (n_blocks, n_heads, block_size * head_dim // (2 if mx else 1))
+        scale_shape = (n_blocks, n_heads, block_size * head_dim // 32) if mx else (n_blocks, n_heads)
+        codes = [torch.empty(code_shape, dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.empty(scale_shape, dtype=torch.uint8 if mx else torch.float32, device=device) for _ in range(2)]
         return cls(fmt, block_size, head_dim, *codes, *scales)
 
     def ref(self):
@@ -345,6 +354,39 @@ def mbd_kv_append(cache: KvCache, k, v, slots, stream=None) -> None:
     st = lib().mbd_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), MBD_BF16 if dt is torch.bfloat16 else MBD_F32, ks, vs, slots.data_ptr(), T,
                              _queue(stream, here))
     check(st, "mbd_kv_append")
+
+
+_ROPE = struct.Struct("@P4iPPqq")                      # MbdRope, in the machine's own layout
+
+
+def mbd_kv_append_rope(cache: KvCache, k, v, slots, positions, table, q=None, q_out=None, interleaved: bool = False, stream=None) -> None:
+    """mbd_kv_append with the first table.shape[1] channels of each head's keys turned by their
+    positions: table fp32 [n_positions][rot_dim], a row its angles' cosines, then their sines.  q
+    [T][heads][head_dim] of the keys' type is turned into q_out, bf16."""
+    import torch
+    here, heads, dim, T, dt = _gpu("k", k), cache.n_heads, cache.head_dim, k.shape[0], k.dtype
+    _held(here, "cache", cache)
+    ks, vs = _rows(here, "k", k, heads, dim, (torch.bfloat16, torch.float32)), _rows(here, "v", v, heads, dim, (dt,))
+    if v.shape[0] != T:
+        raise ValueError("k and v must have as many tokens")
+    _ints(here, torch.int32, ("slots", slots, T), ("positions", positions, T))
+    if table.dim() != 2 or table.dtype is not torch.float32 or not table.is_contiguous():
+        raise ValueError("table must be contiguous fp32 [n_positions][rot_dim]")
+    if table.get_device() != here:
+        _refuse(here, "table", table, "fp32")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    q_heads, q_ptr, out_ptr, qs, outs = 0, 0, 0, 0, 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T or q_out.shape[0] != T:
+            raise ValueError("q and q_out must be [T][heads][head_dim], with as many tokens as k")
+        q_heads = q.shape[1]
+        qs, outs = _rows(here, "q", q, q_heads, dim, (dt,)), _rows(here, "q_out", q_out, q_heads, dim, (torch.bfloat16,))
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    rope = _ROPE.pack(table.data_ptr(), table.shape[0], table.shape[1], bool(interleaved), q_heads, q_ptr, out_ptr, qs, outs)
+    st = lib().mbd_kv_append_rope(cache._ref, rope, k.data_ptr(), v.data_ptr(), MBD_BF16 if dt is torch.bfloat16 else MBD_F32, ks, vs,
+                                  slots.data_ptr(), positions.data_ptr(), T, _queue(stream, here))
+    check(st, "mbd_kv_append_rope")
 
 
 def mbd_kv_gather(cache: KvCache, slots, k_out, v_out, stream=None) -> None:

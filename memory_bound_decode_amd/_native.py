@@ -10,7 +10,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmbd.so")
 MBD_OK, MBD_EINVAL, MBD_ESHAPE, MBD_EALIGN, MBD_ERANGE, MBD_EFORMAT, MBD_EHIP, MBD_ENOMEM = range(8)
 MBD_TERNARY_B128, MBD_INT4_G128, MBD_CASSANDRA, MBD_MX32, MBD_TERNARY_SKIP, MBD_CASSANDRA_MX = 1, 2, 3, 4, 5, 6
 MBD_MAX_SECTIONS = 8
-MBD_KV_INT8, MBD_KV_E4M3 = 1, 2
+MBD_KV_INT8, MBD_KV_E4M3, MBD_KV_MXFP4 = 1, 2, 3
 MBD_BF16, MBD_F32 = 1, 2
 
 
@@ -61,6 +61,11 @@ class MbdKvAttnArgs(Structure):
                 ("q_stride", c_int64), ("out_stride", c_int64)]
 
 
+class MbdRope(Structure):
+    _fields_ = [("table", c_void_p), ("n_positions", c_int32), ("rot_dim", c_int32), ("interleaved", c_int32), ("n_q_heads", c_int32),
+                ("q", c_void_p), ("q_out", c_void_p), ("q_stride", c_int64), ("q_out_stride", c_int64)]
+
+
 SIGNATURES = {
     "mbd_pack": (c_int32, [c_int32, POINTER(c_uint16), c_int64, c_int64, c_void_p,
                            POINTER(MbdPackParams), POINTER(c_void_p)]),
@@ -86,6 +91,9 @@ SIGNATURES = {
     "mbd_kv_slots": (c_int32, [POINTER(MbdKvPool)] + [c_void_p] * 4 + [c_int32] + [c_void_p] * 8),
     "mbd_kv_append": (c_int32, [POINTER(MbdKvCache), c_void_p, c_void_p, c_int32, c_int64, c_int64, c_void_p, c_int32,
                                 c_void_p]),
+    # the rotation by address: the binding packs an MbdRope as bytes
+    "mbd_kv_append_rope": (c_int32, [POINTER(MbdKvCache), c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int64, c_void_p, c_void_p, c_int32,
+                                     c_void_p]),
     "mbd_kv_gather": (c_int32, [POINTER(MbdKvCache), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p]),
     "mbd_kv_attn_workspace_bytes": (c_int32, [POINTER(MbdKvCache), c_int32, c_int32, c_int32, c_int32, POINTER(c_uint64)]),
     # the arguments by address: the binding packs an MbdKvAttnArgs as bytes

@@ -1,12 +1,15 @@
-// The paged 8-bit KV cache around its attention: block tables and slot maps from
-// request lengths, the append that quantises new keys and values, and the read-back.
+// The paged KV cache around its attention: block tables and slot maps from request
+// lengths, the append that quantises new keys and values (turned by their positions on the
+// way, if asked), and the read-back; the 8-bit formats here, the 4-bit one in kv_mxfp4.h.
 // A decode step's time is the bytes that it reads ([Bolt] background); beside the
 // weights those are the cached keys and values, halved here against bf16.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
-#include "kv_common.h"
+#include "kv_mxfp4.h"
+#include "kv_turn.h"
 
 namespace mbd {
 namespace kv {
@@ -225,6 +228,7 @@ struct AppendArgs {
     const int32_t* slots;
     int32_t n_slots;      // slots of the cache
     int32_t T, window, n_heads, head_dim, shift;
+    Turn turn;            // table is NULL: no rotation
 };
 
 template <bool E4M3>
@@ -336,12 +340,18 @@ template <> struct Quad<uint16_t> {
     }
 };
 
+// (of a quad that turned() fills, nothing is loaded as it lies)
+template <class X, class T> __device__ __forceinline__ void load_quad(X& x, const T* p) {
+    if constexpr (std::is_same<X, Quad<T>>::value) x.load(p);
+}
+
 // The tokens of one block that the call brings, places [fill, end), for one head's keys
 // or values, by THREADS threads (a wave, or a workgroup of 256), each with KEEP units in
 // registers between the maximum and the codes (more are read again).  A unit is 16
 // bytes of a code tile: lane (g, m) of slab s holds, of a key tile, token m and channels
-// 64s + 16g .. +16; of a value tile, tokens 4g .. +4 and channels 64s + 4m .. +4.
-template <bool E4M3, bool V, class T, int THREADS, int KEEP>
+// 64s + 16g .. +16; of a value tile, tokens 4g .. +4 and channels 64s + 4m .. +4.  TURN: keys are
+// turned as they are loaded, and held in fp32 from there.
+template <bool E4M3, bool V, bool TURN, class T, int THREADS, int KEEP>
 __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, int64_t block, int fill, int end, int head, uint32_t* lds) {
     const int tid = THREADS == 64 ? threadIdx.x & 63 : threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, m = lane & 15;
@@ -350,10 +360,12 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
     uint8_t* codes = a.codes[V] + ((bh * D) << a.shift);
     const int64_t stride = a.stride[V];
     const T* row0 = static_cast<const T*>(a.x[V]) + int64_t(token) * stride + int64_t(head) * D;
+    constexpr bool turn = TURN && !V;
+    using X = Quad<typename std::conditional<turn, float, T>::type>;
     const float old_scale = fill > 0 ? a.scales[V][bh] : 0.f;
     const int tile0 = fill / kTok, chunks = ((end - 1) / kTok + 1 - tile0) * slabs;   // 64 units each
 
-    Quad<T> x[KEEP][4];
+    X x[KEEP][4];
     u32x4 old[THREADS == 64 ? KEEP : 1];
     auto first_token = [&](int tile) { return tile * kTok + (V ? 4 * g : m); };
     auto unit_at = [&](int tile, int s) { return reinterpret_cast<u32x4*>(codes + int64_t(tile) * kTok * D + s * 1024 + lane * 16); };
@@ -371,23 +383,35 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
             const int c = c0 + i * (THREADS / 64) + wave;
             const int tile = tile0 + c / slabs, s = c % slabs, first = first_token(tile);
             const T* from = row0 + (first - fill) * stride + 64 * s + (V ? 4 * m : 16 * g);
+            if constexpr (turn) {
+                const int32_t row = first - fill;                // of a unit's one token in the run
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[i][k].clear();
+                if (c < chunks && first >= fill && first < end) {
+                    const float* angles = a.turn.table + int64_t(a.turn.positions[token + row]) * a.turn.rot;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[i][k].v = turned(a.turn, row0 + row * stride, angles, 64 * s + 16 * g + 4 * k);
+                }
+                if constexpr (THREADS == 64) old[i] = boundary(c < chunks && !all_new(tile), tile, s);
+                continue;
+            }
             if (c < chunks && all_new(tile)) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[i][k].load(from + (V ? k * stride : 4 * k));
+                for (int k = 0; k < 4; ++k) load_quad(x[i][k], from + (V ? k * stride : 4 * k));
                 continue;
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int tok = V ? first + k : first;
                 x[i][k].clear();
-                if (c < chunks && tok >= fill && tok < end) x[i][k].load(from + (V ? k * stride : 4 * k));
+                if (c < chunks && tok >= fill && tok < end) load_quad(x[i][k], from + (V ? k * stride : 4 * k));
             }
             if constexpr (THREADS == 64) old[i] = boundary(c < chunks, tile, s);   // early: few waves, so latency counts
         }
     };
     constexpr int round = KEEP * (THREADS / 64);
     const bool once = chunks <= round;
-    typename Quad<T>::Top most{};
+    typename X::Top most{};
     for (int c0 = 0; c0 < chunks; c0 += round) {
         load(c0);
 #pragma unroll
@@ -407,7 +431,7 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
         }
         return uint32_t(__builtin_amdgcn_readfirstlane(int(v)));
     };
-    uint32_t top = reduce(Quad<T>::bits(most));
+    uint32_t top = reduce(X::bits(most));
     const bool finite = top < 0x7f800000u;
     if (!finite) {                       // the largest of the finite values
         top = 0;
@@ -478,14 +502,15 @@ struct Look {
     uint64_t starts, more[2];
 };
 
+template <bool TURN>
 __device__ __forceinline__ Look look_at(const AppendArgs& a, int32_t t0) {
     const int lane = threadIdx.x & 63, in_block = (1 << a.shift) - 1;
     int32_t slot[2], prev[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int32_t t = t0 + 64 * h + lane;
-        slot[h] = t < a.T ? a.slots[t] : -1;
-        prev[h] = t < a.T && t > 0 ? a.slots[t - 1] : -2;
+        slot[h] = t < a.T ? slot_at<TURN>(a.slots, a.turn, t) : -1;
+        prev[h] = t < a.T && t > 0 ? slot_at<TURN>(a.slots, a.turn, t - 1) : -2;
     }
     Look k;
     k.slot = slot[0];
@@ -499,6 +524,7 @@ __device__ __forceinline__ Look look_at(const AppendArgs& a, int32_t t0) {
 }
 
 // Tokens of the run that begins at bit l, `first` its slot.
+template <bool TURN>
 __device__ __forceinline__ int run_length(const AppendArgs& a, const Look& k, int32_t t0, int l, int32_t first) {
     const uint64_t rest = l < 63 ? k.more[0] >> (l + 1) : 0;
     int count = 1 + __builtin_ctzll(~rest);            // a shift leaves a zero at the top
@@ -508,29 +534,39 @@ __device__ __forceinline__ int run_length(const AppendArgs& a, const Look& k, in
     const int lane = threadIdx.x & 63, most = (1 << a.shift) - (first & ((1 << a.shift) - 1));
     for (int at = count; at < most; at += 64) {        // a long run of a large block
         const int i = at + lane;
-        const uint64_t off = ~__ballot(i < most && t0 + l + i < a.T && a.slots[t0 + l + i] == first + i);
+        const uint64_t off = ~__ballot(i < most && t0 + l + i < a.T && slot_at<TURN>(a.slots, a.turn, t0 + l + i) == first + i);
         count = at + (off ? __builtin_ctzll(off) : 64);
         if (off) break;
     }
     return count;
 }
 
+// An octet for each thread of the queries of a window's tokens, `part` the workgroup.
+template <class T>
+__device__ __forceinline__ void turn_queries(const AppendArgs& a, int32_t t0, int part) {
+    const int octets = a.turn.n_q_heads * (a.head_dim / 8), e = part * 256 + threadIdx.x, i = e / octets;
+    if (i < a.window && t0 + int64_t(i) < a.T) turn_query<T>(a.turn, t0 + i, e - i * octets, a.head_dim);
+}
+
 // Few tokens: a wave for each (token, head, keys or values), busy where the token begins
 // a run.  The waves of a workgroup take neighbouring heads, which lie side by side.  Bound by
 // its chain of loads (slots -> values, old codes, scale): one token 5.2 us, a verify step of 48
 // requests x 0..9 tokens (fp32, 236 rows) 7.7 us.
-template <bool E4M3, class T>
+template <bool E4M3, class T, bool TURN>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
-    const int hw = blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int hw = blockIdx.x * 4 + (threadIdx.x >> 6), own = (2 * a.n_heads + 3) / 4;
+    const int32_t t0 = int32_t(blockIdx.y);
+    if constexpr (TURN) {
+        if (int(blockIdx.x) >= own) return turn_queries<T>(a, t0, blockIdx.x - own);
+    }
     if (hw >= 2 * a.n_heads) return;
     const int head = hw % a.n_heads;
-    const int32_t t0 = int32_t(blockIdx.y);
-    const Look k = look_at(a, t0);
+    const Look k = look_at<TURN>(a, t0);
     if (!k.starts) return;
     const int32_t first = __builtin_amdgcn_readfirstlane(k.slot);
-    const int fill = first & ((1 << a.shift) - 1), end = fill + run_length(a, k, t0, 0, first);
-    if (hw >= a.n_heads) append_run<E4M3, true, T, 64, 4>(a, t0, first >> a.shift, fill, end, head, nullptr);
-    else append_run<E4M3, false, T, 64, 4>(a, t0, first >> a.shift, fill, end, head, nullptr);
+    const int fill = first & ((1 << a.shift) - 1), end = fill + run_length<TURN>(a, k, t0, 0, first);
+    if (hw >= a.n_heads) append_run<E4M3, true, TURN, T, 64, 4>(a, t0, first >> a.shift, fill, end, head, nullptr);
+    else append_run<E4M3, false, TURN, T, 64, 4>(a, t0, first >> a.shift, fill, end, head, nullptr);
 }
 
 // Many tokens: a workgroup for each (window of tokens, head, keys or values).  Long runs
@@ -538,8 +574,8 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // in flight together; short ones (a wave's units at most) by one wave each.  13 prompts of
 // 19.5k tokens (8 heads x 128, bf16 to int8, 120 MB) take 33.6 us, 3.6 TB/s, from fp32 (200 MB) 48.6
 // us, 4.1 TB/s: the vector units work 42% of that, the rest is the chain of a workgroup's loads.
-template <bool E4M3, class T>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 6 : 4))) void append_window_kernel(AppendArgs a) {
+template <bool E4M3, class T, bool TURN>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TURN ? 3 : sizeof(T) == 2 ? 6 : 4))) void append_window_kernel(AppendArgs a) {
     __shared__ uint32_t lds[4];
     constexpr int kept = 2;            // fewer registers, more workgroups in flight
     const int wave = threadIdx.x >> 6;
@@ -547,19 +583,25 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(sizeof(T) =
     const bool values = int(blockIdx.x) >= a.n_heads;
     for (int64_t at = int64_t(blockIdx.y) * a.window; at < a.T; at += int64_t(gridDim.y) * a.window) {
         const int32_t t0 = int32_t(at);
-        const Look k = look_at(a, t0);                     // the same in every wave
+        if constexpr (TURN) {
+            if (int(blockIdx.x) >= 2 * a.n_heads) {
+                turn_queries<T>(a, t0, blockIdx.x - 2 * a.n_heads);
+                continue;
+            }
+        }
+        const Look k = look_at<TURN>(a, t0);               // the same in every wave
         uint64_t todo = k.starts;
         for (int turn = 0; todo; ++turn) {
             const int l = __builtin_ctzll(todo);
             todo &= todo - 1;
             const int32_t first = __builtin_amdgcn_readlane(k.slot, l), token = t0 + l;
-            const int fill = first & ((1 << a.shift) - 1), end = fill + run_length(a, k, t0, l, first);
+            const int fill = first & ((1 << a.shift) - 1), end = fill + run_length<TURN>(a, k, t0, l, first);
             if (((end - 1) / kTok + 1 - fill / kTok) * a.head_dim > 64 * kept) {
-                if (values) append_run<E4M3, true, T, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
-                else append_run<E4M3, false, T, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
+                if (values) append_run<E4M3, true, TURN, T, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
+                else append_run<E4M3, false, TURN, T, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
             } else if (turn % 4 == wave) {
-                if (values) append_run<E4M3, true, T, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
-                else append_run<E4M3, false, T, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
+                if (values) append_run<E4M3, true, TURN, T, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
+                else append_run<E4M3, false, TURN, T, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
             }
         }
     }
@@ -644,6 +686,77 @@ static mbd_status check_tokens(const void* k, const void* v, int32_t dtype, cons
     return MBD_OK;
 }
 
+static mbd_status check_append(const mbd_kv_cache* cache, const void* k, const void* v, int32_t dtype, int64_t k_stride, int64_t v_stride,
+                               const int32_t* slots, int32_t T) {
+    mbd_status st = check_cache(cache, true);
+    if (st == MBD_OK) st = check_tokens(k, v, dtype, slots, T);
+    if (st != MBD_OK) return st;
+    const int64_t row = int64_t(cache->n_heads) * cache->head_dim;
+    if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8)
+        return fail(MBD_ESHAPE, "token strides must be multiples of 8 and at least n_heads * head_dim");
+    return MBD_OK;
+}
+
+static mbd_status check_rope(const mbd_kv_cache* cache, const mbd_rope* r, const int32_t* positions, int32_t T) {
+    if (!r) return fail(MBD_EINVAL, "NULL argument");
+    if (r->rot_dim < 8 || r->rot_dim > cache->head_dim || r->rot_dim % 8)
+        return fail(MBD_ESHAPE, "rot_dim %d is not a multiple of 8 from 8 to head_dim", r->rot_dim);
+    if (r->n_positions < 1) return fail(MBD_ESHAPE, "n_positions %d below 1", r->n_positions);
+    if (r->n_q_heads < 0 || r->n_q_heads > 65535) return fail(MBD_ESHAPE, "n_q_heads %d outside [0, 65535]", r->n_q_heads);
+    if (!r->table) return fail(MBD_EINVAL, "NULL argument");
+    if (!aligned(r->table, 16)) return fail(MBD_EALIGN, "the table must be 16-byte aligned");
+    const int64_t row = int64_t(r->n_q_heads) * cache->head_dim;
+    if (r->n_q_heads && (r->q_stride < row || r->q_out_stride < row || r->q_stride % 8 || r->q_out_stride % 8))
+        return fail(MBD_ESHAPE, "token strides of queries must be multiples of 8 and at least n_q_heads * head_dim");
+    if (T == 0) return MBD_OK;
+    if (!positions) return fail(MBD_EINVAL, "NULL argument");
+    if (!aligned(positions, 4)) return fail(MBD_EALIGN, "positions must be 4-byte aligned");
+    if (!r->n_q_heads) return MBD_OK;
+    if (!r->q || !r->q_out) return fail(MBD_EINVAL, "NULL argument");
+    if (!aligned(r->q, 16) || !aligned(r->q_out, 16)) return fail(MBD_EALIGN, "q and q_out must be 16-byte aligned");
+    if (r->q == r->q_out) return fail(MBD_EINVAL, "q_out is q");
+    return MBD_OK;
+}
+
+// Both appends, behind their checks.
+static mbd_status append(const mbd_kv_cache* cache, const Turn& turn, const void* k, const void* v, int32_t dtype, int64_t k_stride,
+                         int64_t v_stride, const int32_t* slots, int32_t T, void* stream) {
+    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const bool wide = dtype == MBD_F32;
+    if (cache->fmt == MBD_KV_MXFP4) {
+        if (wide) append4<float>(cache, turn, k, v, k_stride, v_stride, slots, T, s);
+        else append4<uint16_t>(cache, turn, k, v, k_stride, v_stride, slots, T, s);
+        return hip_check("append launch");
+    }
+    // A wave a token up to 4096 waves: above, those that find no run cost more than windows do
+    // (8 heads x 128, waves against windows: 256 requests x 1 token 17.8 and 21.3 us, 128 x 4 21.3 and
+    // 15.2, 128 x 8 fp32 50 and 19, one prompt of 512 12.9 and 10.8).  A window takes the runs that begin in it,
+    // so narrow ones start workgroups that find none; they widen down to 2048 workgroups: one prompt of
+    // 4096 tokens 20.0 us, with 4096 of them 25.4; 512 requests x 8 46.0 and 45.3, with 1024 49.3.
+    const int64_t waves = int64_t(T) * 2 * cache->n_heads;
+    int32_t window = 1;
+    while (window < 64 && waves / window > 2048) window *= 2;
+    const bool few = waves <= 4096;
+    if (few) window = 1;
+    AppendArgs a{{static_cast<uint8_t*>(cache->k_codes), static_cast<uint8_t*>(cache->v_codes)},
+                 {static_cast<float*>(cache->k_scale), static_cast<float*>(cache->v_scale)},
+                 {k, v}, {k_stride, v_stride}, slots, int32_t(cache->n_blocks * cache->block_size), T, window, cache->n_heads,
+                 cache->head_dim, log2_of(cache->block_size), turn};
+    const int own = few ? (2 * cache->n_heads + 3) / 4 : 2 * cache->n_heads;
+    const int turns = turn.table ? (window * turn.n_q_heads * (cache->head_dim / 8) + 255) / 256 : 0;      // the queries' workgroups
+    const dim3 grid(unsigned(own + turns), unsigned(std::min((T + window - 1) / window, 65535)));
+    const auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a); };
+    const auto pick = [&](auto e4m3, auto type, auto turns_keys) {
+        constexpr bool E = decltype(e4m3)::value, U = decltype(turns_keys)::value;
+        using X = decltype(type);
+        few ? run(append_kernel<E, X, U>) : run(append_window_kernel<E, X, U>);
+    };
+    const auto with_turn = [&](auto e4m3, auto type) { turn.table ? pick(e4m3, type, std::true_type{}) : pick(e4m3, type, std::false_type{}); };
+    const auto with_type = [&](auto e4m3) { wide ? with_turn(e4m3, float{}) : with_turn(e4m3, uint16_t{}); };
+    cache->fmt == MBD_KV_E4M3 ? with_type(std::true_type{}) : with_type(std::false_type{});
+    return hip_check("append launch");
+}
+
 }  // namespace kv
 }  // namespace mbd
 
@@ -689,38 +802,20 @@ mbd_status mbd_kv_slots(const mbd_kv_pool* pool, const int32_t* new_tokens, cons
 mbd_status mbd_kv_append(const mbd_kv_cache* cache, const void* k, const void* v, int32_t dtype, int64_t k_stride, int64_t v_stride,
                          const int32_t* slots, int32_t T, void* stream) {
     hip_clear();
-    mbd_status st = kv::check_cache(cache, true);
-    if (st == MBD_OK) st = kv::check_tokens(k, v, dtype, slots, T);
-    if (st != MBD_OK) return st;
-    const int64_t row = int64_t(cache->n_heads) * cache->head_dim;
-    if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8)
-        return fail(MBD_ESHAPE, "token strides must be multiples of 8 and at least n_heads * head_dim");
-    if (T == 0) return MBD_OK;
-    // A wave a token up to 4096 waves: above, those that find no run cost more than windows do
-    // (8 heads x 128, waves against windows: 256 requests x 1 token 17.8 and 21.3 us, 128 x 4 21.3 and
-    // 15.2, 128 x 8 fp32 50 and 19, one prompt of 512 12.9 and 10.8).  A window takes the runs that begin in it,
-    // so narrow ones start workgroups that find none; they widen down to 2048 workgroups: one prompt of
-    // 4096 tokens 20.0 us, with 4096 of them 25.4; 512 requests x 8 46.0 and 45.3, with 1024 49.3.
-    const int64_t waves = int64_t(T) * 2 * cache->n_heads;
-    int32_t window = 1;
-    while (window < 64 && waves / window > 2048) window *= 2;
-    const bool few = waves <= 4096;
-    if (few) window = 1;
-    kv::AppendArgs a{{static_cast<uint8_t*>(cache->k_codes), static_cast<uint8_t*>(cache->v_codes)}, {cache->k_scale, cache->v_scale},
-                     {k, v}, {k_stride, v_stride}, slots, int32_t(cache->n_blocks * cache->block_size), T, window, cache->n_heads,
-                     cache->head_dim, kv::log2_of(cache->block_size)};
-    const dim3 grid(unsigned(few ? (2 * cache->n_heads + 3) / 4 : 2 * cache->n_heads), unsigned(std::min((T + window - 1) / window, 65535)));
-    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    const bool wide = dtype == MBD_F32;
-    const auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a); };
-    if (cache->fmt == MBD_KV_E4M3) {
-        if (few) wide ? run(kv::append_kernel<true, float>) : run(kv::append_kernel<true, uint16_t>);
-        else wide ? run(kv::append_window_kernel<true, float>) : run(kv::append_window_kernel<true, uint16_t>);
-    } else {
-        if (few) wide ? run(kv::append_kernel<false, float>) : run(kv::append_kernel<false, uint16_t>);
-        else wide ? run(kv::append_window_kernel<false, float>) : run(kv::append_window_kernel<false, uint16_t>);
-    }
-    return hip_check("append launch");
+    const mbd_status st = kv::check_append(cache, k, v, dtype, k_stride, v_stride, slots, T);
+    if (st != MBD_OK || T == 0) return st;
+    return kv::append(cache, kv::Turn{}, k, v, dtype, k_stride, v_stride, slots, T, stream);
+}
+
+mbd_status mbd_kv_append_rope(const mbd_kv_cache* cache, const mbd_rope* rope, const void* k, const void* v, int32_t dtype, int64_t k_stride,
+                              int64_t v_stride, const int32_t* slots, const int32_t* positions, int32_t T, void* stream) {
+    hip_clear();
+    mbd_status st = kv::check_append(cache, k, v, dtype, k_stride, v_stride, slots, T);
+    if (st == MBD_OK) st = kv::check_rope(cache, rope, positions, T);
+    if (st != MBD_OK || T == 0) return st;
+    const kv::Turn turn{rope->table, positions, rope->q, rope->q_out, rope->q_stride, rope->q_out_stride, rope->n_positions, rope->rot_dim,
+                        rope->n_q_heads, rope->interleaved != 0};
+    return kv::append(cache, turn, k, v, dtype, k_stride, v_stride, slots, T, stream);
 }
 
 mbd_status mbd_kv_gather(const mbd_kv_cache* cache, const int32_t* slots, int32_t T, int32_t dtype, void* k_out, void* v_out,
@@ -729,8 +824,14 @@ mbd_status mbd_kv_gather(const mbd_kv_cache* cache, const int32_t* slots, int32_
     mbd_status st = kv::check_cache(cache, true);
     if (st == MBD_OK) st = kv::check_tokens(k_out, v_out, dtype, slots, T);
     if (st != MBD_OK || T == 0) return st;
+    if (cache->fmt == MBD_KV_MXFP4) {
+        const hipStream_t s4 = reinterpret_cast<hipStream_t>(stream);
+        if (dtype == MBD_F32) kv::gather4<float>(cache, slots, T, k_out, v_out, s4);
+        else kv::gather4<uint16_t>(cache, slots, T, k_out, v_out, s4);
+        return hip_check("gather launch");
+    }
     kv::GatherArgs a{{static_cast<const uint8_t*>(cache->k_codes), static_cast<const uint8_t*>(cache->v_codes)},
-                     {cache->k_scale, cache->v_scale}, {k_out, v_out}, slots, int32_t(cache->n_blocks * cache->block_size), T,
+                     {static_cast<float*>(cache->k_scale), static_cast<float*>(cache->v_scale)}, {k_out, v_out}, slots, int32_t(cache->n_blocks * cache->block_size), T,
                      cache->n_heads, cache->head_dim, kv::log2_of(cache->block_size)};
     const int per = 256 / (cache->head_dim / 4) * kv::kGatherTokens;
     const dim3 grid(unsigned(cache->n_heads), unsigned(std::min((T + per - 1) / per, 65535)));

@@ -1,0 +1,451 @@
+// Attention over the 4-bit KV cache (MBD_KV_MXFP4): the products of kv_attn.hip,
+//   S^T [tokens][rows] = K [tokens][d] Q^T,  O^T [d][rows] += V^T [d][tokens] P^T
+// with the same sharing of the work.
+//
+// Keys go to the matrix cores as they are stored: v_mfma_scale_f32_16x16x128_f8f6f4 takes e2m1 codes with a
+// power of two for each 32 along the sum, which is a cached group.  Its other operand is the
+// queries in 8 bits: a bf16 of 8 significant bits is the sum of two e4m3 of 4, so a row of Q enters as
+// hi + lo, each with one power of two for the row, and the scores are those of bf16 queries (an
+// element below 2^-17 of its row's largest is off by at most 2^-21 of that).  Two such products of
+// 128 channels take the time of the four bf16 ones that they replace, and nothing is unpacked.  Where 64
+// channels are left (head_dim 64, 192), hi and lo stand in the two halves of one product and the codes
+// are given to both.
+//
+// Values become bf16 (exact; the conversion applies the exponent) and their tokens, which lie in a
+// lane's words one after the other, are paired up by byte permutes: the sum runs over tokens, and
+// their scales differ.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "kv_attn_share.h"
+
+namespace mbd {
+namespace kv {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int per_cu4(int dq, int nt) { return nt == 1 ? (dq <= 2 ? 4 : dq == 3 ? 3 : 2) : (dq == 1 ? 4 : dq == 2 ? 3 : 2); }
+
+// Sixteen bf16 of a query row over 2^(E - 7), E the exponent of the row's largest: below 256, as hi + lo / 16,
+// both e4m3.  The rest behind hi is at most half of its step, 2^4 of 256, so 16 of them fit as well.
+struct QuerySplit { u32x4 hi, lo; };
+
+__device__ __forceinline__ QuerySplit split_query(const u32x4 w0, const u32x4 w1, float down) {
+    QuerySplit r;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t a = q < 2 ? w0[2 * q] : w1[2 * q - 4], b = q < 2 ? w0[2 * q + 1] : w1[2 * q - 3];
+        const float x[4] = {__uint_as_float(a << 16) * down, __uint_as_float(a & 0xffff0000u) * down, __uint_as_float(b << 16) * down,
+                            __uint_as_float(b & 0xffff0000u) * down};
+        int h = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+        h = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], h, true);
+        int l = __builtin_amdgcn_cvt_pk_fp8_f32((x[0] - __builtin_amdgcn_cvt_f32_fp8(h, 0)) * 16.f, (x[1] - __builtin_amdgcn_cvt_f32_fp8(h, 1)) * 16.f, 0, false);
+        l = __builtin_amdgcn_cvt_pk_fp8_f32((x[2] - __builtin_amdgcn_cvt_f32_fp8(h, 2)) * 16.f, (x[3] - __builtin_amdgcn_cvt_f32_fp8(h, 3)) * 16.f, l, true);
+        r.hi[q] = uint32_t(h);
+        r.lo[q] = uint32_t(l);
+    }
+    return r;
+}
+
+// Keys (e2m1, format 4) times queries (e4m3, format 0); the low byte of each scale word counts.
+__device__ __forceinline__ f32x4 key_product(const u32x4 k, const u32x4 q0, const u32x4 q1, f32x4 c, uint32_t k_scale, uint32_t q_scale) {
+    const i32x8 a = {int(k[0]), int(k[1]), int(k[2]), int(k[3]), 0, 0, 0, 0};
+    const i32x8 b = {int(q0[0]), int(q0[1]), int(q0[2]), int(q0[3]), int(q1[0]), int(q1[1]), int(q1[2]), int(q1[3])};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 0, 0, int(k_scale), 0, int(q_scale));
+}
+
+// Channels 2 B and 2 B + 1 of a word of codes as bf16; of the scale its exponent bits alone count.
+template <int B>
+__device__ __forceinline__ uint32_t value_pair(uint32_t w, uint32_t scale) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, __uint_as_float(scale), B));
+}
+
+// Token T's byte of a word of four exponents, in the place of an fp32's exponent; what else stays in
+// the word has no meaning to value_pair.
+template <int T>
+__device__ __forceinline__ uint32_t exponent_of(uint32_t w) {
+    return T == 0 ? w << 23 : T == 1 ? w << 15 : T == 2 ? w << 7 : w >> 1;
+}
+
+// Two channels (low and high halves of t[..]) of eight tokens as the operands of two products.
+__device__ __forceinline__ void pair_up(const uint32_t (&t)[8], bf16x8* even, bf16x8* odd) {
+    u32x4 e, o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        e[i] = __builtin_amdgcn_perm(t[2 * i + 1], t[2 * i], 0x05040100);
+        o[i] = __builtin_amdgcn_perm(t[2 * i + 1], t[2 * i], 0x07060302);
+    }
+    *even = __builtin_bit_cast(bf16x8, e);
+    *odd = __builtin_bit_cast(bf16x8, o);
+}
+
+// (NaN if one is: fmaxf spends an instruction on each operand for those that are signalling)
+__device__ __forceinline__ float max3(float a, float b, float c) { return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c); }
+
+// DQ = head_dim / 64, NT = tiles of 16 query rows, EXT: cap, window, distance bias, or a factor of scores
+// near 0; WAVES: of a part (as attn_kernel).
+template <int DQ, int NT, bool EXT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_cu4(DQ, NT)))) void attn4_kernel(AttnArgs a) {
+    constexpr int D = 64 * DQ, ROWS = 16 * NT, PITCH = 68, F = DQ / 2, H = DQ % 2, S = F + H;   // slabs of 128 channels, of 64
+    __shared__ float merge[WAVES][ROWS][PITCH];     // pitch: rows 4 banks apart
+    __shared__ float merge_m[WAVES][ROWS], merge_l[WAVES][ROWS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, n = lane & 15;
+    const int in_block = (1 << a.shift) - 1;
+    const int want = blockIdx.x / uint32_t(a.n_kv), head = blockIdx.x - want * a.n_kv;
+    Seq sq;
+    int splits;
+    const Item it = find_item(a, want, &sq, &splits);
+    if (head == 0 && threadIdx.x == 0 && want >= splits && want < a.n_splits) a.splits[want] = Split{0, 0, 0, 0, 0, 0};
+    if (it.seq < 0) return;
+    const int row_tiles = row_tiles_of(a, sq), part = it.index / row_tiles;
+    const int row_tile = row_tiles - 1 - (it.index - part * row_tiles);       // the last rows, which see most, first
+    const int r0 = row_tile * ROWS, slot = it.slot + row_tile;
+    const int rows = min(ROWS, sq.rows - r0);
+    // what the first and the last row see bounds what any row sees
+    const int pos_first = sq.p0 + token_of(a, r0), pos_last = sq.p0 + token_of(a, r0 + rows - 1);
+    const int all_end = pos_first + 1, all_begin = a.window > 0 ? max(pos_last, 0) - a.window + 1 : 0;
+    int t0 = sq.lo, t1 = min(sq.hi, (max(pos_last + 1, 0) + kTok - 1) / kTok);
+    if (it.parts > 1) {
+        // (starts that fall, which no request can have, could count rows twice; in range all the same)
+        if (it.split + row_tile >= a.n_splits || slot + int64_t(it.parts - 1) * row_tiles >= a.n_parts) return;
+        const int size = even_part(tiles_of(sq), it.parts);
+        t0 += part * size;
+        t1 = min(t1, t0 + size);
+        if (head == 0 && threadIdx.x == 0 && part == 0) a.splits[it.split + row_tile] = Split{it.parts, slot, row_tiles, sq.row0, r0, rows};
+    }
+    if (a.window > 0) t0 = max(t0, max(max(pos_first, 0) - a.window + 1, 0) / kTok);
+
+    const int steps = (max(t1 - t0, 0) + kStep - 1) / kStep;
+    const int mine = steps > wave ? (steps - wave + WAVES - 1) / WAVES : 0;
+    auto tile_of = [&](int k) { return t0 + kStep * (wave + WAVES * k); };
+    // lane l looks up tile l % 2 of step k0 + l / 2; the first look is on its way before the queries
+    const int32_t* table = a.table + int64_t(it.seq) * a.max_blocks;
+    auto look_up = [&](int k0) {
+        const int tile = tile_of(k0 + lane / kStep) + lane % kStep;
+        return tile < t1 ? table[(tile * kTok) >> a.shift] : -1;
+    };
+    int32_t next_id = look_up(0);
+
+    // The rows of Q, split.  Lane (g, n) holds channels 16 g .. +16 of each 64 of row n: a product takes
+    // 16 of the first and 16 of the second 64 of its 128.  Two row tiles' lie in LDS.
+    constexpr bool kQueryLds = NT > 1;
+    __shared__ u32x4 queries[kQueryLds ? NT * 2 * DQ : 1][64];
+    u32x4 held[kQueryLds ? 1 : NT][kQueryLds ? 1 : 2 * DQ];
+    uint32_t q_hi[NT], q_lo[NT];         // the rows' scales
+    int pos[NT];
+    float slope[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = r0 + 16 * t + n;
+        const bool in = r < sq.rows;
+        const int j = token_of(a, r), qh = head * a.group + (r - j * a.group);
+        pos[t] = in ? sq.p0 + j : -1;
+        slope[t] = 0.f;
+        if (EXT && a.slopes && in) slope[t] = a.slopes[qh] * kLog2e;
+        const uint16_t* row = a.q + int64_t(sq.row0 + j) * a.q_stride + int64_t(qh) * D + 16 * g;
+        u32x4 w[2 * DQ];
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < 2 * DQ; ++c) {
+            w[c] = u32x4{0, 0, 0, 0};
+            if (in) w[c] = *reinterpret_cast<const u32x4*>(row + 64 * (c / 2) + 8 * (c % 2));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                top = max(top, max(w[c][i] & 0x7fffu, w[c][i] >> 16 & 0x7fffu));
+                w[c][i] ^= a.flip;
+            }
+        }
+        top = __float_as_uint(lane_max(__uint_as_float(min(top, 0x7f80u) << 16)));   // (a NaN as infinity: max would drop it)
+        const int e = max(int(top >> 23), 27) - 127;
+        const float down = __uint_as_float(uint32_t(134 - e) << 23);      // 2^(7 - e)
+        const bool bad = top >= 0x7f800000u;                               // an infinity or NaN: the row's scores are NaN
+        q_hi[t] = bad ? 255u : uint32_t(e + 120);
+        q_lo[t] = bad ? 255u : uint32_t(e + 116);
+#pragma unroll
+        for (int c = 0; c < DQ; ++c) {
+            if (kQueryLds && c % WAVES != wave) continue;
+            const QuerySplit s = split_query(w[2 * c], w[2 * c + 1], down);
+            if constexpr (kQueryLds) {
+                queries[(t * DQ + c) * 2][lane] = s.hi;
+                queries[(t * DQ + c) * 2 + 1][lane] = s.lo;
+            } else {
+                held[t][2 * c] = s.hi;
+                held[t][2 * c + 1] = s.lo;
+            }
+        }
+    }
+    if (kQueryLds) __syncthreads();
+    auto query = [&](int t, int c, int lo) {
+        if constexpr (kQueryLds) return queries[(t * DQ + c) * 2 + lo][lane];
+        else return held[t][2 * c + lo];
+    };
+
+    f32x4 acc[4 * DQ][NT];               // 8 products of a slab of 128 channels, 4 of one of 64
+    float top[NT], sum[NT];              // base of the weights (log2 domain); this lane's share of their sum
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        top[t] = -INFINITY;
+        sum[t] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4 * DQ; ++c) acc[c][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    int32_t my_id = -1;
+    u32x4 kc[kStep][S], vc[kStep][S];    // one step's codes (of a half slab's values two words)
+    uint32_t ks[kStep][S], vs[kStep][S]; // and exponents: of the lane's key, of four tokens' values
+    auto tile_at = [&](int tile, int l) {
+        const int32_t id = max(__builtin_amdgcn_readlane(my_id, l), 0);
+        return ((int64_t(id) * a.n_kv + head) << (a.shift - 4)) + (((tile * kTok) & in_block) >> 4);
+    };
+    // A wave's base and a lane's offset of 32 bits are the loads' own address form; the empty asms keep the
+    // compiler from widening the offsets ahead of the loop (five registers, and two operations a load).
+    const uint32_t lane16 = lane * 16, half16 = lane % 32 * 16, lane8 = lane * 8;
+    const uint32_t scales_at = n / 4 * 16 + 4 * g, half_scales_at = n / 8 * 16 + 4 * g;
+    auto here = [](uint32_t off) {
+        asm("" : "+v"(off));
+        return off;
+    };
+    // one tile of query rows is all there is: the codes are read once and streamed; with several, the
+    // other tiles find them in L2
+    auto read = [&](auto* from) { return NT == 1 ? __builtin_nontemporal_load(from) : *from; };
+    auto load_keys = [&](int tile, int l) {
+#pragma unroll
+        for (int h = 0; h < kStep; ++h) {
+            const int64_t at = tile_at(tile + h, l + h);
+            const uint8_t *codes = a.k + at * (512 * DQ), *scales = static_cast<const uint8_t*>(a.k_scale) + at * (32 * DQ);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                kc[h][s] = read(reinterpret_cast<const u32x4*>(codes + s * 1024 + here(s < F ? lane16 : half16)));
+                ks[h][s] = (scales + s * 64)[here(s < F ? uint32_t(lane) : uint32_t(lane % 32))];
+            }
+        }
+    };
+    auto load_values = [&](int tile, int l) {
+#pragma unroll
+        for (int h = 0; h < kStep; ++h) {
+            const int64_t at = tile_at(tile + h, l + h);
+            const uint8_t *codes = a.v + at * (512 * DQ), *scales = static_cast<const uint8_t*>(a.v_scale) + at * (32 * DQ);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                if (s < F) {
+                    vc[h][s] = read(reinterpret_cast<const u32x4*>(codes + s * 1024 + here(lane16)));
+                } else {
+                    const u32x2 w = read(reinterpret_cast<const u32x2*>(codes + s * 1024 + here(lane8)));
+                    vc[h][s] = u32x4{w.x, w.y, 0, 0};
+                }
+                vs[h][s] = *reinterpret_cast<const uint32_t*>(scales + s * 64 + here(s < F ? scales_at : half_scales_at));
+            }
+        }
+    };
+
+    auto step = [&](int tile, int l, int next_tile, bool more) {
+        if (kQueryLds) asm volatile("" ::: "memory");      // the queries are read again in each step
+        f32x4 s[kStep][NT];
+        bool whole = tile * kTok >= all_begin && (tile + kStep) * kTok <= all_end;
+#pragma unroll
+        for (int h = 0; h < kStep; ++h) {
+            whole = whole && __builtin_amdgcn_readlane(my_id, l + h) >= 0;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) s[h][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int c = 0; c < S; ++c)
+#pragma unroll
+                for (int lo = 0; lo < (c < F ? 2 : 1); ++lo) {
+                    if (kQueryLds) keep_order();
+                    const u32x4 q0 = c < F ? query(t, 2 * c, lo) : query(t, 2 * c, 0), q1 = c < F ? query(t, 2 * c + 1, lo) : query(t, 2 * c, 1);
+                    const uint32_t scale = c < F ? (lo ? q_lo[t] : q_hi[t]) : (g < 2 ? q_hi[t] : q_lo[t]);
+#pragma unroll
+                    for (int h = 0; h < kStep; ++h) s[h][t] = key_product(kc[h][c], q0, q1, s[h][t], ks[h][c], scale);
+                }
+        // (the products stay here: behind the loads, old and new codes and all queries would be held at once)
+#pragma unroll
+        for (int h = 0; h < kStep; ++h)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) asm volatile("" : "+v"(s[h][t]));
+        keep_order();
+        if (more) load_keys(next_tile, l + kStep);
+        keep_order();
+        bf16x8 pf[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float u[kStep][4];
+            const float away = float(tile * kTok + 4 * g - pos[t]);
+#pragma unroll
+            for (int h = 0; h < kStep; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x = s[h][t][i];
+                    if (EXT) {
+                        x *= a.to_score;
+                        if (a.softcap > 0.f) x = a.softcap * tanh_of(x);
+                        x += slope[t] * (away + float(h * kTok + i));
+                    }
+                    u[h][i] = x;
+                }
+            if (!whole) {
+#pragma unroll
+                for (int h = 0; h < kStep; ++h) {
+                    const bool id_ok = __builtin_amdgcn_readlane(my_id, l + h) >= 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = (tile + h) * kTok + 4 * g + i;
+                        bool sees = id_ok && tok <= pos[t];
+                        if (EXT && a.window > 0) sees = sees && pos[t] - tok < a.window;
+                        u[h][i] = sees ? u[h][i] : -INFINITY;
+                    }
+                }
+            }
+            float m = lane_max(max3(max3(u[0][0], u[0][1], u[0][2]), max3(u[0][3], u[1][0], u[1][1]), max3(u[1][2], u[1][3], u[1][3])));
+            if (!EXT) m *= a.to_score;
+            // the base of the weights need not be the maximum, only near it: it moves where a
+            // weight would pass 2^8, so most steps leave the sums as they are
+            if (__ballot(m > top[t] + 8.f)) {
+                m = fmaxf(m, top[t]);
+                const float f = __builtin_amdgcn_exp2f(top[t] - (m == -INFINITY ? 0.f : m));
+                sum[t] *= f;
+#pragma unroll
+                for (int c = 0; c < 4 * DQ; ++c) acc[c][t] *= f;
+                top[t] = m;
+            }
+            const float base = top[t] == -INFINITY ? 0.f : top[t];
+            float p[kStep][4];
+#pragma unroll
+            for (int h = 0; h < kStep; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    p[h][i] = __builtin_amdgcn_exp2f(EXT ? u[h][i] - base : __builtin_fmaf(u[h][i], a.to_score, -base));
+                    sum[t] += p[h][i];
+                }
+            // The matrix unit takes bf16: a weight is off by at most 2^-8 of itself.  The sums are of the weights before it.
+            const u32x4 w = {pack_bf16(p[0][0], p[0][1]), pack_bf16(p[0][2], p[0][3]), pack_bf16(p[1][0], p[1][1]), pack_bf16(p[1][2], p[1][3])};
+            pf[t] = __builtin_bit_cast(bf16x8, w);
+        }
+        if (!whole) {
+            // tokens that do not exist may have any codes and exponents, and a zero weight does not silence a
+            // NaN: 0 * 2^-127 instead
+#pragma unroll
+            for (int h = 0; h < kStep; ++h) {
+                const bool id_ok = __builtin_amdgcn_readlane(my_id, l + h) >= 0;
+                const int tok = (tile + h) * kTok + 4 * g;
+                const uint32_t live = id_ok ? live_bytes(tok, sq.len) : 0u;
+#pragma unroll
+                for (int c = 0; c < S; ++c) {
+                    vs[h][c] &= live;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (c < F) vc[h][c][i] = id_ok && tok + i < sq.len ? vc[h][c][i] : 0u;
+                        else if (i < 2) vc[h][c][i] &= (live >> (16 * i) & 1 ? 0xffffu : 0u) | (live >> (16 * i + 8) & 1 ? 0xffff0000u : 0u);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < S; ++c) {
+            auto exponent = [&](int h, int i) { return i == 0 ? vs[h][c] << 23 : i == 1 ? vs[h][c] << 15 : i == 2 ? vs[h][c] << 7 : vs[h][c] >> 1; };
+            auto two = [&](auto byte) {                  // two channels: the products 2 B and 2 B + 1 of the slab
+                constexpr int B = decltype(byte)::value;
+                keep_order();
+                asm("" : "+v"(vs[0][c]), "+v"(vs[1][c]));
+                uint32_t t8[8];
+#pragma unroll
+                for (int h = 0; h < kStep; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        t8[4 * h + i] = c < F ? value_pair<B>(vc[h][c][i], exponent(h, i))
+                                              : (i % 2 ? value_pair<(B + 2) % 4>(vc[h][c][i / 2], exponent(h, i)) : value_pair<B>(vc[h][c][i / 2], exponent(h, i)));
+                bf16x8 even, odd;
+                pair_up(t8, &even, &odd);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    acc[8 * c + 2 * B][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even, pf[t], acc[8 * c + 2 * B][t], 0, 0, 0);
+                    acc[8 * c + 2 * B + 1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd, pf[t], acc[8 * c + 2 * B + 1][t], 0, 0, 0);
+                }
+            };
+            two(Const<0>{});
+            two(Const<1>{});
+            if (c < F) {
+                two(Const<2>{});
+                two(Const<3>{});
+            }
+        }
+        keep_order();
+        if (more) load_values(next_tile, l + kStep);
+    };
+
+    for (int k0 = 0; k0 < mine; k0 += kRefill) {
+        my_id = next_id >= 0 && next_id < a.n_blocks ? next_id : -1;
+        const int end = min(mine - k0, kRefill);
+        load_keys(tile_of(k0), 0);
+        load_values(tile_of(k0), 0);
+        next_id = look_up(k0 + kRefill);
+        for (int k = 0; k < end; ++k) step(tile_of(k0 + k), kStep * k, tile_of(k0 + k + 1), k + 1 < end);
+    }
+
+    // A row's four channels from d on: final, from their weighted sum, and the row's sum of weights.
+    auto put = [&](int r, int d, const f32x4 o, float m, float l) {
+        const int j = token_of(a, r0 + r), qh = head * a.group + (r0 + r - j * a.group);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint16_t* to = a.out + int64_t(sq.row0 + j) * a.out_stride + int64_t(qh) * D + d;
+        *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+        if (d == 0 && a.lse) a.lse[int64_t(sq.row0 + j) * (a.n_kv * a.group) + qh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    };
+    // Join the waves: a common maximum a row, then sums four products at a time through LDS.
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        sum[t] += __shfl_xor(sum[t], 16);
+        sum[t] += __shfl_xor(sum[t], 32);
+        if (g == 0) {
+            merge_m[wave][16 * t + n] = top[t];
+            merge_l[wave][16 * t + n] = sum[t];
+        }
+    }
+    __syncthreads();
+    float f[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) m = fmaxf(m, merge_m[w][16 * t + n]);
+        f[t] = __builtin_amdgcn_exp2f(top[t] - (m == -INFINITY ? 0.f : m));
+    }
+#pragma unroll
+    for (int c = 0; c < DQ; ++c) {
+        if (c) __syncthreads();
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)      // register i of product j: channel j of the octet (in a half slab, the four) 4 g + i
+                *reinterpret_cast<f32x4*>(&merge[wave][16 * t + n][16 * g + 4 * i]) =
+                    f32x4{acc[4 * c][t][i], acc[4 * c + 1][t][i], acc[4 * c + 2][t][i], acc[4 * c + 3][t][i]} * f[t];
+        __syncthreads();
+        for (int e = threadIdx.x; e < rows * 16; e += 64 * WAVES) {
+            const int r = e >> 4, unit = e & 15, d = c < 2 * F ? c / 2 * 128 + unit * 8 + c % 2 * 4 : F * 128 + unit * 4;
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) m = fmaxf(m, merge_m[w][r]);
+            const float base = m == -INFINITY ? 0.f : m;
+            f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) {
+                l += merge_l[w][r] * __builtin_amdgcn_exp2f(merge_m[w][r] - base);
+                o += *reinterpret_cast<const f32x4*>(&merge[w][r][unit * 4]);
+            }
+            if (it.parts == 1) {
+                put(r, d, o, m, l);
+            } else {
+                const int64_t to = ((slot + int64_t(part) * row_tiles) * a.n_kv + head) * ROWS + r;
+                *reinterpret_cast<f32x4*>(a.part_o + to * D + d) = o;
+                if (d == 0) *reinterpret_cast<f32x2*>(a.part_ml + to * 2) = f32x2{m, l};
+            }
+        }
+    }
+}
+
+}  // namespace kv
+}  // namespace mbd

@@ -1,4 +1,4 @@
-// The 8-bit KV cache's addresses and codes, shared by its HIP sources.
+// The KV cache's addresses and codes, shared by its HIP sources.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -24,7 +24,7 @@ inline int log2_of(int32_t b) { return __builtin_ctz(unsigned(b)); }
 // Checks shared by every call that takes a cache; device memory is not looked at.
 inline mbd_status check_cache(const mbd_kv_cache* c, bool pointers) {
     if (!c) return fail(MBD_EINVAL, "NULL cache");
-    if (c->fmt != MBD_KV_INT8 && c->fmt != MBD_KV_E4M3) return fail(MBD_EINVAL, "unknown cache format %d", c->fmt);
+    if (c->fmt != MBD_KV_INT8 && c->fmt != MBD_KV_E4M3 && c->fmt != MBD_KV_MXFP4) return fail(MBD_EINVAL, "unknown cache format %d", c->fmt);
     if (!block_size_ok(c->block_size)) return fail(MBD_ESHAPE, "block_size %d is not 16, 32, 64, 128 or 256", c->block_size);
     if (c->head_dim < 64 || c->head_dim > 256 || c->head_dim % 64)
         return fail(MBD_ESHAPE, "head_dim %d is not 64, 128, 192 or 256", c->head_dim);
