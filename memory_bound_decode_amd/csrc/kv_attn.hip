@@ -375,17 +375,17 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
     }
 }
 
-// The parts of the split row tiles: a workgroup for each four query rows of a tile and head,
+// The parts of the split row tiles: a workgroup for each ROWS query rows of a tile and head,
 // WAVES waves a row; lanes over channels, waves over parts.
 // A second launch: joining in the last workgroup to arrive needs partial results that
 // pass the XCDs' L2s and a counter, which took longer (with an earlier form of the kernel above, one
 // request of 2048 tokens 10.5 against 8.9 us, one of 131072 84 against 57).
-constexpr int kJoinRows = 4, kJoinAhead = 8;
+constexpr int kJoinAhead = 8;
 
-template <int DQ, int WAVES>
-__global__ __launch_bounds__(64 * kJoinRows * WAVES) void join_kernel(AttnArgs a, int rows_of_tile) {
+template <int DQ, int WAVES, int ROWS>
+__global__ __launch_bounds__(64 * ROWS * WAVES) void join_kernel(AttnArgs a, int rows_of_tile) {
     constexpr int D = 64 * DQ;
-    __shared__ float joined[kJoinRows][WAVES][D], top[kJoinRows][WAVES], sum[kJoinRows][WAVES];
+    __shared__ float joined[ROWS][WAVES][D], top[ROWS][WAVES], sum[ROWS][WAVES];
     const int lane = threadIdx.x & 63, row = threadIdx.x / (64 * WAVES), wave = (threadIdx.x >> 6) % WAVES;
     const Split sp = a.splits[blockIdx.x];
     const int head = blockIdx.y;
@@ -395,8 +395,8 @@ __global__ __launch_bounds__(64 * kJoinRows * WAVES) void join_kernel(AttnArgs a
     if (sp.rows > rows_of_tile || sp.slot < 0 || sp.stride < 1 || sp.slot + int64_t(sp.parts - 1) * sp.stride >= a.n_parts || sp.row0 < 0 ||
         sp.r0 < 0 || sp.r0 >= (1 << 24) || int64_t(sp.row0) + token_of(a, sp.r0 + sp.rows - 1) >= a.T)
         return;
-    for (int pass = blockIdx.z; pass * kJoinRows < sp.rows; pass += gridDim.z) {
-        const int in_tile = pass * kJoinRows + row;
+    for (int pass = blockIdx.z; pass * ROWS < sp.rows; pass += gridDim.z) {
+        const int in_tile = pass * ROWS + row;
         if (pass != int(blockIdx.z)) __syncthreads();          // the last pass's sums are read
         const bool mine = in_tile < sp.rows;
         const int r = sp.r0 + in_tile;
@@ -545,15 +545,17 @@ static void launch(const AttnArgs& a, const Plan& p, int64_t items, bool ext, hi
     else ext ? run(attn_kernel<FMT == MBD_KV_E4M3, DQ, NT, true, WAVES>) : run(attn_kernel<FMT == MBD_KV_E4M3, DQ, NT, false, WAVES>);
     if (a.n_splits) {
         const int rows = std::min(16 * NT, a.max_new * a.group);
-        // (at most four workgroups a tile: where few tiles are split, most find nothing to do)
-        const dim3 joins(unsigned(a.n_splits), unsigned(a.n_kv), unsigned(std::min((rows + kJoinRows - 1) / kJoinRows, 4)));
+        const auto join = [&](auto kernel, int waves, int a_time, int most) {
+            const dim3 joins(unsigned(a.n_splits), unsigned(a.n_kv), unsigned(std::min((rows + a_time - 1) / a_time, most)));
+            hipLaunchKernelGGL(kernel, joins, dim3(64 * a_time * waves), 0, s, a, 16 * NT);
+        };
+        // (at most four workgroups of four rows a tile: where few tiles are split, most find nothing to do)
         // few row tiles can have many parts each: more waves over them (four against one, one request of
         // 131072 tokens 58.8 and 69.3 us, 8 of up to 4096 13.9 and 14.8, one of 500 10.0 and 8.9; with more row
         // tiles, 32 of up to 8192 54.9 and 53.7, a verify step of 8 x 5 15.3 and 14.2)
-        if (a.n_seqs * int64_t(p.row_tiles) * 8 < p.places)
-            hipLaunchKernelGGL((join_kernel<DQ, 4>), joins, dim3(64 * kJoinRows * 4), 0, s, a, 16 * NT);
-        else
-            hipLaunchKernelGGL((join_kernel<DQ, 1>), joins, dim3(64 * kJoinRows), 0, s, a, 16 * NT);
+        if (a.n_seqs * int64_t(p.row_tiles) * 8 >= p.places) join(join_kernel<DQ, 1, 4>, 1, 4, 4);
+        else if constexpr (FMT == MBD_KV_MXFP4) join(join_kernel<DQ, 16, 1>, 16, 1, 16);
+        else join(join_kernel<DQ, 4, 4>, 4, 4, 4);
     }
 }
 

@@ -62,12 +62,9 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t w, uint32_t scale) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, __uint_as_float(scale), B));
 }
 
-// Token T's byte of a word of four exponents, in the place of an fp32's exponent; what else stays in
+// Token i's byte of a word of four exponents, in the place of an fp32's exponent; what else stays in
 // the word has no meaning to value_pair.
-template <int T>
-__device__ __forceinline__ uint32_t exponent_of(uint32_t w) {
-    return T == 0 ? w << 23 : T == 1 ? w << 15 : T == 2 ? w << 7 : w >> 1;
-}
+__device__ __forceinline__ uint32_t exponent_of(uint32_t w, int i) { return i == 3 ? w >> 1 : w << (23 - 8 * i); }
 
 // Two channels (low and high halves of t[..]) of eight tokens as the operands of two products.
 __device__ __forceinline__ void pair_up(const uint32_t (&t)[8], bf16x8* even, bf16x8* odd) {
@@ -131,7 +128,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
 
     // The rows of Q, split.  Lane (g, n) holds channels 16 g .. +16 of each 64 of row n: a product takes
     // 16 of the first and 16 of the second 64 of its 128.  Two row tiles' lie in LDS.
-    constexpr bool kQueryLds = NT > 1;
+    constexpr bool kQueryLds = NT > 1, kLean = EXT || DQ > 2;
     __shared__ u32x4 queries[kQueryLds ? NT * 2 * DQ : 1][64];
     u32x4 held[kQueryLds ? 1 : NT][kQueryLds ? 1 : 2 * DQ];
     uint32_t q_hi[NT], q_lo[NT];         // the rows' scales
@@ -347,11 +344,12 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
         }
 #pragma unroll
         for (int c = 0; c < S; ++c) {
-            auto exponent = [&](int h, int i) { return i == 0 ? vs[h][c] << 23 : i == 1 ? vs[h][c] << 15 : i == 2 ? vs[h][c] << 7 : vs[h][c] >> 1; };
+            auto exponent = [&](int h, int i) { return exponent_of(vs[h][c], i); };
             auto two = [&](auto byte) {                  // two channels: the products 2 B and 2 B + 1 of the slab
                 constexpr int B = decltype(byte)::value;
                 keep_order();
-                asm("" : "+v"(vs[0][c]), "+v"(vs[1][c]));
+                // (where registers are short, the eight exponents are made anew for each two channels)
+                if (kLean) asm("" : "+v"(vs[0][c]), "+v"(vs[1][c]));
                 uint32_t t8[8];
 #pragma unroll
                 for (int h = 0; h < kStep; ++h)

@@ -3,9 +3,9 @@
 // A token's codes depend on that token alone, so there is nothing to share between its rows: a
 // lane takes eight channels of one token (an octet), four lanes a group of 32, whose maximum
 // gives the exponent.  What costs is where the bytes lie: a tile of 16 tokens keeps a token's codes
-// in pieces of 16 bytes (keys) and 4 (values), so the lanes of a wave are laid over (tokens,
-// octets) such that its stores fill whole lines where tokens follow each other in a tile: keys 16
-// tokens x one group, values 4 tokens x 16 octets.
+// in pieces of 16 bytes (keys) and 4 (values).  A wave takes 8 tokens x 8 octets: a line of 64 bf16
+// channels in, and where the tokens follow each other in a tile whole lines of codes out; and the same of
+// several heads one after the other, which are turned by the same angles.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -15,7 +15,8 @@
 namespace mbd {
 namespace kv {
 
-constexpr int kRows4 = 16;               // tokens of a workgroup's window
+constexpr int kRows4 = 8;                // tokens of a wave
+constexpr int kHeads4 = 4;               // heads whose loads are in flight together
 
 struct Cache4Args {
     uint8_t *codes[2], *scales[2];
@@ -39,8 +40,8 @@ struct Place4 {
     __device__ static bool halved(int d) { return DQ % 2 && d >= DQ / 2 * 128; }
     __device__ int64_t value(int d) const {
         const int64_t at = tile * (512 * DQ) + d / 128 * 1024;
-        if (halved(d)) return at + t / 4 * 128 + d % 64 / 4 * 8 + t % 4 * 2;
-        return at + t / 4 * 256 + d % 128 / 8 * 16 + t % 4 * 4;
+        if (halved(d)) return at + t / 4 * 128 + d % 64 / 4 * 8 + t % 4 * 2 + d % 4 / 2;
+        return at + t / 4 * 256 + d % 128 / 8 * 16 + t % 4 * 4 + d % 8 / 2;
     }
 };
 
@@ -48,7 +49,8 @@ struct Append4Args {
     Cache4Args c;
     const void* x[2];
     int64_t stride[2];
-    int32_t k_tasks, v_tasks, tasks;     // of waves; what follows the keys' and the values' are the queries'
+    int32_t heads;                       // of one wave's task
+    int32_t kv_tasks, tasks;             // of the keys, as many of the values; and all
     Turn turn;
 };
 
@@ -83,82 +85,114 @@ __device__ __forceinline__ uint32_t encode4(const f32x4 x0, const f32x4 x1, int*
     return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], s, 3);
 }
 
+// Eight channels as loaded, all from one address or each four from its own.
+template <class T> struct Eight;
+template <> struct Eight<float> {
+    f32x4 a, b;
+    __device__ void load(const float* p) { load(p, p + 4); }
+    __device__ void load(const float* p, const float* q) { a = load4(p), b = load4(q); }
+    __device__ f32x4 low() const { return a; }
+    __device__ f32x4 high() const { return b; }
+};
+template <> struct Eight<uint16_t> {
+    u32x4 w;
+    static __device__ f32x4 four(uint32_t x, uint32_t y) {
+        return f32x4{__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u), __uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u)};
+    }
+    __device__ void load(const uint16_t* p) { w = *reinterpret_cast<const u32x4*>(p); }
+    __device__ void load(const uint16_t* p, const uint16_t* q) {
+        const u32x2 x = *reinterpret_cast<const u32x2*>(p), y = *reinterpret_cast<const u32x2*>(q);
+        w = u32x4{x[0], x[1], y[0], y[1]};
+    }
+    __device__ f32x4 low() const { return four(w[0], w[1]); }
+    __device__ f32x4 high() const { return four(w[2], w[3]); }
+};
+
 template <int DQ, class T, bool TURN>
 __global__ __launch_bounds__(256) void append4_kernel(Append4Args a) {
     constexpr int D = 64 * DQ;
     const int lane = threadIdx.x & 63;
     const int task = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (task >= a.tasks) return;
-    const bool keys = task < a.k_tasks, queries = TURN && task >= a.k_tasks + a.v_tasks;
-    const int side = keys ? 0 : 1, spread = queries ? task - a.k_tasks - a.v_tasks : task - a.k_tasks;
-    const int row = keys ? lane >> 2 : (spread & 3) * 4 + (lane >> 4);
-    const int octet = keys ? task * 4 + (lane & 3) : (spread >> 2) * 16 + (lane & 15);
-    const int octets = (queries ? a.turn.n_q_heads : a.c.n_heads) * (D / 8);
-    if (octet >= octets) return;
-    const int head = octet / (D / 8), d = (octet - head * (D / 8)) * 8;
+    const int side = task < a.kv_tasks ? 0 : TURN && task >= 2 * a.kv_tasks ? 2 : 1;     // keys, values, queries
+    const int mine = task - side * a.kv_tasks, d = mine % DQ * 64 + (lane & 7) * 8;
+    const int h0 = mine / DQ * a.heads, h1 = min(h0 + a.heads, side == 2 ? a.turn.n_q_heads : a.c.n_heads);
+    const bool turns = TURN && side != 1;
+    const T* x = static_cast<const T*>(side == 2 ? a.turn.q : a.x[side & 1]);
+    const int64_t stride = side == 2 ? a.turn.q_stride : a.stride[side & 1];
     for (int64_t w0 = int64_t(blockIdx.y) * kRows4; w0 < a.c.T; w0 += int64_t(gridDim.y) * kRows4) {
-        const int64_t token = w0 + row;
+        const int64_t token = w0 + (lane >> 3);
         if (token >= a.c.T) continue;
-        if (queries) {
-            if constexpr (TURN) turn_query<T>(a.turn, int32_t(token), octet, D);
-            continue;
+        const T* from = x + token * stride + d;
+        Angles a0, a1;
+        if constexpr (TURN) {
+            const int32_t p = a.turn.positions[token];
+            if (p < 0 || p >= a.turn.n_positions) continue;
+            a0.partner = a1.partner = -1;
+            if (turns) {
+                const float* row = a.turn.table + int64_t(p) * a.turn.rot;
+                a0.load(a.turn, row, d);
+                a1.load(a.turn, row, d + 4);
+            }
         }
-        const int32_t slot = slot_at<TURN>(a.c.slots, a.turn, int32_t(token));
+        const int32_t slot = side == 2 ? 0 : a.c.slots[token];
         if (slot < 0 || slot >= a.c.n_slots) continue;
-        const T* from = static_cast<const T*>(a.x[side]) + token * a.stride[side] + int64_t(head) * D;
-        f32x4 x0, x1;
-        if (TURN && keys) {
-            const float* angles = a.turn.table + int64_t(a.turn.positions[token]) * a.turn.rot;
-            x0 = turned(a.turn, from, angles, d);
-            x1 = turned(a.turn, from, angles, d + 4);
-        } else {
-            x0 = load4(from + d);
-            x1 = load4(from + d + 4);
-        }
-        int e;
-        const uint32_t codes = encode4(x0, x1, &e);
-        const Place4<DQ> at(a.c, slot, head);
-        if ((lane & 3) == 0) a.c.scales[side][at.scale(d)] = uint8_t(e);
-        if (keys) {
-            *reinterpret_cast<uint32_t*>(a.c.codes[0] + at.key(d)) = codes;
-        } else if (Place4<DQ>::halved(d)) {
-            uint16_t* to = reinterpret_cast<uint16_t*>(a.c.codes[1] + at.value(d));
-            to[0] = uint16_t(codes);
-            to[4] = uint16_t(codes >> 16);
-        } else {
-            *reinterpret_cast<uint32_t*>(a.c.codes[1] + at.value(d)) = codes;
+        const bool whole = TURN && a.turn.rot % 16 == 0;     // an octet's partners are an octet
+        for (int hb = h0; hb < h1; hb += kHeads4) {
+            Eight<T> x[kHeads4], y[kHeads4];
+#pragma unroll
+            for (int i = 0; i < kHeads4; ++i) {
+                if (hb + i >= h1) break;
+                const T* head = from + (hb + i) * D;
+                x[i].load(head);
+                if (TURN && !a.turn.pairs) {             // (channels that are not turned load themselves)
+                    const T *p = a0.partner < 0 ? head : head - d + a0.partner, *q = a1.partner < 0 ? head + 4 : head - d + a1.partner;
+                    if (whole) y[i].load(p);
+                    else y[i].load(p, q);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kHeads4; ++i) {
+                if (hb + i >= h1) break;
+                f32x4 x0 = x[i].low(), x1 = x[i].high();
+                if (TURN) {
+                    const bool pairs = a.turn.pairs;
+                    const f32x4 y0 = pairs ? f32x4{x0[1], x0[0], x0[3], x0[2]} : y[i].low(), y1 = pairs ? f32x4{x1[1], x1[0], x1[3], x1[2]} : y[i].high();
+                    if (a0.partner >= 0) x0 = a0.turn(x0, y0);
+                    if (a1.partner >= 0) x1 = a1.turn(x1, y1);
+                    if (side == 2) {
+                        *reinterpret_cast<u32x4*>(a.turn.q_out + token * a.turn.q_out_stride + (hb + i) * D + d) =
+                            u32x4{pack_bf16(x0[0], x0[1]), pack_bf16(x0[2], x0[3]), pack_bf16(x1[0], x1[1]), pack_bf16(x1[2], x1[3])};
+                        continue;
+                    }
+                }
+                int e;
+                const uint32_t codes = encode4(x0, x1, &e);
+                const Place4<DQ> at(a.c, slot, hb + i);
+                uint8_t* to = a.c.codes[side & 1] + (side ? at.value(d) : at.key(d));
+                if ((lane & 3) == 0) a.c.scales[side & 1][at.scale(d)] = uint8_t(e);
+                if (side && Place4<DQ>::halved(d)) {
+                    *reinterpret_cast<uint16_t*>(to) = uint16_t(codes);
+                    *reinterpret_cast<uint16_t*>(to + 8) = uint16_t(codes >> 16);
+                } else {
+                    *reinterpret_cast<uint32_t*>(to) = codes;
+                }
+            }
         }
     }
 }
 
-// Eight codes and the scale's bits as fp32.
-__device__ __forceinline__ void decode4(uint32_t w, uint32_t e, f32x4* x0, f32x4* x1) {
-    const float s = __uint_as_float(e << 23);
-    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1);
-    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);
-    *x0 = f32x4{a[0], a[1], b[0], b[1]};
-    *x1 = f32x4{c[0], c[1], d[0], d[1]};
-}
+constexpr int kGather4 = 4;              // tokens of one thread
 
-__device__ __forceinline__ void stream8(float* p, const f32x4 x0, const f32x4 x1) {
-    __builtin_nontemporal_store(x0, reinterpret_cast<f32x4*>(p));
-    __builtin_nontemporal_store(x1, reinterpret_cast<f32x4*>(p + 4));
-}
-__device__ __forceinline__ void stream8(uint16_t* p, const f32x4 x0, const f32x4 x1) {
-    __builtin_nontemporal_store(u32x4{pack_bf16(x0[0], x0[1]), pack_bf16(x0[2], x0[3]), pack_bf16(x1[0], x1[1]), pack_bf16(x1[2], x1[3])},
-                                reinterpret_cast<u32x4*>(p));
-}
-
-constexpr int kGather4 = 2;              // tokens of one thread
-
-// 16 octets x 16 tokens, twice, of keys and values: a line of codes holds 8 tokens of one group, or
-// 4 of 64 channels, all of them read by this workgroup.
+// A thread writes 16 bytes (8 bf16 or 4 fp32 channels), a wave 4 tokens x 256 bytes of keys and as much of values;
+// a line of codes, which holds 8 tokens of one group or 4 of 64 channels, is read by this workgroup alone.
+// The outputs are not read again here: streamed past the caches.
 template <int DQ, class T>
 __global__ __launch_bounds__(256) void gather4_kernel(Cache4Args a, T* k_out, T* v_out) {
-    constexpr int D = 64 * DQ;
-    const int row = threadIdx.x >> 4, octet = blockIdx.x * 16 + (threadIdx.x & 15), octets = a.n_heads * (D / 8);
-    if (octet >= octets) return;
-    const int head = octet / (D / 8), d = (octet - head * (D / 8)) * 8;
+    constexpr int D = 64 * DQ, C = 16 / sizeof(T);
+    const int row = threadIdx.x >> 4, unit = blockIdx.x * 16 + (threadIdx.x & 15), units = a.n_heads * (D / C);
+    if (unit >= units) return;
+    const int head = unit / (D / C), d = (unit - head * (D / C)) * C;
     for (int64_t w0 = int64_t(blockIdx.y) * (16 * kGather4); w0 < a.T; w0 += int64_t(gridDim.y) * (16 * kGather4)) {
         int32_t slot[kGather4];
         uint32_t kw[kGather4], vw[kGather4], ke[kGather4], ve[kGather4];
@@ -172,12 +206,14 @@ __global__ __launch_bounds__(256) void gather4_kernel(Cache4Args a, T* k_out, T*
         for (int i = 0; i < kGather4; ++i)
             if (slot[i] >= 0) {
                 const Place4<DQ> at(a, slot[i], head);
-                kw[i] = *reinterpret_cast<const uint32_t*>(a.codes[0] + at.key(d));
-                if (Place4<DQ>::halved(d)) {
-                    const uint16_t* from = reinterpret_cast<const uint16_t*>(a.codes[1] + at.value(d));
-                    vw[i] = from[0] | uint32_t(from[4]) << 16;
+                const uint8_t *k = a.codes[0] + at.key(d), *v = a.codes[1] + at.value(d);
+                if constexpr (C == 4) {
+                    kw[i] = *reinterpret_cast<const uint16_t*>(k);
+                    vw[i] = *reinterpret_cast<const uint16_t*>(v);
                 } else {
-                    vw[i] = *reinterpret_cast<const uint32_t*>(a.codes[1] + at.value(d));
+                    kw[i] = *reinterpret_cast<const uint32_t*>(k);
+                    if (Place4<DQ>::halved(d)) vw[i] = *reinterpret_cast<const uint16_t*>(v) | uint32_t(*reinterpret_cast<const uint16_t*>(v + 8)) << 16;
+                    else vw[i] = *reinterpret_cast<const uint32_t*>(v);
                 }
                 ke[i] = a.scales[0][at.scale(d)];
                 ve[i] = a.scales[1][at.scale(d)];
@@ -185,12 +221,21 @@ __global__ __launch_bounds__(256) void gather4_kernel(Cache4Args a, T* k_out, T*
 #pragma unroll
         for (int i = 0; i < kGather4; ++i)
             if (slot[i] >= 0) {
-                const int64_t to = (w0 + 16 * i + row) * (int64_t(a.n_heads) * D) + int64_t(octet) * 8;
-                f32x4 x0, x1;
-                decode4(kw[i], ke[i], &x0, &x1);
-                stream8(k_out + to, x0, x1);
-                decode4(vw[i], ve[i], &x0, &x1);
-                stream8(v_out + to, x0, x1);
+                const int64_t to = (w0 + 16 * i + row) * (int64_t(a.n_heads) * D) + int64_t(unit) * C;
+#pragma unroll
+                for (int side = 0; side < 2; ++side) {
+                    const uint32_t w = side ? vw[i] : kw[i];
+                    const float s = __uint_as_float((side ? ve[i] : ke[i]) << 23);
+                    const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1);
+                    u32x4 r;
+                    if constexpr (C == 4) {
+                        r = __builtin_bit_cast(u32x4, f32x4{p0[0], p0[1], p1[0], p1[1]});
+                    } else {
+                        const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);
+                        r = u32x4{pack_bf16(p0[0], p0[1]), pack_bf16(p1[0], p1[1]), pack_bf16(p2[0], p2[1]), pack_bf16(p3[0], p3[1])};
+                    }
+                    __builtin_nontemporal_store(r, reinterpret_cast<u32x4*>((side ? v_out : k_out) + to));
+                }
             }
     }
 }
@@ -210,12 +255,14 @@ void launch_append4(const Append4Args& a, dim3 grid, hipStream_t s) {
 template <class T>
 void append4(const mbd_kv_cache* c, const Turn& turn, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
              const int32_t* slots, int32_t T_, hipStream_t s) {
-    Append4Args a{cache4_args(c, slots, T_), {k, v}, {k_stride, v_stride}, 0, 0, 0, turn};
     const int dq = c->head_dim / 64;
-    a.k_tasks = c->n_heads * 2 * dq;
-    a.v_tasks = (c->n_heads * 8 * dq + 15) / 16 * 4;
-    a.tasks = a.k_tasks + a.v_tasks + (turn.table ? (turn.n_q_heads * 8 * dq + 15) / 16 * 4 : 0);
-    const dim3 grid(unsigned((a.tasks + 3) / 4), unsigned(T_ / kRows4 < 65535 ? (T_ + kRows4 - 1) / kRows4 : 65535));
+    const int64_t windows = (int64_t(T_) + kRows4 - 1) / kRows4;
+    // heads of a task: as many as leave 4096 waves
+    int heads = 1;
+    while (heads < 8 && windows * dq * (2 * int64_t(c->n_heads) + turn.n_q_heads) / (2 * heads) >= 4096) heads *= 2;
+    const int kv_tasks = (c->n_heads + heads - 1) / heads * dq, q_tasks = turn.table ? (turn.n_q_heads + heads - 1) / heads * dq : 0;
+    const Append4Args a{cache4_args(c, slots, T_), {k, v}, {k_stride, v_stride}, heads, kv_tasks, 2 * kv_tasks + q_tasks, turn};
+    const dim3 grid(unsigned((a.tasks + 3) / 4), unsigned(windows < 65535 ? windows : 65535));
     if (dq == 1) launch_append4<1, T>(a, grid, s);
     else if (dq == 2) launch_append4<2, T>(a, grid, s);
     else if (dq == 3) launch_append4<3, T>(a, grid, s);
@@ -227,7 +274,7 @@ void gather4(const mbd_kv_cache* c, const int32_t* slots, int32_t n, void* k_out
     const Cache4Args a = cache4_args(c, slots, n);
     T *k = static_cast<T*>(k_out), *v = static_cast<T*>(v_out);
     const int dq = c->head_dim / 64, per = 16 * kGather4;
-    const dim3 grid(unsigned((c->n_heads * 8 * dq + 15) / 16), unsigned(n / per < 65535 ? (n + per - 1) / per : 65535));
+    const dim3 grid(unsigned((int64_t(c->n_heads) * 64 * dq * int64_t(sizeof(T)) / 16 + 15) / 16), unsigned(n / per < 65535 ? (n + per - 1) / per : 65535));
     if (dq == 1) hipLaunchKernelGGL((gather4_kernel<1, T>), grid, dim3(256), 0, s, a, k, v);
     else if (dq == 2) hipLaunchKernelGGL((gather4_kernel<2, T>), grid, dim3(256), 0, s, a, k, v);
     else if (dq == 3) hipLaunchKernelGGL((gather4_kernel<3, T>), grid, dim3(256), 0, s, a, k, v);

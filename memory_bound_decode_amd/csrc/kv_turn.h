@@ -35,29 +35,46 @@ __device__ __forceinline__ int32_t slot_at(const int32_t* slots, const Turn& u, 
     return s;
 }
 
-// Channels d .. d+4 of a head whose channel 0 is at `head`, turned by a row of the table.  rot / 2
-// is a multiple of 4, so the four have their partners side by side as well.  Products and sums
-// are rounded one by one: the codes that come of them are the same wherever they are computed.
+// What turns channels d .. d+4 of any head of a token: x becomes x c + y s, where y are their partners.
+// Products and sums are rounded one by one: the codes that come of them are the same wherever they are
+// computed.  rot / 2 is a multiple of 4, so the four have their partners side by side as well.
+struct Angles {
+    f32x4 c, s;
+    int partner;                         // first channel of the partners; d itself: in the four; -1: not turned
+
+    __device__ __forceinline__ void load(const Turn& u, const float* row, int d) {
+        const int half = u.rot / 2;
+        partner = -1;
+        if (d >= u.rot) return;
+        if (u.pairs) {
+            const f32x2 a = *reinterpret_cast<const f32x2*>(row + d / 2), b = *reinterpret_cast<const f32x2*>(row + half + d / 2);
+            c = f32x4{a[0], a[0], a[1], a[1]};
+            s = f32x4{-b[0], b[0], -b[1], b[1]};
+            partner = d;
+            return;
+        }
+        const bool second = d >= half;
+        const int j = second ? d - half : d;
+        c = load4(row + j);
+        s = load4(row + half + j);
+        if (!second) s = -s;
+        partner = second ? j : d + half;
+    }
+    __device__ __forceinline__ f32x4 turn(const f32x4 x, const f32x4 y) const {
+#pragma clang fp contract(off)
+        const f32x4 a = x * c, b = y * s;
+        return a + b;
+    }
+};
+
+// Channels d .. d+4 of a head whose channel 0 is at `head`, turned by a row of the table.
 template <class T>
 __device__ __forceinline__ f32x4 turned(const Turn& u, const T* head, const float* row, int d) {
-#pragma clang fp contract(off)
     const f32x4 x = load4(head + d);
-    if (d >= u.rot) return x;
-    const int half = u.rot / 2;
-    if (u.pairs) {
-        const f32x2 c = *reinterpret_cast<const f32x2*>(row + d / 2), s = *reinterpret_cast<const f32x2*>(row + half + d / 2);
-        return f32x4{x[0] * c[0] - x[1] * s[0], x[1] * c[0] + x[0] * s[0], x[2] * c[1] - x[3] * s[1], x[3] * c[1] + x[2] * s[1]};
-    }
-    const bool second = d >= half;
-    const int j = second ? d - half : d;
-    const f32x4 y = load4(head + (second ? j : d + half)), c = load4(row + j), s = load4(row + half + j);
-    f32x4 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float a = x[i] * c[i], b = y[i] * s[i];
-        r[i] = second ? a + b : a - b;
-    }
-    return r;
+    Angles a;
+    a.load(u, row, d);
+    if (a.partner < 0) return x;
+    return a.turn(x, a.partner == d ? f32x4{x[1], x[0], x[3], x[2]} : load4(head + a.partner));
 }
 
 // Eight channels (octet `o` of a token's row of queries) turned and rounded to bf16.
