@@ -28,15 +28,15 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int per_cu4(int dq, int nt) { return nt == 1 ? (dq <= 2 ? 4 : dq == 3 ? 3 : 2) : (dq == 1 ? 4 : dq == 2 ? 3 : 2); }
 
-// Sixteen bf16 of a query row over 2^(E - 7), E the exponent of the row's largest: below 256, as hi + lo / 16,
+// Eight bf16 of a query row over 2^(E - 7), E the exponent of the row's largest: below 256, as hi + lo / 16,
 // both e4m3.  The rest behind hi is at most half of its step, 2^4 of 256, so 16 of them fit as well.
-struct QuerySplit { u32x4 hi, lo; };
+struct QuerySplit { u32x2 hi, lo; };
 
-__device__ __forceinline__ QuerySplit split_query(const u32x4 w0, const u32x4 w1, float down) {
+__device__ __forceinline__ QuerySplit split_query(const u32x4 w, float down) {
     QuerySplit r;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const uint32_t a = q < 2 ? w0[2 * q] : w1[2 * q - 4], b = q < 2 ? w0[2 * q + 1] : w1[2 * q - 3];
+    for (int q = 0; q < 2; ++q) {
+        const uint32_t a = w[2 * q], b = w[2 * q + 1];
         const float x[4] = {__uint_as_float(a << 16) * down, __uint_as_float(a & 0xffff0000u) * down, __uint_as_float(b << 16) * down,
                             __uint_as_float(b & 0xffff0000u) * down};
         int h = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
@@ -78,6 +78,22 @@ __device__ __forceinline__ void pair_up(const uint32_t (&t)[8], bf16x8* even, bf
     *odd = __builtin_bit_cast(bf16x8, o);
 }
 
+// What a workgroup does, from the wave that found out.
+struct Share {
+    Item it;
+    Seq sq;
+    int32_t splits;
+    __device__ __forceinline__ void read(const Share& from) {      // into scalar registers
+        constexpr int words = sizeof(Share) / 4;
+        static_assert(words <= 64, "a word a lane");
+        const int32_t mine = reinterpret_cast<const int32_t*>(&from)[min(int(threadIdx.x & 63), words - 1)];
+        int32_t all[words];
+#pragma unroll
+        for (int i = 0; i < words; ++i) all[i] = __builtin_amdgcn_readlane(mine, i);
+        *this = __builtin_bit_cast(Share, all);
+    }
+};
+
 // (NaN if one is: fmaxf spends an instruction on each operand for those that are signalling)
 __device__ __forceinline__ float max3(float a, float b, float c) { return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c); }
 
@@ -88,13 +104,25 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
     constexpr int D = 64 * DQ, ROWS = 16 * NT, PITCH = 68, F = DQ / 2, H = DQ % 2, S = F + H;   // slabs of 128 channels, of 64
     __shared__ float merge[WAVES][ROWS][PITCH];     // pitch: rows 4 banks apart
     __shared__ float merge_m[WAVES][ROWS], merge_l[WAVES][ROWS];
+    __shared__ Share share;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, n = lane & 15;
     const int in_block = (1 << a.shift) - 1;
     const int want = blockIdx.x / uint32_t(a.n_kv), head = blockIdx.x - want * a.n_kv;
-    Seq sq;
-    int splits;
-    const Item it = find_item(a, want, &sq, &splits);
+    // One wave looks for the workgroup's share (400 operations: in every wave at once they kept the
+    // vector units busy for the longer part of the start); not always the same, whose SIMD would have it all.
+    Share sh;
+    if (WAVES == 1 || wave == int(blockIdx.x / kCus % WAVES)) {
+        sh.it = find_item(a, want, &sh.sq, &sh.splits);
+        if (WAVES > 1 && lane == 0) share = sh;
+    }
+    if (WAVES > 1) {
+        __syncthreads();
+        sh.read(share);
+    }
+    const Item it = sh.it;
+    const Seq sq = sh.sq;
+    const int splits = sh.splits;
     if (head == 0 && threadIdx.x == 0 && want >= splits && want < a.n_splits) a.splits[want] = Split{0, 0, 0, 0, 0, 0};
     if (it.seq < 0) return;
     const int row_tiles = row_tiles_of(a, sq), part = it.index / row_tiles;
@@ -127,57 +155,81 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
     int32_t next_id = look_up(0);
 
     // The rows of Q, split.  Lane (g, n) holds channels 16 g .. +16 of each 64 of row n: a product takes
-    // 16 of the first and 16 of the second 64 of its 128.  Two row tiles' lie in LDS.
+    // 16 of the first and 16 of the second 64 of its 128.  The waves split pieces of 8 channels in turn and
+    // leave them in LDS; of one row tile each wave then takes all into registers.  Rows past the last repeat
+    // it: they see nothing, and nothing of them is kept.
     constexpr bool kQueryLds = NT > 1, kLean = EXT || DQ > 2;
-    __shared__ u32x4 queries[kQueryLds ? NT * 2 * DQ : 1][64];
-    u32x4 held[kQueryLds ? 1 : NT][kQueryLds ? 1 : 2 * DQ];
+    constexpr int kPieces = NT * 2 * DQ, kMine = (kPieces + WAVES - 1) / WAVES;
+    __shared__ u32x2 queries[NT * DQ][2][64][2];         // [64 channels][hi, lo][lane][8 channels]
+    __shared__ uint32_t row_top[WAVES][NT][16];
     uint32_t q_hi[NT], q_lo[NT];         // the rows' scales
     int pos[NT];
     float slope[NT];
+    const uint16_t* row_at[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int r = r0 + 16 * t + n;
-        const bool in = r < sq.rows;
-        const int j = token_of(a, r), qh = head * a.group + (r - j * a.group);
-        pos[t] = in ? sq.p0 + j : -1;
-        slope[t] = 0.f;
-        if (EXT && a.slopes && in) slope[t] = a.slopes[qh] * kLog2e;
-        const uint16_t* row = a.q + int64_t(sq.row0 + j) * a.q_stride + int64_t(qh) * D + 16 * g;
-        u32x4 w[2 * DQ];
+        const int r = r0 + 16 * t + n, j = token_of(a, min(r, sq.rows - 1)), qh = head * a.group + (min(r, sq.rows - 1) - j * a.group);
+        pos[t] = r < sq.rows ? sq.p0 + j : -1;
+        slope[t] = EXT && a.slopes ? a.slopes[qh] * kLog2e : 0.f;
+        row_at[t] = a.q + int64_t(sq.row0 + j) * a.q_stride + int64_t(qh) * D + 16 * g;
+    }
+    u32x4 w[kMine];
+    uint32_t most[NT] = {};
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        const int piece = WAVES == 1 ? k : k * WAVES + wave, t = piece / (2 * DQ), c = piece % (2 * DQ);
+        if (kPieces % WAVES && piece >= kPieces) break;
+        w[k] = *reinterpret_cast<const u32x4*>((NT == 1 || t == 0 ? row_at[0] : row_at[NT - 1]) + 64 * (c / 2) + 8 * (c % 2));
         uint32_t top = 0;
 #pragma unroll
-        for (int c = 0; c < 2 * DQ; ++c) {
-            w[c] = u32x4{0, 0, 0, 0};
-            if (in) w[c] = *reinterpret_cast<const u32x4*>(row + 64 * (c / 2) + 8 * (c % 2));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                top = max(top, max(w[c][i] & 0x7fffu, w[c][i] >> 16 & 0x7fffu));
-                w[c][i] ^= a.flip;
-            }
+        for (int i = 0; i < 4; ++i) {
+            top = max(top, max(w[k][i] & 0x7fffu, w[k][i] >> 16 & 0x7fffu));
+            w[k][i] ^= a.flip;
         }
-        top = __float_as_uint(lane_max(__uint_as_float(min(top, 0x7f80u) << 16)));   // (a NaN as infinity: max would drop it)
+        if (NT == 1 || t == 0) most[0] = max(most[0], top);
+        else most[NT - 1] = max(most[NT - 1], top);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        // (a NaN as infinity: max would drop it)
+        most[t] = __float_as_uint(lane_max(__uint_as_float(min(most[t], 0x7f80u) << 16)));
+        if (WAVES > 1 && g == 0) row_top[wave][t][n] = most[t];
+    }
+    if (WAVES > 1) __syncthreads();
+    float down[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        uint32_t top = most[t];
+#pragma unroll
+        for (int v = 0; v < WAVES; ++v)
+            if (WAVES > 1) top = max(top, row_top[v][t][n]);
         const int e = max(int(top >> 23), 27) - 127;
-        const float down = __uint_as_float(uint32_t(134 - e) << 23);      // 2^(7 - e)
+        down[t] = __uint_as_float(uint32_t(134 - e) << 23);               // 2^(7 - e)
         const bool bad = top >= 0x7f800000u;                               // an infinity or NaN: the row's scores are NaN
         q_hi[t] = bad ? 255u : uint32_t(e + 120);
         q_lo[t] = bad ? 255u : uint32_t(e + 116);
+    }
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        const int piece = WAVES == 1 ? k : k * WAVES + wave, t = piece / (2 * DQ), c = piece % (2 * DQ);
+        if (kPieces % WAVES && piece >= kPieces) break;
+        const QuerySplit s = split_query(w[k], NT == 1 || t == 0 ? down[0] : down[NT - 1]);
+        queries[t * DQ + c / 2][0][lane][c % 2] = s.hi;
+        queries[t * DQ + c / 2][1][lane][c % 2] = s.lo;
+    }
+    if (WAVES > 1) __syncthreads();
+    else wave_sync_lds();
+    auto from_lds = [&](int t, int c, int lo) { return *reinterpret_cast<const u32x4*>(&queries[t * DQ + c][lo][lane][0]); };
+    u32x4 held[kQueryLds ? 1 : 2 * DQ];
+    if constexpr (!kQueryLds)
 #pragma unroll
         for (int c = 0; c < DQ; ++c) {
-            if (kQueryLds && c % WAVES != wave) continue;
-            const QuerySplit s = split_query(w[2 * c], w[2 * c + 1], down);
-            if constexpr (kQueryLds) {
-                queries[(t * DQ + c) * 2][lane] = s.hi;
-                queries[(t * DQ + c) * 2 + 1][lane] = s.lo;
-            } else {
-                held[t][2 * c] = s.hi;
-                held[t][2 * c + 1] = s.lo;
-            }
+            held[2 * c] = from_lds(0, c, 0);
+            held[2 * c + 1] = from_lds(0, c, 1);
         }
-    }
-    if (kQueryLds) __syncthreads();
     auto query = [&](int t, int c, int lo) {
-        if constexpr (kQueryLds) return queries[(t * DQ + c) * 2 + lo][lane];
-        else return held[t][2 * c + lo];
+        if constexpr (kQueryLds) return from_lds(t, c, lo);
+        else return held[2 * c + lo];
     };
 
     f32x4 acc[4 * DQ][NT];               // 8 products of a slab of 128 channels, 4 of one of 64
