@@ -470,7 +470,7 @@ __global__ __launch_bounds__(64 * ROWS * WAVES) void join_kernel(AttnArgs a, int
 // How a call is laid out; the same for the workspace's size and the launch.
 struct Plan {
     int32_t group, nt, waves, row_tiles, places, unit;
-    bool split;
+    bool split, direct;      // direct (4 bits): a workgroup a request
     int64_t longest;         // parts of a request at most
     uint64_t parts;          // partial results of a head, of nt * 16 rows
     uint64_t splits;         // row tiles that they can come from
@@ -496,7 +496,16 @@ static void lay_out(const mbd_kv_cache* c, int64_t tiles, int64_t seq_tiles, Pla
     p->bytes = p->parts * c->n_heads * (16u * p->nt) * (c->head_dim + 2) * sizeof(float) + p->splits * sizeof(Split);
 }
 
-static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs, int32_t max_new, int32_t max_blocks, Plan* p) {
+// 4 bits: requests of which a query sees at most this many tiles are not cut (see direct_waves).
+constexpr int64_t kDirectTiles = 128;
+
+// Waves of a workgroup that takes a whole request: as many as a CU holds, or four where there are requests enough to
+// fill the chip so.
+static int direct_waves(const mbd_kv_cache* c, int32_t n_seqs) {
+    return int64_t(n_seqs) * c->n_heads > 2 * kCus ? kMaxWaves : c->head_dim <= 128 ? 16 : 8;
+}
+
+static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs, int32_t max_new, int32_t max_blocks, int32_t window, Plan* p) {
     if (n_heads < 1 || n_heads % c->n_heads) return fail(MBD_ESHAPE, "n_heads %d is not a multiple of the cache's %d", n_heads, c->n_heads);
     if (n_seqs < 1 || n_seqs > kMaxSeqs) return fail(MBD_ESHAPE, "n_seqs %d outside [1, %d]", n_seqs, kMaxSeqs);
     if (max_blocks < 1 || int64_t(max_blocks) * c->block_size > (int64_t(1) << 30))
@@ -515,6 +524,13 @@ static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs
     while (((seq_tiles * p->row_tiles) >> p->unit) + 1 >= (int64_t(1) << 31) / n_seqs) ++p->unit;
     p->waves = p->nt == 1 && tiles > places_of(c, 1, kMaxWaves) ? 1 : kMaxWaves;
     lay_out(c, tiles, seq_tiles, p);
+    const int64_t seen = window > 0 ? std::min(seq_tiles, (int64_t(window) + max_new - 2) / kTok + 2) : seq_tiles;
+    p->direct = c->fmt == MBD_KV_MXFP4 && p->nt == 1 && seen <= kDirectTiles;
+    if (p->direct) {
+        p->waves = direct_waves(c, n_seqs);
+        p->split = false;
+        p->parts = p->splits = p->bytes = 0;
+    }
     return MBD_OK;
 }
 
@@ -524,6 +540,7 @@ static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs
 static uint64_t largest_workspace(const mbd_kv_cache* c, int32_t n_seqs, int32_t max_blocks, const Plan& own) {
     const int64_t seq_tiles = int64_t(max_blocks) * (c->block_size / kTok);
     uint64_t bytes = own.bytes;
+    if (own.direct) return bytes;              // and so is every smaller call
     if (own.group > 16) return bytes;          // a single token has two row tiles
     Plan p{};
     p.nt = 1;
@@ -537,11 +554,11 @@ static uint64_t largest_workspace(const mbd_kv_cache* c, int32_t n_seqs, int32_t
     return bytes;
 }
 
-template <int FMT, int DQ, int NT, int WAVES>
+template <int FMT, int DQ, int NT, int WAVES, bool DIRECT = false>
 static void launch(const AttnArgs& a, const Plan& p, int64_t items, bool ext, hipStream_t s) {
     const dim3 grid(unsigned(items) * unsigned(a.n_kv)), block(64 * WAVES);
     const auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a); };
-    if constexpr (FMT == MBD_KV_MXFP4) ext ? run(attn4_kernel<DQ, NT, true, WAVES>) : run(attn4_kernel<DQ, NT, false, WAVES>);
+    if constexpr (FMT == MBD_KV_MXFP4) ext ? run(attn4_kernel<DQ, NT, true, WAVES, DIRECT>) : run(attn4_kernel<DQ, NT, false, WAVES, DIRECT>);
     else ext ? run(attn_kernel<FMT == MBD_KV_E4M3, DQ, NT, true, WAVES>) : run(attn_kernel<FMT == MBD_KV_E4M3, DQ, NT, false, WAVES>);
     if (a.n_splits) {
         const int rows = std::min(16 * NT, a.max_new * a.group);
@@ -561,6 +578,8 @@ static void launch(const AttnArgs& a, const Plan& p, int64_t items, bool ext, hi
 
 template <int FMT, int DQ>
 static void launch_rows(const AttnArgs& a, const Plan& p, int64_t items, bool ext, hipStream_t s) {
+    if constexpr (FMT == MBD_KV_MXFP4)
+        if (p.direct) return p.waves == kMaxWaves ? launch<FMT, DQ, 1, 4, true>(a, p, items, ext, s) : launch<FMT, DQ, 1, DQ <= 2 ? 16 : 8, true>(a, p, items, ext, s);
     if (p.nt == 2) launch<FMT, DQ, 2, 4>(a, p, items, ext, s);
     else if (p.waves == 4) launch<FMT, DQ, 1, 4>(a, p, items, ext, s);
     else launch<FMT, DQ, 1, 1>(a, p, items, ext, s);
@@ -586,7 +605,7 @@ mbd_status mbd_kv_attn_workspace_bytes(const mbd_kv_cache* cache, int32_t n_head
     if (!bytes) return fail(MBD_EINVAL, "NULL argument");
     kv::Plan p;
     mbd_status st = kv::check_cache(cache, false);
-    if (st == MBD_OK) st = kv::plan_of(cache, n_heads, n_seqs, max_new, max_blocks, &p);
+    if (st == MBD_OK) st = kv::plan_of(cache, n_heads, n_seqs, max_new, max_blocks, 0, &p);
     if (st == MBD_OK) *bytes = kv::largest_workspace(cache, n_seqs, max_blocks, p);
     return st;
 }
@@ -599,7 +618,7 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     mbd_status st = kv::check_cache(cache, true);
     if (st != MBD_OK) return st;
     if (!args) return fail(MBD_EINVAL, "NULL argument");
-    st = kv::plan_of(cache, args->n_heads, args->n_seqs, args->max_new, args->max_blocks, &p);
+    st = kv::plan_of(cache, args->n_heads, args->n_seqs, args->max_new, args->max_blocks, std::max(args->window, 0), &p);
     if (st != MBD_OK) return st;
     if (args->T < 0 || args->T > (1 << 24)) return fail(MBD_ESHAPE, "T %d outside [0, 2^24]", args->T);
     if (args->window < 0) return fail(MBD_EINVAL, "window %d below 0", args->window);
@@ -617,7 +636,7 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
         return fail(MBD_EALIGN, "int32 and fp32 arrays must be 4-byte aligned");
     // a head's items: places, and the row tiles that the sums may pass them by; T bounds those
     const int64_t used = std::min<int64_t>(int64_t(args->n_seqs) * p.row_tiles, int64_t(args->T) * p.group / (16 * p.nt) + args->n_seqs);
-    const int64_t items = p.split ? std::min(p.places + used, used * p.longest) : used;
+    const int64_t items = p.direct ? args->n_seqs : p.split ? std::min(p.places + used, used * p.longest) : used;
     if (items * cache->n_heads >= (int64_t(1) << 24)) return fail(MBD_ESHAPE, "KV heads times tiles of query rows is 2^24 or more");
     if (args->T == 0) return MBD_OK;
     if (!q || !out) return fail(MBD_EINVAL, "NULL argument");

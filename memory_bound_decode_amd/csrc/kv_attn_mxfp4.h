@@ -78,6 +78,79 @@ __device__ __forceinline__ void pair_up(const uint32_t (&t)[8], bf16x8* even, bf
     *odd = __builtin_bit_cast(bf16x8, o);
 }
 
+// ceil(n / chunk), 0 for 0: exact where the quotient is below 2^20, as a reciprocal's errors then move
+// it by less than one.
+__device__ __forceinline__ int parts_in(int n, int chunk, float inverse) {
+    int q = int(float(n - 1) * inverse);
+    const int rest = n - 1 - q * chunk;
+    q += rest >= chunk ? 1 : rest < 0 ? -1 : 0;
+    return n > 0 ? q + 1 : 0;
+}
+
+// find_item for up to 64 requests, one a lane.  The way to a workgroup's first load goes through here, so it
+// is kept short: four chunks are tried at once, two counts to a word, and the smallest that fits is
+// taken.  (Parts and row tiles add up to about work / chunk + used / 2, so that is where the candidates stand; the
+// last always fits.)
+// Where there are more items than places, those of the longest parts come first, in four classes: the
+// last ones to start then end early.
+__device__ __forceinline__ Item find_item_64(const AttnArgs& a, int32_t want, Seq* sq, int* splits) {
+    const int lane = threadIdx.x & 63;
+    const Seq s = load_seq(a, min(lane, a.n_seqs - 1));
+    const int n = lane < a.n_seqs ? tiles_of(s) : 0, rt = n ? row_tiles_of(a, s) : 0;
+    auto total = [](int scan) { return __builtin_amdgcn_readlane(scan, 63); };
+    auto uniform = [](int v, int l) { return __builtin_amdgcn_readlane(v, l); };
+    int chunk = 0x3fffffff;
+    float inverse = 0x1p-30f;
+    if (a.split) {
+        const int units = a.unit ? int((uint64_t(uint32_t(n)) * uint32_t(rt) + (uint64_t(1) << a.unit) - 1) >> a.unit) : n * rt;
+        const int work = max(total(wave_scan(units)), 1), used = total(wave_scan(rt));
+        // lane k's candidate: at least work / room, as the reciprocal's and the roundings' errors are below 2^-21
+        const int eighths = lane == 0 ? 3 : lane == 1 ? 4 : lane == 2 ? 5 : 8;
+        const int room = used < a.places ? a.places - (eighths * used + 7) / 8 : (a.places + 1) / 2;
+        const uint32_t share = uint32_t(float(work) * __builtin_amdgcn_rcpf(float(room)) * (1 + 0x1p-20f)) + 1;
+        const int mine = a.unit ? int(min(max(uint64_t(share) << a.unit, uint64_t(a.min_part)), uint64_t(1) << 30)) : int(max(share, uint32_t(a.min_part)));
+        const float one_over = __builtin_amdgcn_rcpf(float(mine));
+        int best = 3;
+        if (used < a.places) {
+            uint32_t count[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                auto items = [&](int t) { return parts_in(n, uniform(mine, t), __int_as_float(uniform(__float_as_int(one_over), t))) * rt; };
+                count[k] = wave_scan(items(2 * k) | items(2 * k + 1) << 16);     // below 2^14 each: up to room + used
+            }
+            const int last = total(count[1]), first = total(count[0]);
+            best = (first & 0xffff) <= a.places ? 0 : (first >> 16) <= a.places ? 1 : (last & 0xffff) <= a.places ? 2 : 3;
+        }
+        chunk = uniform(mine, best);
+        inverse = __int_as_float(uniform(__float_as_int(one_over), best));
+    }
+    const int p = parts_in(n, chunk, inverse);
+    const int mine = p * rt, my_slots = p > 1 ? mine : 0, my_cuts = p > 1 ? rt : 0;
+    int end = wave_scan(mine);
+    const int slots_end = wave_scan(my_slots), cuts_end = wave_scan(my_cuts);
+    *splits = total(cuts_end);
+    if (total(end) > a.places) {
+        const int length = p > 0 ? int(float(n) * __builtin_amdgcn_rcpf(float(p))) : 0;
+        float longest = lane_max(float(length));
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) longest = fmaxf(longest, __shfl_xor(longest, d));
+        const int four = 4 * length, most = int(longest), kind = four > 3 * most ? 0 : four > 2 * most ? 1 : four > most ? 2 : 3;
+        int before = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int in = wave_scan(kind == k ? mine : 0);
+            if (kind == k) end = before + in;
+            before += total(in);
+        }
+    }
+    const uint64_t who = __ballot(want >= end - mine && want < end);
+    if (!who) return {-1, 0, 0, 0, 0};
+    const int l = __builtin_ctzll(who);
+    auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+    *sq = {of(s.row0), of(s.n_new), of(s.rows), of(s.p0), of(s.lo), of(s.hi), of(s.len)};
+    return {l, of(p), want - of(end - mine), of(slots_end - my_slots), of(cuts_end - my_cuts)};
+}
+
 // What a workgroup does, from the wave that found out.
 struct Share {
     Item it;
@@ -98,11 +171,20 @@ struct Share {
 __device__ __forceinline__ float max3(float a, float b, float c) { return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c); }
 
 // DQ = head_dim / 64, NT = tiles of 16 query rows, EXT: cap, window, distance bias, or a factor of scores
-// near 0; WAVES: of a part (as attn_kernel).
-template <int DQ, int NT, bool EXT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_cu4(DQ, NT)))) void attn4_kernel(AttnArgs a) {
-    constexpr int D = 64 * DQ, ROWS = 16 * NT, PITCH = 68, F = DQ / 2, H = DQ % 2, S = F + H;   // slabs of 128 channels, of 64
-    __shared__ float merge[WAVES][ROWS][PITCH];     // pitch: rows 4 banks apart
+// near 0; WAVES: of a part (as attn_kernel).  DIRECT: a workgroup takes a whole request, its own number, of one row
+// tile: nothing to look for, nothing to join.
+template <int DQ, int NT, bool EXT, int WAVES, bool DIRECT>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVES == 16 ? 4 : per_cu4(DQ, NT)))) void attn4_kernel(AttnArgs a) {
+    constexpr int D = 64 * DQ, ROWS = 16 * NT, F = DQ / 2, H = DQ % 2, S = F + H;   // slabs of 128 channels, of 64
+    // The waves' sums are joined in LDS, of one row tile all at once, of two 64 channels at a time; of one tile the
+    // queries, which are in registers by then, lie in the same place before.  Pitch: rows 4 banks apart.
+    constexpr int SLABS = NT == 1 ? DQ : 1, PITCH = 64 * SLABS + 4;
+    typedef float Merge[ROWS][PITCH];
+    typedef u32x2 Queries[2][64][2];                     // 64 channels: [hi, lo][lane][8 channels]
+    constexpr int kMergeBytes = WAVES * int(sizeof(Merge)), kQueryBytes = NT * DQ * int(sizeof(Queries));
+    __shared__ __attribute__((aligned(16))) char lds[NT == 1 ? (kMergeBytes > kQueryBytes ? kMergeBytes : kQueryBytes) : kMergeBytes + kQueryBytes];
+    Merge* merge = reinterpret_cast<Merge*>(lds);
+    Queries* queries = reinterpret_cast<Queries*>(lds + (NT == 1 ? 0 : kMergeBytes));
     __shared__ float merge_m[WAVES][ROWS], merge_l[WAVES][ROWS];
     __shared__ Share share;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -112,20 +194,23 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
     // One wave looks for the workgroup's share (400 operations: in every wave at once they kept the
     // vector units busy for the longer part of the start); not always the same, whose SIMD would have it all.
     Share sh;
-    if (WAVES == 1 || wave == int(blockIdx.x / kCus % WAVES)) {
-        sh.it = find_item(a, want, &sh.sq, &sh.splits);
+    if (DIRECT) {
+        sh = {{want, 1, 0, 0, 0}, load_seq(a, want), 0};
+        if (sh.sq.n_new < 1) return;
+    } else if (WAVES == 1 || wave == int(blockIdx.x / kCus % WAVES)) {
+        sh.it = a.n_seqs <= 64 ? find_item_64(a, want, &sh.sq, &sh.splits) : find_item(a, want, &sh.sq, &sh.splits);
         if (WAVES > 1 && lane == 0) share = sh;
     }
-    if (WAVES > 1) {
+    if (WAVES > 1 && !DIRECT) {
         __syncthreads();
         sh.read(share);
     }
     const Item it = sh.it;
     const Seq sq = sh.sq;
     const int splits = sh.splits;
-    if (head == 0 && threadIdx.x == 0 && want >= splits && want < a.n_splits) a.splits[want] = Split{0, 0, 0, 0, 0, 0};
+    if (!DIRECT && head == 0 && threadIdx.x == 0 && want >= splits && want < a.n_splits) a.splits[want] = Split{0, 0, 0, 0, 0, 0};
     if (it.seq < 0) return;
-    const int row_tiles = row_tiles_of(a, sq), part = it.index / row_tiles;
+    const int row_tiles = DIRECT ? 1 : row_tiles_of(a, sq), part = DIRECT ? 0 : it.index / row_tiles;
     const int row_tile = row_tiles - 1 - (it.index - part * row_tiles);       // the last rows, which see most, first
     const int r0 = row_tile * ROWS, slot = it.slot + row_tile;
     const int rows = min(ROWS, sq.rows - r0);
@@ -133,7 +218,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
     const int pos_first = sq.p0 + token_of(a, r0), pos_last = sq.p0 + token_of(a, r0 + rows - 1);
     const int all_end = pos_first + 1, all_begin = a.window > 0 ? max(pos_last, 0) - a.window + 1 : 0;
     int t0 = sq.lo, t1 = min(sq.hi, (max(pos_last + 1, 0) + kTok - 1) / kTok);
-    if (it.parts > 1) {
+    if (!DIRECT && it.parts > 1) {
         // (starts that fall, which no request can have, could count rows twice; in range all the same)
         if (it.split + row_tile >= a.n_splits || slot + int64_t(it.parts - 1) * row_tiles >= a.n_parts) return;
         const int size = even_part(tiles_of(sq), it.parts);
@@ -160,7 +245,6 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
     // it: they see nothing, and nothing of them is kept.
     constexpr bool kQueryLds = NT > 1, kLean = EXT || DQ > 2;
     constexpr int kPieces = NT * 2 * DQ, kMine = (kPieces + WAVES - 1) / WAVES;
-    __shared__ u32x2 queries[NT * DQ][2][64][2];         // [64 channels][hi, lo][lane][8 channels]
     __shared__ uint32_t row_top[WAVES][NT][16];
     uint32_t q_hi[NT], q_lo[NT];         // the rows' scales
     int pos[NT];
@@ -174,74 +258,14 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
         row_at[t] = a.q + int64_t(sq.row0 + j) * a.q_stride + int64_t(qh) * D + 16 * g;
     }
     u32x4 w[kMine];
-    uint32_t most[NT] = {};
 #pragma unroll
     for (int k = 0; k < kMine; ++k) {
         const int piece = WAVES == 1 ? k : k * WAVES + wave, t = piece / (2 * DQ), c = piece % (2 * DQ);
         if (kPieces % WAVES && piece >= kPieces) break;
         w[k] = *reinterpret_cast<const u32x4*>((NT == 1 || t == 0 ? row_at[0] : row_at[NT - 1]) + 64 * (c / 2) + 8 * (c % 2));
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            top = max(top, max(w[k][i] & 0x7fffu, w[k][i] >> 16 & 0x7fffu));
-            w[k][i] ^= a.flip;
-        }
-        if (NT == 1 || t == 0) most[0] = max(most[0], top);
-        else most[NT - 1] = max(most[NT - 1], top);
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        // (a NaN as infinity: max would drop it)
-        most[t] = __float_as_uint(lane_max(__uint_as_float(min(most[t], 0x7f80u) << 16)));
-        if (WAVES > 1 && g == 0) row_top[wave][t][n] = most[t];
-    }
-    if (WAVES > 1) __syncthreads();
-    float down[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        uint32_t top = most[t];
-#pragma unroll
-        for (int v = 0; v < WAVES; ++v)
-            if (WAVES > 1) top = max(top, row_top[v][t][n]);
-        const int e = max(int(top >> 23), 27) - 127;
-        down[t] = __uint_as_float(uint32_t(134 - e) << 23);               // 2^(7 - e)
-        const bool bad = top >= 0x7f800000u;                               // an infinity or NaN: the row's scores are NaN
-        q_hi[t] = bad ? 255u : uint32_t(e + 120);
-        q_lo[t] = bad ? 255u : uint32_t(e + 116);
-    }
-#pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-        const int piece = WAVES == 1 ? k : k * WAVES + wave, t = piece / (2 * DQ), c = piece % (2 * DQ);
-        if (kPieces % WAVES && piece >= kPieces) break;
-        const QuerySplit s = split_query(w[k], NT == 1 || t == 0 ? down[0] : down[NT - 1]);
-        queries[t * DQ + c / 2][0][lane][c % 2] = s.hi;
-        queries[t * DQ + c / 2][1][lane][c % 2] = s.lo;
-    }
-    if (WAVES > 1) __syncthreads();
-    else wave_sync_lds();
-    auto from_lds = [&](int t, int c, int lo) { return *reinterpret_cast<const u32x4*>(&queries[t * DQ + c][lo][lane][0]); };
-    u32x4 held[kQueryLds ? 1 : 2 * DQ];
-    if constexpr (!kQueryLds)
-#pragma unroll
-        for (int c = 0; c < DQ; ++c) {
-            held[2 * c] = from_lds(0, c, 0);
-            held[2 * c + 1] = from_lds(0, c, 1);
-        }
-    auto query = [&](int t, int c, int lo) {
-        if constexpr (kQueryLds) return from_lds(t, c, lo);
-        else return held[2 * c + lo];
-    };
-
-    f32x4 acc[4 * DQ][NT];               // 8 products of a slab of 128 channels, 4 of one of 64
-    float top[NT], sum[NT];              // base of the weights (log2 domain); this lane's share of their sum
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        top[t] = -INFINITY;
-        sum[t] = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4 * DQ; ++c) acc[c][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
+    // The first step's codes are on their way while the queries are split.
     int32_t my_id = -1;
     u32x4 kc[kStep][S], vc[kStep][S];    // one step's codes (of a half slab's values two words)
     uint32_t ks[kStep][S], vs[kStep][S]; // and exponents: of the lane's key, of four tokens' values
@@ -289,6 +313,83 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
             }
         }
     };
+
+    auto refill = [&](int k0) {
+        my_id = next_id >= 0 && next_id < a.n_blocks ? next_id : -1;
+        if (k0 < mine) {
+            load_keys(tile_of(k0), 0);
+            load_values(tile_of(k0), 0);
+        }
+        next_id = look_up(k0 + kRefill);
+    };
+    refill(0);
+
+    uint32_t most[NT] = {};
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        const int piece = WAVES == 1 ? k : k * WAVES + wave, t = piece / (2 * DQ);
+        if (kPieces % WAVES && piece >= kPieces) break;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            top = max(top, max(w[k][i] & 0x7fffu, w[k][i] >> 16 & 0x7fffu));
+            w[k][i] ^= a.flip;
+        }
+        if (NT == 1 || t == 0) most[0] = max(most[0], top);
+        else most[NT - 1] = max(most[NT - 1], top);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        // (a NaN as infinity: max would drop it)
+        most[t] = __float_as_uint(lane_max(__uint_as_float(min(most[t], 0x7f80u) << 16)));
+        if (WAVES > 1 && g == 0) row_top[wave][t][n] = most[t];
+    }
+    if (WAVES > 1) __syncthreads();
+    float down[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        uint32_t top = most[t];
+#pragma unroll
+        for (int v = 0; v < (WAVES < kPieces ? WAVES : kPieces); ++v)
+            if (WAVES > 1) top = max(top, row_top[v][t][n]);
+        const int e = max(int(top >> 23), 27) - 127;
+        down[t] = __uint_as_float(uint32_t(134 - e) << 23);               // 2^(7 - e)
+        const bool bad = top >= 0x7f800000u;                               // an infinity or NaN: the row's scores are NaN
+        q_hi[t] = bad ? 255u : uint32_t(e + 120);
+        q_lo[t] = bad ? 255u : uint32_t(e + 116);
+    }
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        const int piece = WAVES == 1 ? k : k * WAVES + wave, t = piece / (2 * DQ), c = piece % (2 * DQ);
+        if (kPieces % WAVES && piece >= kPieces) break;
+        const QuerySplit s = split_query(w[k], NT == 1 || t == 0 ? down[0] : down[NT - 1]);
+        queries[t * DQ + c / 2][0][lane][c % 2] = s.hi;
+        queries[t * DQ + c / 2][1][lane][c % 2] = s.lo;
+    }
+    if (WAVES > 1) __syncthreads();
+    else wave_sync_lds();
+    auto from_lds = [&](int t, int c, int lo) { return *reinterpret_cast<const u32x4*>(&queries[t * DQ + c][lo][lane][0]); };
+    u32x4 held[kQueryLds ? 1 : 2 * DQ];
+    if constexpr (!kQueryLds)
+#pragma unroll
+        for (int c = 0; c < DQ; ++c) {
+            held[2 * c] = from_lds(0, c, 0);
+            held[2 * c + 1] = from_lds(0, c, 1);
+        }
+    auto query = [&](int t, int c, int lo) {
+        if constexpr (kQueryLds) return from_lds(t, c, lo);
+        else return held[2 * c + lo];
+    };
+
+    f32x4 acc[4 * DQ][NT];               // 8 products of a slab of 128 channels, 4 of one of 64
+    float top[NT], sum[NT];              // base of the weights (log2 domain); this lane's share of their sum
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        top[t] = -INFINITY;
+        sum[t] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4 * DQ; ++c) acc[c][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
 
     auto step = [&](int tile, int l, int next_tile, bool more) {
         if (kQueryLds) asm volatile("" ::: "memory");      // the queries are read again in each step
@@ -428,13 +529,11 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
         if (more) load_values(next_tile, l + kStep);
     };
 
-    for (int k0 = 0; k0 < mine; k0 += kRefill) {
-        my_id = next_id >= 0 && next_id < a.n_blocks ? next_id : -1;
+    for (int k0 = 0; k0 < mine;) {
         const int end = min(mine - k0, kRefill);
-        load_keys(tile_of(k0), 0);
-        load_values(tile_of(k0), 0);
-        next_id = look_up(k0 + kRefill);
         for (int k = 0; k < end; ++k) step(tile_of(k0 + k), kStep * k, tile_of(k0 + k + 1), k + 1 < end);
+        k0 += kRefill;
+        if (k0 < mine) refill(k0);
     }
 
     // A row's four channels from d on: final, from their weighted sum, and the row's sum of weights.
@@ -465,17 +564,21 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
         f[t] = __builtin_amdgcn_exp2f(top[t] - (m == -INFINITY ? 0.f : m));
     }
 #pragma unroll
-    for (int c = 0; c < DQ; ++c) {
-        if (c) __syncthreads();
+    for (int c0 = 0; c0 < DQ; c0 += SLABS) {
+        if (c0) __syncthreads();
 #pragma unroll
         for (int t = 0; t < NT; ++t)
+            if (16 * t + n < rows)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)      // register i of product j: channel j of the octet (in a half slab, the four) 4 g + i
-                *reinterpret_cast<f32x4*>(&merge[wave][16 * t + n][16 * g + 4 * i]) =
-                    f32x4{acc[4 * c][t][i], acc[4 * c + 1][t][i], acc[4 * c + 2][t][i], acc[4 * c + 3][t][i]} * f[t];
+                for (int c = c0; c < c0 + SLABS; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)  // register i of product j: channel j of the octet (in a half slab, the four) 4 g + i
+                        *reinterpret_cast<f32x4*>(&merge[wave][16 * t + n][64 * (c - c0) + 16 * g + 4 * i]) =
+                            f32x4{acc[4 * c][t][i], acc[4 * c + 1][t][i], acc[4 * c + 2][t][i], acc[4 * c + 3][t][i]} * f[t];
         __syncthreads();
-        for (int e = threadIdx.x; e < rows * 16; e += 64 * WAVES) {
-            const int r = e >> 4, unit = e & 15, d = c < 2 * F ? c / 2 * 128 + unit * 8 + c % 2 * 4 : F * 128 + unit * 4;
+        for (int e = threadIdx.x; e < rows * 16 * SLABS; e += 64 * WAVES) {
+            const int r = e / (16 * SLABS), at = e % (16 * SLABS), c = c0 + at / 16, unit = at & 15;
+            const int d = c < 2 * F ? c / 2 * 128 + unit * 8 + c % 2 * 4 : F * 128 + unit * 4;
             float m = -INFINITY, l = 0.f;
 #pragma unroll
             for (int w = 0; w < WAVES; ++w) m = fmaxf(m, merge_m[w][r]);
@@ -484,9 +587,9 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(per_
 #pragma unroll
             for (int w = 0; w < WAVES; ++w) {
                 l += merge_l[w][r] * __builtin_amdgcn_exp2f(merge_m[w][r] - base);
-                o += *reinterpret_cast<const f32x4*>(&merge[w][r][unit * 4]);
+                o += *reinterpret_cast<const f32x4*>(&merge[w][r][at * 4]);
             }
-            if (it.parts == 1) {
+            if (DIRECT || it.parts == 1) {
                 put(r, d, o, m, l);
             } else {
                 const int64_t to = ((slot + int64_t(part) * row_tiles) * a.n_kv + head) * ROWS + r;

@@ -378,6 +378,15 @@ def test_attn_empty_rows(dev):
         _run(dev, dim, 16, 1, 2, [64, 700, 20], [1, 2, 1], holes=[(0, 1), (1, 0), (1, 7), (1, 43), (2, 0), (2, 1)])
 
 
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("opts", [{}, dict(softcap=8.0, alibi=True), dict(window=300)])
+def test_attn_whole_requests(dev, dim, opts):
+    """Tables or windows so short that a workgroup takes a whole request: few and many of them, empty ones, all rows of a tile."""
+    for hkv, group, lens, new in ((2, 4, [2048, 1, 0, 333, 16], [1, 1, 1, 4, 2]), (1, 3, [700, 40, 0], [5, 0, 3]), (70, 1, [60, 33, 90, 1, 250, 17, 18, 100], [1] * 8)):
+        _run(dev, dim, 32, hkv, group, lens, new, pad=1, qpad=8, **opts)
+    _run(dev, dim, 16, 1, 2, [5000, 4100], [2, 1], window=1900)
+
+
 def test_attn_split_long(dev):
     """Long requests beside short ones: parts joined from the workspace."""
     _run(dev, 128, 64, 1, 8, [20000, 1, 300, 4097], [1, 1, 1, 1])
@@ -392,6 +401,20 @@ def test_attn_prompts_beside_decodes(dev):
 
 def test_attn_row_tiles_beyond_places(dev):
     _run(dev, 256, 32, 4, 16, [9000] + [24] * 70, [1] + [24] * 70)
+
+
+def test_attn_prompts_beyond_places(dev):
+    """More row tiles than places in few requests: the longest start first, and nothing is cut or done twice."""
+    _run(dev, 64, 32, 16, 2, [500, 900, 310], [500, 400, 300])
+    _run(dev, 64, 32, 16, 2, [310, 4000, 700], [300, 40, 690], window=700)
+
+
+@pytest.mark.parametrize("n", [5, 33, 40, 63, 64, 65])
+def test_attn_shares_of_ragged_requests(dev, n):
+    """Requests of all lengths around the chunk that they are cut by, up to and past a wave's lanes."""
+    rng = np.random.default_rng(n)
+    for dim, hkv in ((64, 4), (128, 32)):
+        _run(dev, dim, 16, hkv, 1, [int(x) for x in 2 ** rng.uniform(0, 11, n)], [1] * n)
 
 
 @pytest.mark.parametrize("dim", [64, 128, 192, 256])
