@@ -229,7 +229,26 @@ struct AppendArgs {
     int32_t n_slots;      // slots of the cache
     int32_t T, window, n_heads, head_dim, shift;
     Turn turn;            // table is NULL: no rotation
+    int32_t columns, rows, q_heads;   // with it: workgroups of keys and values side by side, windows of them, query heads of a task
 };
+
+// Where a workgroup with TURN stands among those of keys and values (x < 0: behind them, taking queries).
+struct TurnBlock { int x, y, queries; };
+
+__device__ __forceinline__ TurnBlock turn_block(const AppendArgs& a) {
+    const int64_t own = int64_t(a.columns) * a.rows;
+    if (blockIdx.x >= own) return {-1, 0, int(blockIdx.x - own)};
+    const int y = blockIdx.x / uint32_t(a.columns);
+    return {int(blockIdx.x - y * a.columns), y, 0};
+}
+
+template <class T>
+__device__ __forceinline__ void turn_query_task(const AppendArgs& a, int block) {
+    const int task = block * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), columns = a.head_dim / 64;
+    const int blocks = (a.turn.n_q_heads + a.q_heads - 1) / a.q_heads, window = task / (columns * blocks), in = task - window * (columns * blocks);
+    const int h0 = in / columns * a.q_heads;
+    turn_queries<T>(a.turn, int64_t(window) * kTurnRows, a.T, in % columns, h0, min(h0 + a.q_heads, a.turn.n_q_heads), a.head_dim);
+}
 
 template <bool E4M3>
 __device__ __forceinline__ float wanted_scale(float amax) {
@@ -261,26 +280,27 @@ __device__ __forceinline__ uint32_t encode(const float v[4]) {
     return w;
 }
 
-// Sixteen values x over a scale, as the codes of one unit.  r is the scale's reciprocal,
+// Four values a word x over a scale, as codes (of a unit: four words).  r is the scale's reciprocal,
 // correctly rounded.  E4M3: where the scale is a power of two, the product is the quotient.  INT8:
 // Markstein's theorem (IBM J. Res. Dev. 34, 1990): for such an r and a q within an ulp of
 // x / s, q + r (x - q s) with fused operations rounds correctly; three operations where a
 // division without r takes ten and more.  Adding 1.5 * 2^23 then rounds to a whole number,
 // ties to even, whose low byte is the code.  (The bare product x r will not do: a value of half
 // the block's maximum is a tie, 63.5, which is found in two of three waves.)
-template <bool E4M3>
-__device__ __forceinline__ u32x4 encode_unit(const float x[16], float div, float r, bool any_values) {
-    u32x4 w;
+template <bool E4M3, class W = u32x4>
+__device__ __forceinline__ W encode_unit(const float* x, float div, float r, bool any_values) {
+    constexpr int words = sizeof(W) / 4;
+    W w;
     if (!any_values) {
         if constexpr (E4M3) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < words; ++q) {
                 const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * q] * r, x[4 * q + 1] * r, 0, false);
                 w[q] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(x[4 * q + 2] * r, x[4 * q + 3] * r, lo, true));
             }
         } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < words; ++q) {
                 uint32_t c[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -293,7 +313,7 @@ __device__ __forceinline__ u32x4 encode_unit(const float x[16], float div, float
         return w;
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < words; ++q) {
         const float v[4] = {x[4 * q] / div, x[4 * q + 1] / div, x[4 * q + 2] / div, x[4 * q + 3] / div};
         w[q] = encode<E4M3>(v);
     }
@@ -340,18 +360,12 @@ template <> struct Quad<uint16_t> {
     }
 };
 
-// (of a quad that turned() fills, nothing is loaded as it lies)
-template <class X, class T> __device__ __forceinline__ void load_quad(X& x, const T* p) {
-    if constexpr (std::is_same<X, Quad<T>>::value) x.load(p);
-}
-
 // The tokens of one block that the call brings, places [fill, end), for one head's keys
 // or values, by THREADS threads (a wave, or a workgroup of 256), each with KEEP units in
 // registers between the maximum and the codes (more are read again).  A unit is 16
 // bytes of a code tile: lane (g, m) of slab s holds, of a key tile, token m and channels
-// 64s + 16g .. +16; of a value tile, tokens 4g .. +4 and channels 64s + 4m .. +4.  TURN: keys are
-// turned as they are loaded, and held in fp32 from there.
-template <bool E4M3, bool V, bool TURN, class T, int THREADS, int KEEP>
+// 64s + 16g .. +16; of a value tile, tokens 4g .. +4 and channels 64s + 4m .. +4.
+template <bool E4M3, bool V, class T, int THREADS, int KEEP>
 __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, int64_t block, int fill, int end, int head, uint32_t* lds) {
     const int tid = THREADS == 64 ? threadIdx.x & 63 : threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, m = lane & 15;
@@ -360,12 +374,10 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
     uint8_t* codes = a.codes[V] + ((bh * D) << a.shift);
     const int64_t stride = a.stride[V];
     const T* row0 = static_cast<const T*>(a.x[V]) + int64_t(token) * stride + int64_t(head) * D;
-    constexpr bool turn = TURN && !V;
-    using X = Quad<typename std::conditional<turn, float, T>::type>;
     const float old_scale = fill > 0 ? a.scales[V][bh] : 0.f;
     const int tile0 = fill / kTok, chunks = ((end - 1) / kTok + 1 - tile0) * slabs;   // 64 units each
 
-    X x[KEEP][4];
+    Quad<T> x[KEEP][4];
     u32x4 old[THREADS == 64 ? KEEP : 1];
     auto first_token = [&](int tile) { return tile * kTok + (V ? 4 * g : m); };
     auto unit_at = [&](int tile, int s) { return reinterpret_cast<u32x4*>(codes + int64_t(tile) * kTok * D + s * 1024 + lane * 16); };
@@ -383,35 +395,23 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
             const int c = c0 + i * (THREADS / 64) + wave;
             const int tile = tile0 + c / slabs, s = c % slabs, first = first_token(tile);
             const T* from = row0 + (first - fill) * stride + 64 * s + (V ? 4 * m : 16 * g);
-            if constexpr (turn) {
-                const int32_t row = first - fill;                // of a unit's one token in the run
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[i][k].clear();
-                if (c < chunks && first >= fill && first < end) {
-                    const float* angles = a.turn.table + int64_t(a.turn.positions[token + row]) * a.turn.rot;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[i][k].v = turned(a.turn, row0 + row * stride, angles, 64 * s + 16 * g + 4 * k);
-                }
-                if constexpr (THREADS == 64) old[i] = boundary(c < chunks && !all_new(tile), tile, s);
-                continue;
-            }
             if (c < chunks && all_new(tile)) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) load_quad(x[i][k], from + (V ? k * stride : 4 * k));
+                for (int k = 0; k < 4; ++k) x[i][k].load(from + (V ? k * stride : 4 * k));
                 continue;
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int tok = V ? first + k : first;
                 x[i][k].clear();
-                if (c < chunks && tok >= fill && tok < end) load_quad(x[i][k], from + (V ? k * stride : 4 * k));
+                if (c < chunks && tok >= fill && tok < end) x[i][k].load(from + (V ? k * stride : 4 * k));
             }
             if constexpr (THREADS == 64) old[i] = boundary(c < chunks, tile, s);   // early: few waves, so latency counts
         }
     };
     constexpr int round = KEEP * (THREADS / 64);
     const bool once = chunks <= round;
-    typename X::Top most{};
+    typename Quad<T>::Top most{};
     for (int c0 = 0; c0 < chunks; c0 += round) {
         load(c0);
 #pragma unroll
@@ -431,7 +431,7 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
         }
         return uint32_t(__builtin_amdgcn_readfirstlane(int(v)));
     };
-    uint32_t top = reduce(X::bits(most));
+    uint32_t top = reduce(Quad<T>::bits(most));
     const bool finite = top < 0x7f800000u;
     if (!finite) {                       // the largest of the finite values
         top = 0;
@@ -494,6 +494,99 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
         }
 }
 
+// append_run of turned keys.  A lane takes octets of one token each, so that a wave reads whole rows and the partners lie in
+// a lane's own row; PASSES rounds of them stay in registers between the maximum and the codes (more are turned
+// again).  An octet of new codes is eight bytes of its own; old ones are met only where the scale grew.
+template <bool E4M3, class T, int THREADS, int PASSES>
+__device__ __forceinline__ void append_turned_keys(const AppendArgs& a, int32_t token, int64_t block, int fill, int end, int head, uint32_t* lds) {
+    const int tid = THREADS == 64 ? threadIdx.x & 63 : threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int D = a.head_dim, octets = D / 8, units = (end - fill) * octets;
+    const int64_t bh = block * a.n_heads + head;
+    uint8_t* codes = a.codes[0] + ((bh * D) << a.shift);
+    const T* row0 = static_cast<const T*>(a.x[0]) + int64_t(token) * a.stride[0] + int64_t(head) * D;
+    const float old_scale = fill > 0 ? a.scales[0][bh] : 0.f;
+    f32x4 x[PASSES][2];
+    auto place = [&](int u, int* d) {                         // token of unit u in the run, and its first channel
+        const int r = u / octets;
+        *d = (u - r * octets) * 8;
+        return r;
+    };
+    auto load = [&](int u0) {
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            x[i][0] = x[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+            const int u = u0 + i * THREADS + tid;
+            if (u >= units) continue;
+            int d;
+            const int r = place(u, &d);
+            const float* row = a.turn.table + int64_t(a.turn.positions[token + r]) * a.turn.rot;
+            Angles a0, a1;
+            a0.load(a.turn, row, d);
+            a1.load(a.turn, row, d + 4);
+            each_head<true>(a.turn, row0 + r * a.stride[0], d, 0, 0, 1, a0, a1, [&](int, const f32x4 x0, const f32x4 x1) {
+                x[i][0] = x0;
+                x[i][1] = x1;
+            });
+        }
+    };
+    constexpr int round = PASSES * THREADS;
+    const bool once = units <= round;
+    uint32_t top = 0;                    // the largest of the finite values; bit 31: there are others
+    for (int u0 = 0; u0 < units; u0 += round) {
+        load(u0);
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t b = __float_as_uint(x[i][j / 4][j % 4]) & 0x7fffffffu;
+                top = b < 0x7f800000u ? max(top & 0x7fffffffu, b) | (top & 0x80000000u) : top | 0x80000000u;
+            }
+    }
+    auto both = [](uint32_t p, uint32_t q) { return max(p & 0x7fffffffu, q & 0x7fffffffu) | ((p | q) & 0x80000000u); };
+#pragma unroll
+    for (int d = 32; d; d >>= 1) top = both(top, uint32_t(__shfl_xor(int(top), d)));
+    if constexpr (THREADS > 64) {
+        __syncthreads();
+        if (lane == 0) lds[wave] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < THREADS / 64; ++w) top = both(top, lds[w]);
+    }
+    top = uint32_t(__builtin_amdgcn_readfirstlane(int(top)));
+    const bool finite = !(top >> 31);
+    const float wanted = wanted_scale<E4M3>(__uint_as_float(top & 0x7fffffffu));
+    const bool grew = wanted > old_scale;
+    const float now = grew ? wanted : old_scale, div = now > 0.f ? now : 1.f, r = 1.f / div, ratio = old_scale / div;
+    const bool any_values = !finite || !(div >= 0x1p-100f) || (E4M3 && (__float_as_uint(div) & 0x7fffffu));     // as in append_run
+    if (tid == 0 && (grew || fill == 0)) a.scales[0][bh] = now;
+    for (int u0 = 0; u0 < units; u0 += round) {
+        if (!once) load(u0);
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            const int u = u0 + i * THREADS + tid;
+            if (u >= units) continue;
+            int d;
+            const int t = fill + place(u, &d);
+            const float v[8] = {x[i][0][0], x[i][0][1], x[i][0][2], x[i][0][3], x[i][1][0], x[i][1][1], x[i][1][2], x[i][1][3]};
+            *reinterpret_cast<u32x2*>(codes + int64_t(t / kTok) * kTok * D + d / 64 * 1024 + d / 16 % 4 * 256 + t % kTok * 16 + d % 16) =
+                encode_unit<E4M3, u32x2>(v, div, r, any_values);
+        }
+    }
+    if (grew && fill > 0)                // tokens of before: a unit of 16 bytes is one token's
+        for (int c = wave; c < ((fill - 1) / kTok + 1) * (D / 64); c += THREADS / 64) {
+            const int tile = c / (D / 64);
+            u32x4* unit = reinterpret_cast<u32x4*>(codes + int64_t(tile) * kTok * D + c % (D / 64) * 1024 + lane * 16);
+            if (tile * kTok + (lane & 15) < fill) *unit = rescale_unit<E4M3>(*unit, ratio);
+        }
+}
+
+template <bool E4M3, class T, bool TURN, int THREADS, int KEEP>
+__device__ __forceinline__ void append_keys(const AppendArgs& a, int32_t token, int64_t block, int fill, int end, int head, uint32_t* lds) {
+    if constexpr (TURN) append_turned_keys<E4M3, T, THREADS, 4>(a, token, block, fill, end, head, lds);
+    else append_run<E4M3, false, T, THREADS, KEEP>(a, token, block, fill, end, head, lds);
+}
+
 // What a wave sees of the slots from token t0 on: lane l holds token t0 + l's; a bit of
 // `starts` is a token that begins a run, of `more[0]`, `more[1]` one of the first 128 that
 // goes on with its predecessor's run (the next place of the same block).
@@ -541,32 +634,29 @@ __device__ __forceinline__ int run_length(const AppendArgs& a, const Look& k, in
     return count;
 }
 
-// An octet for each thread of the queries of a window's tokens, `part` the workgroup.
-template <class T>
-__device__ __forceinline__ void turn_queries(const AppendArgs& a, int32_t t0, int part) {
-    const int octets = a.turn.n_q_heads * (a.head_dim / 8), e = part * 256 + threadIdx.x, i = e / octets;
-    if (i < a.window && t0 + int64_t(i) < a.T) turn_query<T>(a.turn, t0 + i, e - i * octets, a.head_dim);
-}
-
 // Few tokens: a wave for each (token, head, keys or values), busy where the token begins
 // a run.  The waves of a workgroup take neighbouring heads, which lie side by side.  Bound by
 // its chain of loads (slots -> values, old codes, scale): one token 5.2 us, a verify step of 48
 // requests x 0..9 tokens (fp32, 236 rows) 7.7 us.
 template <bool E4M3, class T, bool TURN>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
-    const int hw = blockIdx.x * 4 + (threadIdx.x >> 6), own = (2 * a.n_heads + 3) / 4;
-    const int32_t t0 = int32_t(blockIdx.y);
+    int x = blockIdx.x, y = blockIdx.y;
     if constexpr (TURN) {
-        if (int(blockIdx.x) >= own) return turn_queries<T>(a, t0, blockIdx.x - own);
+        const TurnBlock b = turn_block(a);
+        if (b.x < 0) return turn_query_task<T>(a, b.queries);
+        x = b.x;
+        y = b.y;
     }
+    const int hw = x * 4 + (threadIdx.x >> 6);
     if (hw >= 2 * a.n_heads) return;
     const int head = hw % a.n_heads;
+    const int32_t t0 = y;
     const Look k = look_at<TURN>(a, t0);
     if (!k.starts) return;
     const int32_t first = __builtin_amdgcn_readfirstlane(k.slot);
     const int fill = first & ((1 << a.shift) - 1), end = fill + run_length<TURN>(a, k, t0, 0, first);
-    if (hw >= a.n_heads) append_run<E4M3, true, TURN, T, 64, 4>(a, t0, first >> a.shift, fill, end, head, nullptr);
-    else append_run<E4M3, false, TURN, T, 64, 4>(a, t0, first >> a.shift, fill, end, head, nullptr);
+    if (hw >= a.n_heads) append_run<E4M3, true, T, 64, 4>(a, t0, first >> a.shift, fill, end, head, nullptr);
+    else append_keys<E4M3, T, TURN, 64, 4>(a, t0, first >> a.shift, fill, end, head, nullptr);
 }
 
 // Many tokens: a workgroup for each (window of tokens, head, keys or values).  Long runs
@@ -579,16 +669,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TURN ? 3 : 
     __shared__ uint32_t lds[4];
     constexpr int kept = 2;            // fewer registers, more workgroups in flight
     const int wave = threadIdx.x >> 6;
-    const int head = blockIdx.x % uint32_t(a.n_heads);
-    const bool values = int(blockIdx.x) >= a.n_heads;
-    for (int64_t at = int64_t(blockIdx.y) * a.window; at < a.T; at += int64_t(gridDim.y) * a.window) {
+    int x = blockIdx.x, y = blockIdx.y, rows = gridDim.y;
+    if constexpr (TURN) {
+        const TurnBlock b = turn_block(a);
+        if (b.x < 0) return turn_query_task<T>(a, b.queries);
+        x = b.x;
+        y = b.y;
+        rows = a.rows;
+    }
+    const int head = x % a.n_heads;
+    const bool values = x >= a.n_heads;
+    for (int64_t at = int64_t(y) * a.window; at < a.T; at += int64_t(rows) * a.window) {
         const int32_t t0 = int32_t(at);
-        if constexpr (TURN) {
-            if (int(blockIdx.x) >= 2 * a.n_heads) {
-                turn_queries<T>(a, t0, blockIdx.x - 2 * a.n_heads);
-                continue;
-            }
-        }
         const Look k = look_at<TURN>(a, t0);               // the same in every wave
         uint64_t todo = k.starts;
         for (int turn = 0; todo; ++turn) {
@@ -597,11 +689,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TURN ? 3 : 
             const int32_t first = __builtin_amdgcn_readlane(k.slot, l), token = t0 + l;
             const int fill = first & ((1 << a.shift) - 1), end = fill + run_length<TURN>(a, k, t0, l, first);
             if (((end - 1) / kTok + 1 - fill / kTok) * a.head_dim > 64 * kept) {
-                if (values) append_run<E4M3, true, TURN, T, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
-                else append_run<E4M3, false, TURN, T, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
+                if (values) append_run<E4M3, true, T, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
+                else append_keys<E4M3, T, TURN, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
             } else if (turn % 4 == wave) {
-                if (values) append_run<E4M3, true, TURN, T, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
-                else append_run<E4M3, false, TURN, T, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
+                if (values) append_run<E4M3, true, T, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
+                else append_keys<E4M3, T, TURN, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
             }
         }
     }
@@ -741,10 +833,16 @@ static mbd_status append(const mbd_kv_cache* cache, const Turn& turn, const void
     AppendArgs a{{static_cast<uint8_t*>(cache->k_codes), static_cast<uint8_t*>(cache->v_codes)},
                  {static_cast<float*>(cache->k_scale), static_cast<float*>(cache->v_scale)},
                  {k, v}, {k_stride, v_stride}, slots, int32_t(cache->n_blocks * cache->block_size), T, window, cache->n_heads,
-                 cache->head_dim, log2_of(cache->block_size), turn};
-    const int own = few ? (2 * cache->n_heads + 3) / 4 : 2 * cache->n_heads;
-    const int turns = turn.table ? (window * turn.n_q_heads * (cache->head_dim / 8) + 255) / 256 : 0;      // the queries' workgroups
-    const dim3 grid(unsigned(own + turns), unsigned(std::min((T + window - 1) / window, 65535)));
+                 cache->head_dim, log2_of(cache->block_size), turn, 0, 0, 1};
+    a.columns = few ? (2 * cache->n_heads + 3) / 4 : 2 * cache->n_heads;
+    a.rows = std::min((T + window - 1) / window, 65535);
+    dim3 grid(unsigned(a.columns), unsigned(a.rows));
+    if (turn.table) {                    // keys and values in one row of workgroups, and the queries behind them
+        const int64_t windows = (int64_t(T) + kTurnRows - 1) / kTurnRows, dq = cache->head_dim / 64;
+        while (a.q_heads < 8 && windows * dq * turn.n_q_heads / (2 * a.q_heads) >= 4096) a.q_heads *= 2;
+        const int64_t tasks = windows * dq * ((turn.n_q_heads + a.q_heads - 1) / a.q_heads);
+        grid = dim3(unsigned(int64_t(a.columns) * a.rows + (tasks + 3) / 4));
+    }
     const auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a); };
     const auto pick = [&](auto e4m3, auto type, auto turns_keys) {
         constexpr bool E = decltype(e4m3)::value, U = decltype(turns_keys)::value;

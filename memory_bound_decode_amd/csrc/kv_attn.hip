@@ -496,8 +496,13 @@ static void lay_out(const mbd_kv_cache* c, int64_t tiles, int64_t seq_tiles, Pla
     p->bytes = p->parts * c->n_heads * (16u * p->nt) * (c->head_dim + 2) * sizeof(float) + p->splits * sizeof(Split);
 }
 
-// 4 bits: requests of which a query sees at most this many tiles are not cut (see direct_waves).
-constexpr int64_t kDirectTiles = 128;
+// 4 bits: requests of which a query sees at most 2048 tokens are not cut, if there are workgroups for half the CUs, or
+// each has at most 64 KB to read: a CU alone reads about 45 GB/s.  (Cut and whole: a verify step of 8 x 5 tokens x 16
+// heads behind a window of 1024 14.1 and 10.7 us, 256 requests of up to 1000 45 and 34, 1000 of up to 600 89 and 46;
+// one request of 2048 x 8 heads 10.2 and 11.6.)
+static bool takes_whole(const mbd_kv_cache* c, int32_t n_seqs, int64_t seen) {
+    return seen <= 128 && (int64_t(n_seqs) * c->n_heads >= kCus / 2 || seen * 17 * c->head_dim <= 65536);
+}
 
 // Waves of a workgroup that takes a whole request: as many as a CU holds, or four where there are requests enough to
 // fill the chip so.
@@ -525,7 +530,7 @@ static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs
     p->waves = p->nt == 1 && tiles > places_of(c, 1, kMaxWaves) ? 1 : kMaxWaves;
     lay_out(c, tiles, seq_tiles, p);
     const int64_t seen = window > 0 ? std::min(seq_tiles, (int64_t(window) + max_new - 2) / kTok + 2) : seq_tiles;
-    p->direct = c->fmt == MBD_KV_MXFP4 && p->nt == 1 && seen <= kDirectTiles;
+    p->direct = c->fmt == MBD_KV_MXFP4 && p->nt == 1 && takes_whole(c, n_seqs, seen);
     if (p->direct) {
         p->waves = direct_waves(c, n_seqs);
         p->split = false;
@@ -540,7 +545,6 @@ static mbd_status plan_of(const mbd_kv_cache* c, int32_t n_heads, int32_t n_seqs
 static uint64_t largest_workspace(const mbd_kv_cache* c, int32_t n_seqs, int32_t max_blocks, const Plan& own) {
     const int64_t seq_tiles = int64_t(max_blocks) * (c->block_size / kTok);
     uint64_t bytes = own.bytes;
-    if (own.direct) return bytes;              // and so is every smaller call
     if (own.group > 16) return bytes;          // a single token has two row tiles
     Plan p{};
     p.nt = 1;

@@ -15,9 +15,6 @@
 namespace mbd {
 namespace kv {
 
-constexpr int kRows4 = 8;                // tokens of a wave
-constexpr int kHeads4 = 4;               // heads whose loads are in flight together
-
 struct Cache4Args {
     uint8_t *codes[2], *scales[2];
     const int32_t* slots;
@@ -85,29 +82,6 @@ __device__ __forceinline__ uint32_t encode4(const f32x4 x0, const f32x4 x1, int*
     return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], s, 3);
 }
 
-// Eight channels as loaded, all from one address or each four from its own.
-template <class T> struct Eight;
-template <> struct Eight<float> {
-    f32x4 a, b;
-    __device__ void load(const float* p) { load(p, p + 4); }
-    __device__ void load(const float* p, const float* q) { a = load4(p), b = load4(q); }
-    __device__ f32x4 low() const { return a; }
-    __device__ f32x4 high() const { return b; }
-};
-template <> struct Eight<uint16_t> {
-    u32x4 w;
-    static __device__ f32x4 four(uint32_t x, uint32_t y) {
-        return f32x4{__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u), __uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u)};
-    }
-    __device__ void load(const uint16_t* p) { w = *reinterpret_cast<const u32x4*>(p); }
-    __device__ void load(const uint16_t* p, const uint16_t* q) {
-        const u32x2 x = *reinterpret_cast<const u32x2*>(p), y = *reinterpret_cast<const u32x2*>(q);
-        w = u32x4{x[0], x[1], y[0], y[1]};
-    }
-    __device__ f32x4 low() const { return four(w[0], w[1]); }
-    __device__ f32x4 high() const { return four(w[2], w[3]); }
-};
-
 template <int DQ, class T, bool TURN>
 __global__ __launch_bounds__(256) void append4_kernel(Append4Args a) {
     constexpr int D = 64 * DQ;
@@ -118,12 +92,12 @@ __global__ __launch_bounds__(256) void append4_kernel(Append4Args a) {
     const int mine = task - side * a.kv_tasks, d = mine % DQ * 64 + (lane & 7) * 8;
     const int h0 = mine / DQ * a.heads, h1 = min(h0 + a.heads, side == 2 ? a.turn.n_q_heads : a.c.n_heads);
     const bool turns = TURN && side != 1;
-    const T* x = static_cast<const T*>(side == 2 ? a.turn.q : a.x[side & 1]);
+    const T* rows = static_cast<const T*>(side == 2 ? a.turn.q : a.x[side & 1]);
     const int64_t stride = side == 2 ? a.turn.q_stride : a.stride[side & 1];
-    for (int64_t w0 = int64_t(blockIdx.y) * kRows4; w0 < a.c.T; w0 += int64_t(gridDim.y) * kRows4) {
+    for (int64_t w0 = int64_t(blockIdx.y) * kTurnRows; w0 < a.c.T; w0 += int64_t(gridDim.y) * kTurnRows) {
         const int64_t token = w0 + (lane >> 3);
         if (token >= a.c.T) continue;
-        const T* from = x + token * stride + d;
+        const T* from = rows + token * stride;
         Angles a0, a1;
         if constexpr (TURN) {
             const int32_t p = a.turn.positions[token];
@@ -137,48 +111,21 @@ __global__ __launch_bounds__(256) void append4_kernel(Append4Args a) {
         }
         const int32_t slot = side == 2 ? 0 : a.c.slots[token];
         if (slot < 0 || slot >= a.c.n_slots) continue;
-        const bool whole = TURN && a.turn.rot % 16 == 0;     // an octet's partners are an octet
-        for (int hb = h0; hb < h1; hb += kHeads4) {
-            Eight<T> x[kHeads4], y[kHeads4];
-#pragma unroll
-            for (int i = 0; i < kHeads4; ++i) {
-                if (hb + i >= h1) break;
-                const T* head = from + (hb + i) * D;
-                x[i].load(head);
-                if (TURN && !a.turn.pairs) {             // (channels that are not turned load themselves)
-                    const T *p = a0.partner < 0 ? head : head - d + a0.partner, *q = a1.partner < 0 ? head + 4 : head - d + a1.partner;
-                    if (whole) y[i].load(p);
-                    else y[i].load(p, q);
-                }
+        auto put = [&](int h, const f32x4 x0, const f32x4 x1) {
+            if (TURN && side == 2) return store_query(a.turn, token, int64_t(h) * D + d, x0, x1);
+            int e;
+            const uint32_t codes = encode4(x0, x1, &e);
+            const Place4<DQ> at(a.c, slot, h);
+            uint8_t* to = a.c.codes[side & 1] + (side ? at.value(d) : at.key(d));
+            if ((lane & 3) == 0) a.c.scales[side & 1][at.scale(d)] = uint8_t(e);
+            if (side && Place4<DQ>::halved(d)) {
+                *reinterpret_cast<uint16_t*>(to) = uint16_t(codes);
+                *reinterpret_cast<uint16_t*>(to + 8) = uint16_t(codes >> 16);
+            } else {
+                *reinterpret_cast<uint32_t*>(to) = codes;
             }
-#pragma unroll
-            for (int i = 0; i < kHeads4; ++i) {
-                if (hb + i >= h1) break;
-                f32x4 x0 = x[i].low(), x1 = x[i].high();
-                if (TURN) {
-                    const bool pairs = a.turn.pairs;
-                    const f32x4 y0 = pairs ? f32x4{x0[1], x0[0], x0[3], x0[2]} : y[i].low(), y1 = pairs ? f32x4{x1[1], x1[0], x1[3], x1[2]} : y[i].high();
-                    if (a0.partner >= 0) x0 = a0.turn(x0, y0);
-                    if (a1.partner >= 0) x1 = a1.turn(x1, y1);
-                    if (side == 2) {
-                        *reinterpret_cast<u32x4*>(a.turn.q_out + token * a.turn.q_out_stride + (hb + i) * D + d) =
-                            u32x4{pack_bf16(x0[0], x0[1]), pack_bf16(x0[2], x0[3]), pack_bf16(x1[0], x1[1]), pack_bf16(x1[2], x1[3])};
-                        continue;
-                    }
-                }
-                int e;
-                const uint32_t codes = encode4(x0, x1, &e);
-                const Place4<DQ> at(a.c, slot, hb + i);
-                uint8_t* to = a.c.codes[side & 1] + (side ? at.value(d) : at.key(d));
-                if ((lane & 3) == 0) a.c.scales[side & 1][at.scale(d)] = uint8_t(e);
-                if (side && Place4<DQ>::halved(d)) {
-                    *reinterpret_cast<uint16_t*>(to) = uint16_t(codes);
-                    *reinterpret_cast<uint16_t*>(to + 8) = uint16_t(codes >> 16);
-                } else {
-                    *reinterpret_cast<uint32_t*>(to) = codes;
-                }
-            }
-        }
+        };
+        each_head<TURN>(a.turn, from, d, D, h0, h1, a0, a1, put);
     }
 }
 
@@ -256,7 +203,7 @@ template <class T>
 void append4(const mbd_kv_cache* c, const Turn& turn, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
              const int32_t* slots, int32_t T_, hipStream_t s) {
     const int dq = c->head_dim / 64;
-    const int64_t windows = (int64_t(T_) + kRows4 - 1) / kRows4;
+    const int64_t windows = (int64_t(T_) + kTurnRows - 1) / kTurnRows;
     // heads of a task: as many as leave 4096 waves
     int heads = 1;
     while (heads < 8 && windows * dq * (2 * int64_t(c->n_heads) + turn.n_q_heads) / (2 * heads) >= 4096) heads *= 2;
