@@ -241,18 +241,27 @@ def _ints(here, i32, *checks):
             _refuse(here, name, t, "int32", n)
 
 
-def _rows(here, name, t, heads, dim, dtypes):
+def _rows(here, name, t, heads, dim, dtypes, T=None):
     """[T][heads][dim] with dense rows on GPU ``here``; returns the elements from one token to the next."""
+    try:
+        (n, h, d), (s0, s1, s2) = t.shape, t.stride()
+    except ValueError:
+        n = h = d = s0 = s1 = s2 = -1
+    if h != heads or d != dim or s2 != 1 or (s1 != dim and heads > 1) or t.dtype not in dtypes or t.get_device() != here:
+        _refuse_rows(here, name, t, heads, dim, dtypes)
+    if T is not None and n != T:
+        raise ValueError("%s must have as many tokens as the others, %d" % (name, T))
+    return s0 if n > 1 else heads * dim
+
+
+def _refuse_rows(here, name, t, heads, dim, dtypes):
     if t.dim() != 3 or t.dtype not in dtypes:
         raise ValueError("%s must be [T][%d][%d] of %s" % (name, heads, dim, " or ".join(str(d) for d in dtypes)))
-    (n, h, d), (s0, s1, s2) = t.shape, t.stride()
-    if h != heads or d != dim:
+    if tuple(t.shape[1:]) != (heads, dim):
         raise ValueError("%s must be [T][%d][%d]" % (name, heads, dim))
-    if (heads > 1 and s1 != dim) or s2 != 1:
+    if (heads > 1 and t.stride(1) != dim) or t.stride(2) != 1:
         raise ValueError("%s: one token's heads must be dense" % name)
-    if t.get_device() != here:
-        _refuse(here, name, t, "")
-    return s0 if n > 1 else heads * dim
+    _refuse(here, name, t, "")
 
 
 def _queue(stream, here):
@@ -364,29 +373,27 @@ def mbd_kv_append_rope(cache: KvCache, k, v, slots, positions, table, q=None, q_
     positions: table fp32 [n_positions][rot_dim], a row its angles' cosines, then their sines.  q
     [T][heads][head_dim] of the keys' type is turned into q_out, bf16."""
     import torch
-    here, heads, dim, T, dt = _gpu("k", k), cache.n_heads, cache.head_dim, k.shape[0], k.dtype
+    here, heads, dim, T, dt, bf16, f32 = _gpu("k", k), cache.n_heads, cache.head_dim, len(k), k.dtype, torch.bfloat16, torch.float32
     _held(here, "cache", cache)
-    ks, vs = _rows(here, "k", k, heads, dim, (torch.bfloat16, torch.float32)), _rows(here, "v", v, heads, dim, (dt,))
-    if v.shape[0] != T:
-        raise ValueError("k and v must have as many tokens")
+    ks, vs = _rows(here, "k", k, heads, dim, (bf16, f32)), _rows(here, "v", v, heads, dim, (dt,), T)
     _ints(here, torch.int32, ("slots", slots, T), ("positions", positions, T))
-    if table.dim() != 2 or table.dtype is not torch.float32 or not table.is_contiguous():
+    if table.dtype is not f32 or table.dim() != 2 or not table.is_contiguous():
         raise ValueError("table must be contiguous fp32 [n_positions][rot_dim]")
     if table.get_device() != here:
         _refuse(here, "table", table, "fp32")
-    if (q is None) != (q_out is None):
+    n_positions, rot = table.shape
+    if q is not None and q_out is not None:
+        q_heads = q.shape[1] if q.dim() == 3 else 1
+        qs, outs = _rows(here, "q", q, q_heads, dim, (dt,), T), _rows(here, "q_out", q_out, q_heads, dim, (bf16,), T)
+        rope = _ROPE.pack(table.data_ptr(), n_positions, rot, bool(interleaved), q_heads, q.data_ptr(), q_out.data_ptr(), qs, outs)
+    elif q is None and q_out is None:
+        rope = _ROPE.pack(table.data_ptr(), n_positions, rot, bool(interleaved), 0, 0, 0, 0, 0)
+    else:
         raise ValueError("q and q_out go together")
-    q_heads, q_ptr, out_ptr, qs, outs = 0, 0, 0, 0, 0
-    if q is not None:
-        if q.dim() != 3 or q.shape[0] != T or q_out.shape[0] != T:
-            raise ValueError("q and q_out must be [T][heads][head_dim], with as many tokens as k")
-        q_heads = q.shape[1]
-        qs, outs = _rows(here, "q", q, q_heads, dim, (dt,)), _rows(here, "q_out", q_out, q_heads, dim, (torch.bfloat16,))
-        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
-    rope = _ROPE.pack(table.data_ptr(), table.shape[0], table.shape[1], bool(interleaved), q_heads, q_ptr, out_ptr, qs, outs)
-    st = lib().mbd_kv_append_rope(cache._ref, rope, k.data_ptr(), v.data_ptr(), MBD_BF16 if dt is torch.bfloat16 else MBD_F32, ks, vs,
+    st = lib().mbd_kv_append_rope(cache._ref, rope, k.data_ptr(), v.data_ptr(), MBD_BF16 if dt is bf16 else MBD_F32, ks, vs,
                                   slots.data_ptr(), positions.data_ptr(), T, _queue(stream, here))
-    check(st, "mbd_kv_append_rope")
+    if st:
+        check(st, "mbd_kv_append_rope")
 
 
 def mbd_kv_gather(cache: KvCache, slots, k_out, v_out, stream=None) -> None:

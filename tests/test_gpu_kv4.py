@@ -403,6 +403,15 @@ def test_attn_row_tiles_beyond_places(dev):
     _run(dev, 256, 32, 4, 16, [9000] + [24] * 70, [1] + [24] * 70)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("opts", [{}, dict(softcap=7.0, alibi=True), dict(window=90), dict(scale=-0.1)])
+def test_attn_wide_row_tiles(dev, dim, opts):
+    """Prompts of 128 query rows and more: tiles of 64 rows, the last of them with 1 to 64, cut and whole."""
+    _run(dev, dim, 16, 1, 1, [700, 300], [128, 65], pad=1, **opts)
+    _run(dev, dim, 32, 2, 3, [90, 1000, 50, 0], [60, 43, 1, 22], qpad=8, **opts)
+    _run(dev, dim, 64, 1, 4, [9000, 80], [33, 80], **opts)
+
+
 def test_attn_prompts_beyond_places(dev):
     """More row tiles than places in few requests: the longest start first, and nothing is cut or done twice."""
     _run(dev, 64, 32, 16, 2, [500, 900, 310], [500, 400, 300])

@@ -174,7 +174,7 @@ def test_rope_binding_refuses(monkeypatch):
         call()
     for kw, what in ((dict(c=other), "the cache is on"), (dict(pos=ints(2)), "positions"), (dict(slots=ints(4)), "slots"), (dict(v=_on(1, (2, 2, 64), torch.bfloat16)), "as many"),
                      (dict(t=_on(0, (9, 64), f32)), "table is on"), (dict(t=table[:, ::2]), "contiguous fp32"), (dict(t=_on(1, (9, 64), torch.float64)), "fp32"),
-                     (dict(q=q), "go together"), (dict(q=q[:2], q_out=q_out), "as many"), (dict(q=q, q_out=q_out[:, :2]), "q_out"),
+                     (dict(q=q), "go together"), (dict(q=_on(1, (2, 4, 64), torch.bfloat16), q_out=q_out), "as many"), (dict(q=q, q_out=q_out[:, :2]), "q_out"),
                      (dict(q=q.float(), q_out=q_out), "q must"), (dict(q=q, q_out=_on(1, (3, 4, 64), f32)), "q_out"),
                      (dict(q=_on(0, (3, 4, 64), torch.bfloat16), q_out=q_out), "q is on"), (dict(q=q[..., :32], q_out=q_out), "q must")):
         with pytest.raises(ValueError, match=what):
