@@ -451,7 +451,8 @@ typedef struct {
  * queries turned into q_out, rounded to bf16 once (as mbd_kv_attn takes them).  positions [T]
  * device int32, as mbd_kv_slots writes them.  A token whose position is outside the table is
  * not stored, and its row of q_out stays as it was; a slot outside the cache skips the
- * token's key and value alone.  q_out may not overlap q, k or v.  Errors as mbd_kv_append. */
+ * token's key and value alone.  q_out may not overlap q, k or v.  Errors as mbd_kv_append (ESHAPE for T * n_q_heads *
+ * head_dim of 2^38 or more, too). */
 mbd_status mbd_kv_append_rope(const mbd_kv_cache* cache, const mbd_rope* rope, const void* k, const void* v,
                               int32_t dtype, int64_t k_stride, int64_t v_stride, const int32_t* slots,
                               const int32_t* positions, int32_t T, void* stream);
@@ -498,9 +499,8 @@ typedef struct {
  * were.  Sums and statistics are fp32 (so a product q . k of codes (in 4 bits, of keys), an
  * uncapped score times log2(e), and 2^8 times the sum of a channel's |v| over the tokens a query
  * sees have to stay below 2^127); softmax weights (in 8 bits times value scales) enter the second
- * product as bf16, each off by at most 2^-8 of itself.  In 4 bits q enters the first product as
- * the sum of two 8-bit floats, each channel off by at most 2^-21 of its row's largest.  The order
- * of every sum depends on the arguments alone.
+ * product as bf16, each off by at most 2^-8 of itself.  The order of every sum depends on the
+ * arguments alone.
  * ws: device workspace of mbd_kv_attn_workspace_bytes, 16-byte aligned, contents
  * overwritten; may be NULL where that is 0.  One made for the most n_seqs, max_new and
  * max_blocks of a program serves its smaller calls of the same heads too.  Calls that

@@ -800,6 +800,7 @@ static mbd_status check_rope(const mbd_kv_cache* cache, const mbd_rope* r, const
     const int64_t row = int64_t(r->n_q_heads) * cache->head_dim;
     if (r->n_q_heads && (r->q_stride < row || r->q_out_stride < row || r->q_stride % 8 || r->q_out_stride % 8))
         return fail(MBD_ESHAPE, "token strides of queries must be multiples of 8 and at least n_q_heads * head_dim");
+    if (int64_t(T) * row >= int64_t(1) << 38) return fail(MBD_ESHAPE, "T * n_q_heads * head_dim is 2^38 or more");
     if (T == 0) return MBD_OK;
     if (!positions) return fail(MBD_EINVAL, "NULL argument");
     if (!aligned(positions, 4)) return fail(MBD_EALIGN, "positions must be 4-byte aligned");
@@ -838,7 +839,10 @@ static mbd_status append(const mbd_kv_cache* cache, const Turn& turn, const void
     a.rows = std::min((T + window - 1) / window, 65535);
     dim3 grid(unsigned(a.columns), unsigned(a.rows));
     if (turn.table) {                    // keys and values in one row of workgroups, and the queries behind them
+        // (below 2^23 and 2^24 workgroups: of keys and values, which go on to further windows, and of queries, by check_rope)
+        a.rows = std::min(a.rows, std::max((1 << 23) / a.columns, few ? T : 1));
         const int64_t windows = (int64_t(T) + kTurnRows - 1) / kTurnRows, dq = cache->head_dim / 64;
+        // heads of a task: as many as leave 4096 waves
         while (a.q_heads < 8 && windows * dq * turn.n_q_heads / (2 * a.q_heads) >= 4096) a.q_heads *= 2;
         const int64_t tasks = windows * dq * ((turn.n_q_heads + a.q_heads - 1) / a.q_heads);
         grid = dim3(unsigned(int64_t(a.columns) * a.rows + (tasks + 3) / 4));

@@ -1,19 +1,15 @@
 // Attention over the 4-bit KV cache (MBD_KV_MXFP4): the products of kv_attn.hip,
 //   S^T [tokens][rows] = K [tokens][d] Q^T,  O^T [d][rows] += V^T [d][tokens] P^T
-// with the same sharing of the work.
+// on bf16 matrix instructions, with the same sharing of the work.
 //
-// Keys go to the matrix cores as they are stored: v_mfma_scale_f32_16x16x128_f8f6f4 takes e2m1 codes with a
-// power of two for each 32 along the sum, which is a cached group.  Its other operand is the
-// queries in 8 bits: a bf16 of 8 significant bits is the sum of two e4m3 of 4, so a row of Q enters as
-// hi + lo, each with one power of two for the row, and the scores are those of bf16 queries (an
-// element below 2^-17 of its row's largest is off by at most 2^-21 of that).  Two such products of
-// 128 channels take the time of the four bf16 ones that they replace, and nothing is unpacked.  Where 64
-// channels are left (head_dim 64, 192), hi and lo stand in the two halves of one product and the codes
-// are given to both.
+// Keys: a lane holds 32 channels of one token, which is a group with one exponent; v_cvt_scalef32_pk_bf16_fp4 makes
+// two of them the exact bf16 values of an operand.  Values: the pairs of a byte are two channels of one token, and the
+// sum runs over tokens, whose exponents differ; so the pairs of eight tokens are sorted into operands by
+// byte permutes.
 //
-// Values become bf16 (exact; the conversion applies the exponent) and their tokens, which lie in a
-// lane's words one after the other, are paired up by byte permutes: the sum runs over tokens, and
-// their scales differ.
+// (v_mfma_scale_f32_16x16x128_f8f6f4 would take the keys as they are stored, and the queries as the sum of two e4m3.  But
+// it cuts products some 17 bits below the largest of a sum, exponents of groups included: scores were off by
+// 1e-5 where these are by 1e-7, and that is what a log-sum-exp loses.)
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -23,43 +19,17 @@
 namespace mbd {
 namespace kv {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
 constexpr int per_cu4(int dq, int nt) { return nt == 1 ? (dq <= 2 ? 4 : dq == 3 ? 3 : 2) : (dq == 1 ? 4 : dq == 2 ? 3 : 2); }
-
-// Eight bf16 of a query row over 2^(E - 7), E the exponent of the row's largest: below 256, as hi + lo / 16,
-// both e4m3.  The rest behind hi is at most half of its step, 2^4 of 256, so 16 of them fit as well.
-struct QuerySplit { u32x2 hi, lo; };
-
-__device__ __forceinline__ QuerySplit split_query(const u32x4 w, float down) {
-    QuerySplit r;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const uint32_t a = w[2 * q], b = w[2 * q + 1];
-        const float x[4] = {__uint_as_float(a << 16) * down, __uint_as_float(a & 0xffff0000u) * down, __uint_as_float(b << 16) * down,
-                            __uint_as_float(b & 0xffff0000u) * down};
-        int h = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
-        h = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], h, true);
-        int l = __builtin_amdgcn_cvt_pk_fp8_f32((x[0] - __builtin_amdgcn_cvt_f32_fp8(h, 0)) * 16.f, (x[1] - __builtin_amdgcn_cvt_f32_fp8(h, 1)) * 16.f, 0, false);
-        l = __builtin_amdgcn_cvt_pk_fp8_f32((x[2] - __builtin_amdgcn_cvt_f32_fp8(h, 2)) * 16.f, (x[3] - __builtin_amdgcn_cvt_f32_fp8(h, 3)) * 16.f, l, true);
-        r.hi[q] = uint32_t(h);
-        r.lo[q] = uint32_t(l);
-    }
-    return r;
-}
-
-// Keys (e2m1, format 4) times queries (e4m3, format 0); the low byte of each scale word counts.
-__device__ __forceinline__ f32x4 key_product(const u32x4 k, const u32x4 q0, const u32x4 q1, f32x4 c, uint32_t k_scale, uint32_t q_scale) {
-    const i32x8 a = {int(k[0]), int(k[1]), int(k[2]), int(k[3]), 0, 0, 0, 0};
-    const i32x8 b = {int(q0[0]), int(q0[1]), int(q0[2]), int(q0[3]), int(q1[0]), int(q1[1]), int(q1[2]), int(q1[3])};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 0, 0, int(k_scale), 0, int(q_scale));
-}
 
 // Channels 2 B and 2 B + 1 of a word of codes as bf16; of the scale its exponent bits alone count.
 template <int B>
 __device__ __forceinline__ uint32_t value_pair(uint32_t w, uint32_t scale) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, __uint_as_float(scale), B));
+}
+
+// Eight channels of a token as an operand.
+__device__ __forceinline__ bf16x8 key_operand(uint32_t w, uint32_t scale) {
+    return __builtin_bit_cast(bf16x8, u32x4{value_pair<0>(w, scale), value_pair<1>(w, scale), value_pair<2>(w, scale), value_pair<3>(w, scale)});
 }
 
 // Token i's byte of a word of four exponents, in the place of an fp32's exponent; what else stays in
@@ -108,7 +78,7 @@ __device__ __forceinline__ Item find_item_64(const AttnArgs& a, int32_t want, Se
         const int eighths = lane == 0 ? 3 : lane == 1 ? 4 : lane == 2 ? 5 : 8;
         const int room = used < a.places ? a.places - (eighths * used + 7) / 8 : (a.places + 1) / 2;
         const uint32_t share = uint32_t(float(work) * __builtin_amdgcn_rcpf(float(room)) * (1 + 0x1p-20f)) + 1;
-        const int mine = a.unit ? int(min(max(uint64_t(share) << a.unit, uint64_t(a.min_part)), uint64_t(1) << 30)) : int(max(share, uint32_t(a.min_part)));
+        const int mine = int(min(max(uint64_t(share) << a.unit, uint64_t(a.min_part)), uint64_t(1) << 30));     // (no request has as many)
         const float one_over = __builtin_amdgcn_rcpf(float(mine));
         int best = 3;
         if (used < a.places) {
@@ -176,22 +146,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) { return __buil
 template <int DQ, int NT, bool EXT, int WAVES, bool DIRECT>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVES == 16 ? 4 : per_cu4(DQ, NT)))) void attn4_kernel(AttnArgs a) {
     constexpr int D = 64 * DQ, ROWS = 16 * NT, F = DQ / 2, H = DQ % 2, S = F + H;   // slabs of 128 channels, of 64
-    // The waves' sums are joined in LDS, of one row tile all at once, of two 64 channels at a time; of one tile the
-    // queries, which are in registers by then, lie in the same place before.  Pitch: rows 4 banks apart.
+    // The waves' sums are joined in LDS, of one row tile all at once, of two 64 channels at a time.  Pitch: rows 4 banks apart.
     constexpr int SLABS = NT == 1 ? DQ : 1, PITCH = 64 * SLABS + 4;
-    typedef float Merge[ROWS][PITCH];
-    typedef u32x2 Queries[2][64][2];                     // 64 channels: [hi, lo][lane][8 channels]
-    constexpr int kMergeBytes = WAVES * int(sizeof(Merge)), kQueryBytes = NT * DQ * int(sizeof(Queries));
-    __shared__ __attribute__((aligned(16))) char lds[NT == 1 ? (kMergeBytes > kQueryBytes ? kMergeBytes : kQueryBytes) : kMergeBytes + kQueryBytes];
-    Merge* merge = reinterpret_cast<Merge*>(lds);
-    Queries* queries = reinterpret_cast<Queries*>(lds + (NT == 1 ? 0 : kMergeBytes));
+    __shared__ float merge[WAVES][ROWS][PITCH];
     __shared__ float merge_m[WAVES][ROWS], merge_l[WAVES][ROWS];
     __shared__ Share share;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, n = lane & 15;
     const int in_block = (1 << a.shift) - 1;
     const int want = blockIdx.x / uint32_t(a.n_kv), head = blockIdx.x - want * a.n_kv;
-    // One wave looks for the workgroup's share (400 operations: in every wave at once they kept the
+    // One wave looks for the workgroup's share (some hundred operations: in every wave at once they kept the
     // vector units busy for the longer part of the start); not always the same, whose SIMD would have it all.
     Share sh;
     if (DIRECT) {
@@ -239,35 +203,37 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVE
     };
     int32_t next_id = look_up(0);
 
-    // The rows of Q, split.  Lane (g, n) holds channels 16 g .. +16 of each 64 of row n: a product takes
-    // 16 of the first and 16 of the second 64 of its 128.  The waves split pieces of 8 channels in turn and
-    // leave them in LDS; of one row tile each wave then takes all into registers.  Rows past the last repeat
-    // it: they see nothing, and nothing of them is kept.
+    // Lane (g, n) holds row n's channels 32 g .. +32 of a slab of 128, four operands; of one of 64 the 16 from 32 (g % 2) +
+    // 16 (g / 2) on, two.  Two row tiles' lie in LDS, in the lanes' order.  Rows past the last repeat it: they see nothing, and
+    // nothing of them is kept.
     constexpr bool kQueryLds = NT > 1, kLean = EXT || DQ > 2;
-    constexpr int kPieces = NT * 2 * DQ, kMine = (kPieces + WAVES - 1) / WAVES;
-    __shared__ uint32_t row_top[WAVES][NT][16];
-    uint32_t q_hi[NT], q_lo[NT];         // the rows' scales
+    __shared__ u32x4 queries[kQueryLds ? NT * 2 * DQ : 1][64];
+    u32x4 held[kQueryLds ? 1 : 2 * DQ];
     int pos[NT];
     float slope[NT];
-    const uint16_t* row_at[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int r = r0 + 16 * t + n, j = token_of(a, min(r, sq.rows - 1)), qh = head * a.group + (min(r, sq.rows - 1) - j * a.group);
-        pos[t] = r < sq.rows ? sq.p0 + j : -1;
+        const int r = min(r0 + 16 * t + n, sq.rows - 1), j = token_of(a, r), qh = head * a.group + (r - j * a.group);
+        pos[t] = r0 + 16 * t + n < sq.rows ? sq.p0 + j : -1;
         slope[t] = EXT && a.slopes ? a.slopes[qh] * kLog2e : 0.f;
-        row_at[t] = a.q + int64_t(sq.row0 + j) * a.q_stride + int64_t(qh) * D + 16 * g;
-    }
-    u32x4 w[kMine];
+        const uint16_t* row = a.q + int64_t(sq.row0 + j) * a.q_stride + int64_t(qh) * D;
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-        const int piece = WAVES == 1 ? k : k * WAVES + wave, t = piece / (2 * DQ), c = piece % (2 * DQ);
-        if (kPieces % WAVES && piece >= kPieces) break;
-        w[k] = *reinterpret_cast<const u32x4*>((NT == 1 || t == 0 ? row_at[0] : row_at[NT - 1]) + 64 * (c / 2) + 8 * (c % 2));
+        for (int c = 0; c < 2 * DQ; ++c) {
+            if (kQueryLds && c % WAVES != wave) continue;
+            const int d = c < 4 * F ? c / 4 * 128 + 32 * g + c % 4 * 8 : F * 128 + g % 2 * 32 + g / 2 * 16 + c % 4 * 8;
+            const u32x4 w = *reinterpret_cast<const u32x4*>(row + d);
+            if constexpr (kQueryLds) queries[t * 2 * DQ + c][lane] = w ^ a.flip;
+            else held[c] = w;
+        }
     }
+    auto query = [&](int t, int c) {
+        if constexpr (kQueryLds) return __builtin_bit_cast(bf16x8, queries[t * 2 * DQ + c][lane]);
+        else return __builtin_bit_cast(bf16x8, held[c]);
+    };
 
-    // The first step's codes are on their way while the queries are split.
+    // The first step's codes are on their way while the queries come.
     int32_t my_id = -1;
-    u32x4 kc[kStep][S], vc[kStep][S];    // one step's codes (of a half slab's values two words)
+    u32x4 kc[kStep][S], vc[kStep][S];    // one step's codes (of a half slab two words)
     uint32_t ks[kStep][S], vs[kStep][S]; // and exponents: of the lane's key, of four tokens' values
     auto tile_at = [&](int tile, int l) {
         const int32_t id = max(__builtin_amdgcn_readlane(my_id, l), 0);
@@ -275,7 +241,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVE
     };
     // A wave's base and a lane's offset of 32 bits are the loads' own address form; the empty asms keep the
     // compiler from widening the offsets ahead of the loop (five registers, and two operations a load).
-    const uint32_t lane16 = lane * 16, half16 = lane % 32 * 16, lane8 = lane * 8;
+    const uint32_t lane16 = lane * 16, lane8 = lane * 8, key8 = lane % 32 * 16 + lane / 32 * 8;
     const uint32_t scales_at = n / 4 * 16 + 4 * g, half_scales_at = n / 8 * 16 + 4 * g;
     auto here = [](uint32_t off) {
         asm("" : "+v"(off));
@@ -291,7 +257,12 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVE
             const uint8_t *codes = a.k + at * (512 * DQ), *scales = static_cast<const uint8_t*>(a.k_scale) + at * (32 * DQ);
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                kc[h][s] = read(reinterpret_cast<const u32x4*>(codes + s * 1024 + here(s < F ? lane16 : half16)));
+                if (s < F) {
+                    kc[h][s] = read(reinterpret_cast<const u32x4*>(codes + s * 1024 + here(lane16)));
+                } else {
+                    const u32x2 w = read(reinterpret_cast<const u32x2*>(codes + s * 1024 + here(key8)));
+                    kc[h][s] = u32x4{w.x, w.y, 0, 0};
+                }
                 ks[h][s] = (scales + s * 64)[here(s < F ? uint32_t(lane) : uint32_t(lane % 32))];
             }
         }
@@ -324,62 +295,10 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVE
     };
     refill(0);
 
-    uint32_t most[NT] = {};
+    if constexpr (kQueryLds) __syncthreads();
+    else
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-        const int piece = WAVES == 1 ? k : k * WAVES + wave, t = piece / (2 * DQ);
-        if (kPieces % WAVES && piece >= kPieces) break;
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            top = max(top, max(w[k][i] & 0x7fffu, w[k][i] >> 16 & 0x7fffu));
-            w[k][i] ^= a.flip;
-        }
-        if (NT == 1 || t == 0) most[0] = max(most[0], top);
-        else most[NT - 1] = max(most[NT - 1], top);
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        // (a NaN as infinity: max would drop it)
-        most[t] = __float_as_uint(lane_max(__uint_as_float(min(most[t], 0x7f80u) << 16)));
-        if (WAVES > 1 && g == 0) row_top[wave][t][n] = most[t];
-    }
-    if (WAVES > 1) __syncthreads();
-    float down[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        uint32_t top = most[t];
-#pragma unroll
-        for (int v = 0; v < (WAVES < kPieces ? WAVES : kPieces); ++v)
-            if (WAVES > 1) top = max(top, row_top[v][t][n]);
-        const int e = max(int(top >> 23), 27) - 127;
-        down[t] = __uint_as_float(uint32_t(134 - e) << 23);               // 2^(7 - e)
-        const bool bad = top >= 0x7f800000u;                               // an infinity or NaN: the row's scores are NaN
-        q_hi[t] = bad ? 255u : uint32_t(e + 120);
-        q_lo[t] = bad ? 255u : uint32_t(e + 116);
-    }
-#pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-        const int piece = WAVES == 1 ? k : k * WAVES + wave, t = piece / (2 * DQ), c = piece % (2 * DQ);
-        if (kPieces % WAVES && piece >= kPieces) break;
-        const QuerySplit s = split_query(w[k], NT == 1 || t == 0 ? down[0] : down[NT - 1]);
-        queries[t * DQ + c / 2][0][lane][c % 2] = s.hi;
-        queries[t * DQ + c / 2][1][lane][c % 2] = s.lo;
-    }
-    if (WAVES > 1) __syncthreads();
-    else wave_sync_lds();
-    auto from_lds = [&](int t, int c, int lo) { return *reinterpret_cast<const u32x4*>(&queries[t * DQ + c][lo][lane][0]); };
-    u32x4 held[kQueryLds ? 1 : 2 * DQ];
-    if constexpr (!kQueryLds)
-#pragma unroll
-        for (int c = 0; c < DQ; ++c) {
-            held[2 * c] = from_lds(0, c, 0);
-            held[2 * c + 1] = from_lds(0, c, 1);
-        }
-    auto query = [&](int t, int c, int lo) {
-        if constexpr (kQueryLds) return from_lds(t, c, lo);
-        else return held[2 * c + lo];
-    };
+        for (int c = 0; c < 2 * DQ; ++c) held[c] ^= a.flip;
 
     f32x4 acc[4 * DQ][NT];               // 8 products of a slab of 128 channels, 4 of one of 64
     float top[NT], sum[NT];              // base of the weights (log2 domain); this lane's share of their sum
@@ -402,18 +321,18 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVE
             for (int t = 0; t < NT; ++t) s[h][t] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int c = 0; c < S; ++c)
 #pragma unroll
-            for (int c = 0; c < S; ++c)
+            for (int j = 0; j < (c < F ? 4 : 2); ++j) {
+                keep_order();
 #pragma unroll
-                for (int lo = 0; lo < (c < F ? 2 : 1); ++lo) {
-                    if (kQueryLds) keep_order();
-                    const u32x4 q0 = c < F ? query(t, 2 * c, lo) : query(t, 2 * c, 0), q1 = c < F ? query(t, 2 * c + 1, lo) : query(t, 2 * c, 1);
-                    const uint32_t scale = c < F ? (lo ? q_lo[t] : q_hi[t]) : (g < 2 ? q_hi[t] : q_lo[t]);
+                for (int h = 0; h < kStep; ++h) {
+                    const bf16x8 kf = key_operand(kc[h][c][j], ks[h][c] << 23);
 #pragma unroll
-                    for (int h = 0; h < kStep; ++h) s[h][t] = key_product(kc[h][c], q0, q1, s[h][t], ks[h][c], scale);
+                    for (int t = 0; t < NT; ++t) s[h][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, query(t, 4 * c + j), s[h][t], 0, 0, 0);
                 }
-        // (the products stay here: behind the loads, old and new codes and all queries would be held at once)
+            }
+        // (the products stay here: behind the loads, old and new codes would be held at once)
 #pragma unroll
         for (int h = 0; h < kStep; ++h)
 #pragma unroll

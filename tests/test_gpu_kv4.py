@@ -289,13 +289,11 @@ def _case(dev, dim, bs, hkv, group, lens, new, *, scale=None, softcap=0.0, windo
     weight, _, _ = kv.attention(*args)
     for i in range(n):
         mine[start[i] + most:start[i + 1]] = False
-    # du, the error of a score.  A row of q is split over 2^(7 - e), which brings its largest below 2^8 and above
-    # 2^7: hi leaves at most half of its step, lo holds that exactly where |y| >= 2^-6 (8 significant bits, 4 and
-    # 4), else within 2^-14, which is 2^-21 of the row's largest.  Then fp32 sums of 2 dim products, the factors
+    # du, the error of a score: codes under their exponents and bf16 are exact; fp32 sums of dim products, the factors
     # behind them, the cap's exponential, the bias.
     kmax = np.repeat(np.abs(kd).max((0, 2)), group, 0)[None]
     U = abs(sc) * (np.abs(q) * kmax).sum(-1).max() if T else 0.0
-    du = 2.0 ** -23 * (2 * dim * U + 8 * U) + abs(sc) * 2.0 ** -21 * (np.abs(q).max(-1) * kmax.sum(-1)).max()
+    du = 2.0 ** -23 * (dim * U + 8 * U)
     if softcap:
         du += 2.0 ** -20 * softcap
     if slopes is not None:
@@ -651,7 +649,7 @@ def test_decode_steps(dev, graph, dim, rot, pairs):
         args[5] = np.abs(vd)
         mag, _, _ = kv.attention(*args)
         top = np.abs(qt).max() * np.abs(kd).max() * dim * dim ** -0.5
-        du = (2.0 ** -23 * (2 * dim + 8) + 2.0 ** -21) * top
+        du = 2.0 ** -23 * (dim + 8) * top
         o = out.double().cpu().numpy()
         tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 * 1.01 + 2 * du + 2.0 ** -17) * mag + 1e-30
         assert (np.abs(o - want) <= tol)[mine & served].all(), "step %d" % s
