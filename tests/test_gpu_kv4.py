@@ -556,6 +556,110 @@ def test_attn_other_stream_and_graph(dev):
         assert torch.equal(t["out"], want[0]) and torch.equal(t["lse"], want[1]), "replay %d" % i
 
 
+def _formats(mbd):
+    return {"mxfp4": mbd.MBD_KV_MXFP4, "int8": mbd.MBD_KV_INT8, "e4m3": mbd.MBD_KV_E4M3}
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "int8", "e4m3"])
+@pytest.mark.parametrize("T", [40, 1500])                 # few tokens; so many that windows take them
+def test_append_and_gather_on_other_streams_and_in_graphs(dev, fmt, T):
+    """Two captured steps over caches of their own, replayed in turn among eager work, against an eager call."""
+    mbd = _mbd()
+    rng = np.random.default_rng(T)
+    heads, hq, dim, bs, blocks = 3, 6, 128, 32, T // 32 + 2
+    x = torch.from_numpy(rng.standard_normal((2, T, hq + 2 * heads, dim))).to(torch.bfloat16).to(dev)
+    table = torch.from_numpy(_table(rng, T, dim)).to(dev)
+    slots, pos = _ints(rng.permutation(blocks - 1)[:, None] * bs + np.arange(bs), dev).flatten()[:T].contiguous(), _ints(np.arange(T), dev)
+
+    def fresh():
+        c = mbd.KvCache.empty(_formats(mbd)[fmt], blocks, heads, dim, bs)
+        qkv = torch.zeros_like(x[0])
+        return c, qkv, torch.zeros((T, hq, dim), dtype=torch.bfloat16, device=dev), torch.zeros((T, heads, dim), device=dev), torch.zeros((T, heads, dim), device=dev)
+
+    def clear(t):
+        for s in t[0].tensors.values():
+            s.fill_(1)
+        for s in t[2:]:
+            s.fill_(7.0)
+
+    def step(t, s=None):
+        c, qkv, q_out, ko, vo = t
+        q, k, v = qkv[:, :hq], qkv[:, hq:hq + heads], qkv[:, hq + heads:]
+        mbd.mbd_kv_append_rope(c, k, v, slots, pos, table, q, q_out, stream=s)
+        mbd.mbd_kv_gather(c, slots, ko, vo, stream=s)
+
+    def result(t):
+        return [a.clone() for a in (*t[2:], *t[0].tensors.values())]
+
+    sets, want = [fresh() for _ in range(2)], []
+    for i in range(2):
+        clear(sets[0])
+        sets[0][1].copy_(x[i])
+        step(sets[0])
+        torch.cuda.synchronize()
+        want.append(result(sets[0]))
+    assert not torch.equal(want[0][0], want[1][0])
+    side = torch.cuda.Stream()
+    clear(sets[1])
+    sets[1][1].copy_(x[1])
+    side.wait_stream(torch.cuda.current_stream())
+    step(sets[1], side.cuda_stream)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(result(sets[1]), want[1]))
+    graphs = []
+    for t in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(t)
+        graphs.append(g)
+    for turn in range(3):
+        for i, (t, g) in enumerate(zip(sets, graphs)):
+            clear(t)
+            t[1].copy_(x[(i + turn) % 2])
+        torch.cuda.synchronize()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for i, t in enumerate(sets):
+            assert all(torch.equal(a, b) for a, b in zip(result(t), want[(i + turn) % 2])), "replay %d of graph %d" % (turn, i)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "int8"])
+def test_more_windows_than_a_launch_has_rows(dev, fmt):
+    """One call for 4.3 million tokens is what calls for 2^18 each are, written and read back."""
+    mbd = _mbd()
+    T, dim, bs, piece = 4_300_000, 64, 256, 1 << 18
+    blocks = -(-T // bs)
+    gen = torch.Generator(device=dev).manual_seed(5)
+    x = torch.randn((T, 3, dim), generator=gen, device=dev, dtype=torch.bfloat16)
+    q, k, v = x[:, :1], x[:, 1:2], x[:, 2:]
+    rng = np.random.default_rng(6)
+    table = torch.from_numpy(_table(rng, 1000, dim)).to(dev)
+    ids = torch.arange(T, device=dev, dtype=torch.int32)
+    slots, pos = blocks * bs - (ids // bs + 1) * bs + ids % bs, (ids % 1003 - 1).contiguous()       # blocks from the last to the first; some positions have no row
+    if fmt == "int8":
+        pos.clamp_(0, 999)                                # (there a block's tokens stand next to each other)
+    got = []
+    for pieces in ([(0, T)], [(a, min(a + piece, T)) for a in range(0, T, piece)]):
+        c = mbd.KvCache.empty(_formats(mbd)[fmt], blocks, 1, dim, bs)
+        for t in c.tensors.values():
+            t.fill_(1)
+        q_out, ko, vo = (torch.full((T, 1, dim), 7.0, device=dev, dtype=torch.bfloat16) for _ in range(3))
+        for a, b in pieces:
+            mbd.mbd_kv_append_rope(c, k[a:b], v[a:b], slots[a:b], pos[a:b], table, q[a:b], q_out[a:b])
+        for a, b in pieces:
+            mbd.mbd_kv_gather(c, slots[a:b], ko[a:b], vo[a:b])
+        torch.cuda.synchronize()
+        got.append((q_out, ko, vo, *c.tensors.values()))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    known = (pos >= 0) & (pos < 1000)
+    assert bool((got[0][0][~known] == 7).all()) and not bool((got[0][0][known] == 7).all(-1).any())
+    # and they are the values: 2^-2 of a group's largest apart at most (half a step of a code, a rounding to bf16)
+    off = (got[0][2][known].float() - v[known].float()).abs().amax(-1)
+    assert bool((off <= v[known].float().abs().amax(-1) * 0.26).all())
+
+
 def test_attn_repeats_bit_for_bit(dev):
     call, _, t = _case(dev, 128, 32, 4, 4, [5000, 700, 9], [1, 1, 1])
     got = []
