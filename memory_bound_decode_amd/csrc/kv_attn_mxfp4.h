@@ -10,6 +10,11 @@
 // (v_mfma_scale_f32_16x16x128_f8f6f4 would take the keys as they are stored, and the queries as the sum of two e4m3.  But
 // it cuts products some 17 bits below the largest of a sum, exponents of groups included: scores were off by
 // 1e-5 where these are by 1e-7, and that is what a log-sum-exp loses.)
+//
+// One query row tile and long contexts: bound by HBM, 32 requests of 32768 tokens (64 / 4 heads x 128, 572 MB) in 92 us,
+// 6.2 TB/s, and 5 of the join.  Short ones: by the way to the first product (4 us: share, block ids, codes) and the join's
+// launch (4 us).  Two row tiles (prompts): by the vector units, which unpack for 32 rows at a time what the matrix unit
+// then takes a fifth of the time for; 22.5 GFLOP of prompt slices in 46 us.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -6,6 +6,8 @@
 // in pieces of 16 bytes (keys) and 4 (values).  A wave takes 8 tokens x 8 octets: a line of 64 bf16
 // channels in, and where the tokens follow each other in a tile whole lines of codes out; and the same of
 // several heads one after the other, which are turned by the same angles.
+// Prompts of 19.5k tokens (32 + 8 heads x 128, bf16, turned: 250 MB in, 181 out) take 85 us, 5.0 TB/s, the rate of a copy;
+// one token 4.4, which is a launch and a chain of four loads (position, angles and keys, slot).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -134,6 +136,7 @@ constexpr int kGather4 = 4;              // tokens of one thread
 // A thread writes 16 bytes (8 bf16 or 4 fp32 channels), a wave 4 tokens x 256 bytes of keys and as much of values;
 // a line of codes, which holds 8 tokens of one group or 4 of 64 channels, is read by this workgroup alone.
 // The outputs are not read again here: streamed past the caches.
+// 32768 tokens x 8 heads x 128 to bf16 (36 MB in, 134 out): 26.1 us, 6.5 TB/s; to fp32 19.7k tokens 33.7, 5.4 TB/s.
 template <int DQ, class T>
 __global__ __launch_bounds__(256) void gather4_kernel(Cache4Args a, T* k_out, T* v_out) {
     constexpr int D = 64 * DQ, C = 16 / sizeof(T);
