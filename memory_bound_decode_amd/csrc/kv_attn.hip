@@ -483,12 +483,16 @@ static int places_of(const mbd_kv_cache* c, int nt, int waves) {
     return std::max(1, kCus * a_cu * kMaxWaves / waves / c->n_heads);
 }
 
+// Tiles of a part at least: a step a wave (8 bits, with two, three: one request of 2048 tokens 11.4, 12.7 us against
+// 10.2, a verify step of 8 x 5 13.5, 13.5 against 13.9, 8 of up to 4096 13.4, 13.7 against 13.9); of two row tiles in 4 bits
+// eight, since 32 rows are more to join (with one, and eight: a prompt of 250 tokens 18.6 and 8.8 us, 100 tokens behind 900 20.5
+// and 16.1, 50 behind 3950 31.5 and 26.8, one of 500 14.1 and 11.9; four 21.8 for 23.9 with 4 x 30 behind 1970).
+static int least_part(const mbd_kv_cache* c, const Plan& p) { return p.waves * kStep * (c->fmt == MBD_KV_MXFP4 && p.nt == 2 ? 8 : 1); }
+
 // The parts and their memory, for tiles of p->nt * 16 query rows and parts of p->waves waves.
 static void lay_out(const mbd_kv_cache* c, int64_t tiles, int64_t seq_tiles, Plan* p) {
     p->places = places_of(c, p->nt, p->waves);
-    // tiles of a part: a step a wave (with two, three: one request of 2048 tokens 11.4, 12.7 us against
-    // 10.2, a verify step of 8 x 5 13.5, 13.5 against 13.9, 8 of up to 4096 13.4, 13.7 against 13.9)
-    const int64_t least = p->waves * kStep;
+    const int64_t least = least_part(c, *p);
     p->longest = (seq_tiles + least - 1) / least;
     p->split = p->longest > 1 && p->places > 1;
     p->parts = p->split ? std::min<int64_t>(2 * p->places, tiles * p->longest) : 0;
@@ -573,8 +577,9 @@ static void launch(const AttnArgs& a, const Plan& p, int64_t items, bool ext, hi
         // (at most four workgroups of four rows a tile: where few tiles are split, most find nothing to do)
         // few row tiles can have many parts each: more waves over them (four against one, one request of
         // 131072 tokens 58.8 and 69.3 us, 8 of up to 4096 13.9 and 14.8, one of 500 10.0 and 8.9; with more row
-        // tiles, 32 of up to 8192 54.9 and 53.7, a verify step of 8 x 5 15.3 and 14.2)
-        if (a.n_seqs * int64_t(p.row_tiles) * 8 >= p.places) join(join_kernel<DQ, 1, 4>, 1, 4, 4);
+        // tiles, 32 of up to 8192 54.9 and 53.7, a verify step of 8 x 5 15.3 and 14.2; 4 bits, two row tiles, sixteen against one,
+        // 50 tokens behind 3950 26.9 and 22.4, 2 x 9 behind 7990 24.6 and 22.8, 16 behind 32750 30.6 and 34.4)
+        if (a.n_seqs * int64_t(p.row_tiles) * (FMT == MBD_KV_MXFP4 && NT == 2 ? 24 : 8) >= p.places) join(join_kernel<DQ, 1, 4>, 1, 4, 4);
         else if constexpr (FMT == MBD_KV_MXFP4) join(join_kernel<DQ, 16, 1>, 16, 1, 16);
         else join(join_kernel<DQ, 4, 4>, 4, 4, 4);
     }
@@ -677,7 +682,7 @@ mbd_status mbd_kv_attn(const mbd_kv_cache* cache, const mbd_kv_attn_args* args, 
     a.group = p.group;
     a.per_group = uint32_t(((uint64_t(1) << 32) + p.group - 1) / p.group);
     a.row_shift = p.nt == 1 ? 4 : 5;
-    a.min_part = p.waves * kv::kStep;
+    a.min_part = kv::least_part(cache, p);
     a.places = p.places;
     a.unit = p.unit;
     a.n_splits = int32_t(std::min<int64_t>(p.splits, used));
