@@ -498,9 +498,9 @@ typedef struct {
  * NULL.  Rows of no request, and a request's rows past its first max_new, stay as they
  * were.  Sums and statistics are fp32 (so a product q . k of codes (in 4 bits, of keys), an
  * uncapped score times log2(e), and 2^8 times the sum of a channel's |v| over the tokens a query
- * sees have to stay below 2^127); softmax weights (in 8 bits times value scales) enter the second
- * product as bf16, each off by at most 2^-8 of itself.  The order of every sum depends on the
- * arguments alone.
+ * sees have to stay below 2^127); softmax weights enter the second product as bf16: in 8 bits,
+ * times value scales, one each, off by at most 2^-8 of itself; in 4 bits two, whose sum is off by
+ * 2^-16.  The order of every sum depends on the arguments alone.
  * ws: device workspace of mbd_kv_attn_workspace_bytes, 16-byte aligned, contents
  * overwritten; may be NULL where that is 0.  One made for the most n_seqs, max_new and
  * max_blocks of a program serves its smaller calls of the same heads too.  Calls that

@@ -345,7 +345,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVE
         keep_order();
         if (more) load_keys(next_tile, l + kStep);
         keep_order();
-        bf16x8 pf[NT];
+        bf16x8 pf[NT], rest[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             float u[kStep][4];
@@ -396,9 +396,21 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVE
                     p[h][i] = __builtin_amdgcn_exp2f(EXT ? u[h][i] - base : __builtin_fmaf(u[h][i], a.to_score, -base));
                     sum[t] += p[h][i];
                 }
-            // The matrix unit takes bf16: a weight is off by at most 2^-8 of itself.  The sums are of the weights before it.
-            const u32x4 w = {pack_bf16(p[0][0], p[0][1]), pack_bf16(p[0][2], p[0][3]), pack_bf16(p[1][0], p[1][1]), pack_bf16(p[1][2], p[1][3])};
+            // The matrix unit takes bf16: a weight goes in as the nearest one, and what that leaves of it as a second operand,
+            // off by 2^-16 of itself together, so that o is off by its own rounding to bf16 alone (1.65e-3 in the mean; with the
+            // first operand alone 1.9e-3 to 2.1e-3, and up to 2^-8 of the weighted |v| where few tokens have the weight).  The
+            // first alone and both: 32 requests of 32768 tokens 98.0 and 100 us, of up to 8192 34.3 and 35.2, prompt slices 47.2
+            // and 52.8, one prompt of 4000 tokens 184 and 215, of which 20 are the products; put off behind the next two
+            // channels' conversions, or with the remainder from a dot product of pairs, they take as long.
+            u32x4 w, r;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = p[i / 2][i % 2 * 2], y = p[i / 2][i % 2 * 2 + 1];
+                w[i] = pack_bf16(x, y);
+                r[i] = pack_bf16(x - __uint_as_float(w[i] << 16), y - __uint_as_float(w[i] & 0xffff0000u));
+            }
             pf[t] = __builtin_bit_cast(bf16x8, w);
+            rest[t] = __builtin_bit_cast(bf16x8, r);
         }
         if (!whole) {
             // tokens that do not exist may have any codes and exponents, and a zero weight does not silence a
@@ -440,6 +452,11 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVE
                 for (int t = 0; t < NT; ++t) {
                     acc[8 * c + 2 * B][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even, pf[t], acc[8 * c + 2 * B][t], 0, 0, 0);
                     acc[8 * c + 2 * B + 1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd, pf[t], acc[8 * c + 2 * B + 1][t], 0, 0, 0);
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    acc[8 * c + 2 * B][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(even, rest[t], acc[8 * c + 2 * B][t], 0, 0, 0);
+                    acc[8 * c + 2 * B + 1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd, rest[t], acc[8 * c + 2 * B + 1][t], 0, 0, 0);
                 }
             };
             two(Const<0>{});
