@@ -451,7 +451,10 @@ typedef struct {
  * queries turned into q_out, rounded to bf16 once (as mbd_kv_attn takes them).  positions [T]
  * device int32, as mbd_kv_slots writes them.  A token whose position is outside the table is
  * not stored, and its row of q_out stays as it was; a slot outside the cache skips the
- * token's key and value alone.  q_out may not overlap q, k or v.  Errors as mbd_kv_append
+ * token's key and value alone.  In 8 bits a token that is not stored still stands among its
+ * block's tokens: it does not count for the scale, its place keeps what it holds, rounded anew
+ * like the tokens before where the scale grows, and at a block's first place it begins the block
+ * (nothing held before counts).  q_out may not overlap q, k or v.  Errors as mbd_kv_append
  * (ESHAPE for T * n_q_heads * head_dim of 2^36 or more, too). */
 mbd_status mbd_kv_append_rope(const mbd_kv_cache* cache, const mbd_rope* rope, const void* k, const void* v,
                               int32_t dtype, int64_t k_stride, int64_t v_stride, const int32_t* slots,

@@ -320,11 +320,11 @@ __device__ __forceinline__ W encode_unit(const float* x, float div, float r, boo
     return w;
 }
 
-template <bool E4M3>
-__device__ __forceinline__ u32x4 rescale_unit(const u32x4 w, float ratio) {
-    u32x4 res;
+template <bool E4M3, class W>
+__device__ __forceinline__ W rescale_unit(const W w, float ratio) {
+    W res;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < int(sizeof(W) / 4); ++q) {
         const float v[4] = {code_value<E4M3, 0>(w[q]) * ratio, code_value<E4M3, 1>(w[q]) * ratio, code_value<E4M3, 2>(w[q]) * ratio,
                             code_value<E4M3, 3>(w[q]) * ratio};
         res[q] = encode<E4M3>(v);
@@ -365,7 +365,9 @@ template <> struct Quad<uint16_t> {
 // registers between the maximum and the codes (more are read again).  A unit is 16
 // bytes of a code tile: lane (g, m) of slab s holds, of a key tile, token m and channels
 // 64s + 16g .. +16; of a value tile, tokens 4g .. +4 and channels 64s + 4m .. +4.
-template <bool E4M3, bool V, class T, int THREADS, int KEEP>
+// GAPS: tokens whose position has no row in the table are not stored.  They belong to the run all the same, as one
+// block's scale and units can have one writer only; their places keep what they hold, as those before the run do.
+template <bool E4M3, bool V, class T, bool GAPS, int THREADS, int KEEP>
 __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, int64_t block, int fill, int end, int head, uint32_t* lds) {
     const int tid = THREADS == 64 ? threadIdx.x & 63 : threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, m = lane & 15;
@@ -377,7 +379,9 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
     const float old_scale = fill > 0 ? a.scales[V][bh] : 0.f;
     const int tile0 = fill / kTok, chunks = ((end - 1) / kTok + 1 - tile0) * slabs;   // 64 units each
 
+    static_assert(V || !GAPS, "turned keys: append_turned_keys");
     Quad<T> x[KEEP][4];
+    uint32_t there = 0;                  // GAPS: four bits a unit, its tokens that are stored (or not of the run)
     u32x4 old[THREADS == 64 ? KEEP : 1];
     auto first_token = [&](int tile) { return tile * kTok + (V ? 4 * g : m); };
     auto unit_at = [&](int tile, int s) { return reinterpret_cast<u32x4*>(codes + int64_t(tile) * kTok * D + s * 1024 + lane * 16); };
@@ -407,6 +411,18 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
                 if (c < chunks && tok >= fill && tok < end) x[i][k].load(from + (V ? k * stride : 4 * k));
             }
             if constexpr (THREADS == 64) old[i] = boundary(c < chunks, tile, s);   // early: few waves, so latency counts
+        }
+        if constexpr (GAPS) {
+            there = 0;
+#pragma unroll
+            for (int i = 0; i < KEEP; ++i) {
+                const int c = c0 + i * (THREADS / 64) + wave, first = first_token(tile0 + c / slabs);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (c < chunks && first + k >= fill && first + k < end && !has_row(a.turn, token + first + k - fill)) x[i][k].clear();
+                    else there |= 1u << (4 * i + k);
+                }
+            }
         }
     };
     constexpr int round = KEEP * (THREADS / 64);
@@ -469,7 +485,8 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[V ? 4 * j + k : 4 * k + j] = x[i][k].at(j);
             const u32x4 fresh = encode_unit<E4M3>(v, div, r, any_values);
-            if (all_new(tile)) {
+            const uint32_t stored = GAPS ? there >> (4 * i) & 15 : 15;
+            if (all_new(tile) && stored == 15) {
                 *unit_at(tile, s) = fresh;
                 continue;
             }
@@ -478,12 +495,13 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int tok = V ? first + k : first;
-                if (tok >= fill && tok < end) mask |= 255u << (8 * k);
+                if (tok >= fill && tok < end && (stored >> k & 1)) mask |= 255u << (8 * k);
             }
             u32x4 kept;
-            if constexpr (THREADS == 64) kept = old[i];
+            if (GAPS && stored != 15) kept = *unit_at(tile, s);
+            else if constexpr (THREADS == 64) kept = old[i];
             else kept = boundary(true, tile, s);
-            if (grew && fill > 0) kept = rescale_unit<E4M3>(kept, ratio);
+            if (grew && (fill > 0 || stored != 15)) kept = rescale_unit<E4M3>(kept, ratio);
             *unit_at(tile, s) = (fresh & mask) | (kept & ~mask);
         }
     }
@@ -496,8 +514,9 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int32_t token, i
 
 // append_run of turned keys.  A lane takes octets of one token each, so that a wave reads whole rows and the partners lie in
 // a lane's own row; PASSES rounds of them stay in registers between the maximum and the codes (more are turned
-// again).  An octet of new codes is eight bytes of its own; old ones are met only where the scale grew.
-template <bool E4M3, class T, int THREADS, int PASSES>
+// again).  An octet of new codes is eight bytes of its own; old ones, and those at places that are not stored, are
+// met only where the scale grew.
+template <bool E4M3, class T, bool GAPS, int THREADS, int PASSES>
 __device__ __forceinline__ void append_turned_keys(const AppendArgs& a, int32_t token, int64_t block, int fill, int end, int head, uint32_t* lds) {
     const int tid = THREADS == 64 ? threadIdx.x & 63 : threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -507,12 +526,14 @@ __device__ __forceinline__ void append_turned_keys(const AppendArgs& a, int32_t 
     const T* row0 = static_cast<const T*>(a.x[0]) + int64_t(token) * a.stride[0] + int64_t(head) * D;
     const float old_scale = fill > 0 ? a.scales[0][bh] : 0.f;
     f32x4 x[PASSES][2];
+    uint32_t stored = 0;                 // GAPS: a bit a pass, the octet's token is stored
     auto place = [&](int u, int* d) {                         // token of unit u in the run, and its first channel
         const int r = u / octets;
         *d = (u - r * octets) * 8;
         return r;
     };
     auto load = [&](int u0) {
+        stored = 0;
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
             x[i][0] = x[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -520,7 +541,12 @@ __device__ __forceinline__ void append_turned_keys(const AppendArgs& a, int32_t 
             if (u >= units) continue;
             int d;
             const int r = place(u, &d);
-            const float* row = a.turn.table + int64_t(a.turn.positions[token + r]) * a.turn.rot;
+            const int32_t p = a.turn.positions[token + r];
+            if constexpr (GAPS) {
+                if (p < 0 || p >= a.turn.n_positions) continue;
+                stored |= 1u << i;
+            }
+            const float* row = a.turn.table + int64_t(p) * a.turn.rot;
             Angles a0, a1;
             a0.load(a.turn, row, d);
             a1.load(a.turn, row, d + 4);
@@ -568,9 +594,13 @@ __device__ __forceinline__ void append_turned_keys(const AppendArgs& a, int32_t 
             if (u >= units) continue;
             int d;
             const int t = fill + place(u, &d);
+            u32x2* to = reinterpret_cast<u32x2*>(codes + int64_t(t / kTok) * kTok * D + d / 64 * 1024 + d / 16 % 4 * 256 + t % kTok * 16 + d % 16);
+            if (GAPS && !(stored >> i & 1)) {
+                if (grew) *to = rescale_unit<E4M3>(*to, ratio);
+                continue;
+            }
             const float v[8] = {x[i][0][0], x[i][0][1], x[i][0][2], x[i][0][3], x[i][1][0], x[i][1][1], x[i][1][2], x[i][1][3]};
-            *reinterpret_cast<u32x2*>(codes + int64_t(t / kTok) * kTok * D + d / 64 * 1024 + d / 16 % 4 * 256 + t % kTok * 16 + d % 16) =
-                encode_unit<E4M3, u32x2>(v, div, r, any_values);
+            *to = encode_unit<E4M3, u32x2>(v, div, r, any_values);
         }
     }
     if (grew && fill > 0)                // tokens of before: a unit of 16 bytes is one token's
@@ -581,29 +611,41 @@ __device__ __forceinline__ void append_turned_keys(const AppendArgs& a, int32_t 
         }
 }
 
+// A run of keys or of values.  Runs with gaps are rare: of their own code, in few registers.
 template <bool E4M3, class T, bool TURN, int THREADS, int KEEP>
-__device__ __forceinline__ void append_keys(const AppendArgs& a, int32_t token, int64_t block, int fill, int end, int head, uint32_t* lds) {
-    if constexpr (TURN) append_turned_keys<E4M3, T, THREADS, 4>(a, token, block, fill, end, head, lds);
-    else append_run<E4M3, false, T, THREADS, KEEP>(a, token, block, fill, end, head, lds);
+__device__ __forceinline__ void append_side(const AppendArgs& a, bool values, bool gaps, int32_t token, int64_t block, int fill, int end, int head, uint32_t* lds) {
+    if constexpr (TURN) {
+        if (gaps) {
+            if (values) append_run<E4M3, true, T, true, THREADS, 1>(a, token, block, fill, end, head, lds);
+            else append_turned_keys<E4M3, T, true, THREADS, 1>(a, token, block, fill, end, head, lds);
+            return;
+        }
+    }
+    if (values) append_run<E4M3, true, T, false, THREADS, KEEP>(a, token, block, fill, end, head, lds);
+    else if constexpr (TURN) append_turned_keys<E4M3, T, false, THREADS, 4>(a, token, block, fill, end, head, lds);
+    else append_run<E4M3, false, T, false, THREADS, KEEP>(a, token, block, fill, end, head, lds);
 }
 
 // What a wave sees of the slots from token t0 on: lane l holds token t0 + l's; a bit of
 // `starts` is a token that begins a run, of `more[0]`, `more[1]` one of the first 128 that
-// goes on with its predecessor's run (the next place of the same block).
+// goes on with its predecessor's run (the next place of the same block), of `gaps[0]`, `gaps[1]` one that is not
+// stored.
 struct Look {
     int32_t slot;
-    uint64_t starts, more[2];
+    uint64_t starts, more[2], gaps[2];
 };
 
 template <bool TURN>
 __device__ __forceinline__ Look look_at(const AppendArgs& a, int32_t t0) {
     const int lane = threadIdx.x & 63, in_block = (1 << a.shift) - 1;
     int32_t slot[2], prev[2];
+    bool gap[2] = {false, false};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int32_t t = t0 + 64 * h + lane;
-        slot[h] = t < a.T ? slot_at<TURN>(a.slots, a.turn, t) : -1;
-        prev[h] = t < a.T && t > 0 ? slot_at<TURN>(a.slots, a.turn, t - 1) : -2;
+        if (TURN && t < a.T) gap[h] = !has_row(a.turn, t);
+        slot[h] = t < a.T ? a.slots[t] : -1;
+        prev[h] = t < a.T && t > 0 ? a.slots[t - 1] : -2;
     }
     Look k;
     k.slot = slot[0];
@@ -611,27 +653,38 @@ __device__ __forceinline__ Look look_at(const AppendArgs& a, int32_t t0) {
     for (int h = 0; h < 2; ++h) {
         const bool good = slot[h] >= 0 && slot[h] < a.n_slots, goes_on = good && prev[h] == slot[h] - 1 && (slot[h] & in_block) != 0;
         k.more[h] = __ballot(goes_on);
+        k.gaps[h] = TURN ? __ballot(gap[h]) : 0;
         if (h == 0) k.starts = __ballot(good && !goes_on && lane < a.window);
     }
     return k;
 }
 
-// Tokens of the run that begins at bit l, `first` its slot.
+// The run that begins at bit l, `first` its slot: how many tokens, and whether some are not stored.
+struct Run {
+    int count;
+    bool gaps;
+};
+
 template <bool TURN>
-__device__ __forceinline__ int run_length(const AppendArgs& a, const Look& k, int32_t t0, int l, int32_t first) {
+__device__ __forceinline__ Run run_at(const AppendArgs& a, const Look& k, int32_t t0, int l, int32_t first) {
+    auto low = [](uint64_t bits, int n) { return n < 64 ? bits & ((uint64_t(1) << n) - 1) : bits; };
     const uint64_t rest = l < 63 ? k.more[0] >> (l + 1) : 0;
     int count = 1 + __builtin_ctzll(~rest);            // a shift leaves a zero at the top
-    if (count < 64 - l) return count;
-    count = 64 - l + (~k.more[1] ? __builtin_ctzll(~k.more[1]) : 64);
-    if (count < 128 - l) return count;
+    if (count < 64 - l) return {count, TURN && low(k.gaps[0] >> l, count)};
+    const int more = ~k.more[1] ? __builtin_ctzll(~k.more[1]) : 64;
+    count = 64 - l + more;
+    bool gaps = TURN && (k.gaps[0] >> l || low(k.gaps[1], more));
+    if (more < 64) return {count, gaps};
     const int lane = threadIdx.x & 63, most = (1 << a.shift) - (first & ((1 << a.shift) - 1));
     for (int at = count; at < most; at += 64) {        // a long run of a large block
         const int i = at + lane;
-        const uint64_t off = ~__ballot(i < most && t0 + l + i < a.T && slot_at<TURN>(a.slots, a.turn, t0 + l + i) == first + i);
+        const bool in = i < most && t0 + l + i < a.T && a.slots[t0 + l + i] == first + i;
+        if (TURN) gaps = gaps || __ballot(in && !has_row(a.turn, t0 + l + i));
+        const uint64_t off = ~__ballot(in);
         count = at + (off ? __builtin_ctzll(off) : 64);
         if (off) break;
     }
-    return count;
+    return {count, gaps};
 }
 
 // Few tokens: a wave for each (token, head, keys or values), busy where the token begins
@@ -654,9 +707,9 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
     const Look k = look_at<TURN>(a, t0);
     if (!k.starts) return;
     const int32_t first = __builtin_amdgcn_readfirstlane(k.slot);
-    const int fill = first & ((1 << a.shift) - 1), end = fill + run_length<TURN>(a, k, t0, 0, first);
-    if (hw >= a.n_heads) append_run<E4M3, true, T, 64, 4>(a, t0, first >> a.shift, fill, end, head, nullptr);
-    else append_keys<E4M3, T, TURN, 64, 4>(a, t0, first >> a.shift, fill, end, head, nullptr);
+    const Run run = run_at<TURN>(a, k, t0, 0, first);
+    const int fill = first & ((1 << a.shift) - 1), end = fill + run.count;
+    append_side<E4M3, T, TURN, 64, 4>(a, hw >= a.n_heads, run.gaps, t0, first >> a.shift, fill, end, head, nullptr);
 }
 
 // Many tokens: a workgroup for each (window of tokens, head, keys or values).  Long runs
@@ -688,14 +741,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TURN ? 3 : 
             const int l = __builtin_ctzll(todo);
             todo &= todo - 1;
             const int32_t first = __builtin_amdgcn_readlane(k.slot, l), token = t0 + l;
-            const int fill = first & ((1 << a.shift) - 1), end = fill + run_length<TURN>(a, k, t0, l, first);
-            if (((end - 1) / kTok + 1 - fill / kTok) * a.head_dim > 64 * kept) {
-                if (values) append_run<E4M3, true, T, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
-                else append_keys<E4M3, T, TURN, 256, kept>(a, token, first >> a.shift, fill, end, head, lds);
-            } else if (turn % 4 == wave) {
-                if (values) append_run<E4M3, true, T, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
-                else append_keys<E4M3, T, TURN, 64, kept>(a, token, first >> a.shift, fill, end, head, nullptr);
-            }
+            const Run run = run_at<TURN>(a, k, t0, l, first);
+            const int fill = first & ((1 << a.shift) - 1), end = fill + run.count;
+            if (((end - 1) / kTok + 1 - fill / kTok) * a.head_dim > 64 * kept)
+                append_side<E4M3, T, TURN, 256, kept>(a, values, run.gaps, token, first >> a.shift, fill, end, head, lds);
+            else if (turn % 4 == wave)
+                append_side<E4M3, T, TURN, 64, kept>(a, values, run.gaps, token, first >> a.shift, fill, end, head, nullptr);
         }
     }
 }

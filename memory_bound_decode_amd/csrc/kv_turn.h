@@ -24,15 +24,9 @@ __device__ __forceinline__ f32x4 load4(const uint16_t* p) {
     return f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
 }
 
-// The slot that a token goes to: none where its position has no row in the table.
-template <bool TURN>
-__device__ __forceinline__ int32_t slot_at(const int32_t* slots, const Turn& u, int32_t t) {
-    const int32_t s = slots[t];
-    if constexpr (TURN) {
-        const int32_t p = u.positions[t];
-        if (p < 0 || p >= u.n_positions) return -1;
-    }
-    return s;
+__device__ __forceinline__ bool has_row(const Turn& u, int32_t t) {
+    const int32_t p = u.positions[t];
+    return p >= 0 && p < u.n_positions;
 }
 
 // What turns channels d .. d+4 of any head of a token: x becomes x c + y s, where y are their partners.

@@ -78,10 +78,12 @@ def wanted_scale(amax, fmt):
     return np.float32(2.0 ** e)
 
 
-def append(codes, scale, x, slots, fmt):
-    """x [T][heads][dim] into codes [blocks][heads][bs][dim] and scale, both updated."""
+def append(codes, scale, x, slots, fmt, stored=None):
+    """x [T][heads][dim] into codes [blocks][heads][bs][dim] and scale, both updated.  Tokens that are not `stored` belong to
+    their block's run, but do not count for its scale, and their places keep what they hold."""
     blocks, heads, bs, _ = codes.shape
     x = x.astype(np.float64)
+    stored = np.ones(len(slots), bool) if stored is None else np.asarray(stored)
     t = 0
     while t < len(slots):
         if not 0 <= slots[t] < blocks * bs:
@@ -91,18 +93,20 @@ def append(codes, scale, x, slots, fmt):
         n = 1
         while t + n < len(slots) and fill + n < bs and slots[t + n] == slots[t] + n:
             n += 1
+        mine = stored[t:t + n]
+        places, left = fill + np.flatnonzero(mine), np.concatenate([np.arange(fill), fill + np.flatnonzero(~mine)])
         for h in range(heads):
-            new = x[t:t + n, h]
+            new = x[t:t + n, h][mine]
             fin = np.abs(new[np.isfinite(new)])
             want = wanted_scale(fin.max() if fin.size else 0.0, fmt)
             old = np.float32(scale[b, h]) if fill else np.float32(0)
             now = max(old, want)
-            if now > old and fill:
+            if now > old and left.size:
                 ratio = np.float64(np.float32(old / now))
-                codes[b, h, :fill] = encode(np.float32(decode(codes[b, h, :fill], fmt) * ratio).astype(np.float64), fmt)
+                codes[b, h, left] = encode(np.float32(decode(codes[b, h, left], fmt) * ratio).astype(np.float64), fmt)
             with np.errstate(over="ignore"):
                 q = np.float32(new / np.float64(now if now > 0 else 1.0)).astype(np.float64)
-            codes[b, h, fill:fill + n] = encode(q, fmt)
+            codes[b, h, places] = encode(q, fmt)
             scale[b, h] = now
         t += n
 
