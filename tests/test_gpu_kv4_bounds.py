@@ -82,3 +82,61 @@ def test_outputs_are_off_by_their_own_rounding(dev, dim, lens, new, hkv, group, 
         over.max(), np.abs(ref).flat[over.argmax()], weight.flat[over.argmax()])
     # the logarithm of the sum moves by as much as the scores and the sum of weights do, and is rounded itself
     assert (np.abs(lse - ref_lse) <= du + sums + 2.0 ** -19 + 2.0 ** -22 * np.abs(ref_lse)).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("rows", [1, 5, 40])                     # query heads: one row tile and two
+@pytest.mark.parametrize("window", [0, 1])
+def test_scores_keep_every_bit_of_fp32(dev, dim, rows, window):  # noqa: F811
+    """In each group one product of 0.5 to 6 among products of 2^-16 to 2^-5, all of them multiples of 2^-16 and below 2^6 when
+    added up: exact in fp32 in any order, while a sum that drops what lies 17 bits below its largest term loses some 2^-9.  A row
+    sees one token, so the log-sum-exp is its score."""
+    hkv, lens = 2, [1, 200] if window else [1, 1]
+
+    def fill(c, blocks):
+        c.fill(blocks)
+        c.k[blocks] = c.rng.integers(1, 8, c.k[blocks].shape)    # all positive
+        c.ke[blocks] = 127
+
+    def queries(rng, shape):
+        q = rng.integers(1, 128, shape) * 2.0 ** -15
+        q[..., ::32] = 1.0
+        return q
+
+    o, lse, args = _attend(dev, dim, 16, hkv, rows, lens, [1, 1], fill, queries, scale=1.0, window=window)
+    ref, ref_lse, mine = kv.attention(*args)
+    assert mine.all() and np.array_equal(ref_lse * 2 ** 16, np.rint(ref_lse * 2 ** 16)) and (ref_lse < 2 ** 6).all()
+    # log2(e) as fp32, the score times it, the sum of base and weight's logarithm, ln 2 as fp32 and the product with it: half a step
+    # (2^-24) each; the weight that the fused exponent leaves, and its logarithm: a step (2^-23) each
+    assert (np.abs(lse - ref_lse) <= 5 * 2.0 ** -24 * ref_lse + 2 * 2.0 ** -23).all()
+    np.testing.assert_array_equal(o, np.repeat(np.stack([args[5][args[3][i, (n - 1) // 16], :, (n - 1) % 16] for i, n in enumerate(lens)]), rows, 1))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("lens,new,hkv,group,width", SHAPES)
+@pytest.mark.parametrize("opts", [{}, dict(window=200)])
+def test_large_scores_within_their_roundings(dev, dim, lens, new, hkv, group, width, opts):  # noqa: F811
+    """Scores up to some hundreds, maxima that move late, weights that underflow.  Queries are whole numbers, so every product q k is
+    one of 2^-3 and below 2^14 when added up: exact in fp32 in any order."""
+    scale = 2.0
+    o, lse, args = _attend(dev, dim, 16, hkv, group, lens, new, _normal, lambda rng, s: rng.integers(-3, 4, s).astype(float), width, scale=scale, **opts)
+    ref, ref_lse, mine = kv.attention(*args)
+    q, start, table, k, v = args[0], args[1], args[3], args[4], args[5]
+    args[5] = np.abs(v)
+    weight, _, _ = kv.attention(*args)
+    U = np.zeros(lse.shape)                                      # a row's largest |score|
+    for i, n in enumerate(lens):
+        j = np.arange(n)
+        for h in range(hkv):
+            u = q[start[i]:start[i + 1], h * group:(h + 1) * group] @ k[table[i][j // 16], h, j % 16].T
+            U[start[i]:start[i + 1], h * group:(h + 1) * group] = scale * np.abs(u).max(-1)
+    assert mine.all() and U.max() > 100 and 6 * 3 * dim < 2 ** 14
+    # log2(e) times the scale as fp32 (its own error and a rounding), the product with it, its difference to the base (twice as
+    # large at most); for the log-sum-exp the sum with the base, ln 2 and the product with it: eight half steps of the score.
+    du = 8 * 2.0 ** -24 * U
+    sums = 2.0 ** -23 * (2 * np.repeat(lens, new)[:, None] + 64)
+    tol = 2.0 ** -8 * np.abs(ref) + 1.01 * (2.0 ** -16 + 2 * (du + 2.0 ** -22) + 2 * sums)[..., None] * weight + 2.0 ** -100
+    over = np.abs(o - ref) - tol
+    assert (over <= 0).all(), "worst %.3g over, of |o| %.3g and weight %.3g" % (
+        over.max(), np.abs(ref).flat[over.argmax()], weight.flat[over.argmax()])
+    assert (np.abs(lse - ref_lse) <= du + sums + 2.0 ** -22).all()
