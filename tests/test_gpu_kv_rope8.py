@@ -90,3 +90,13 @@ SHAPES = [  # heads, query heads, dim, block size, calls, rotated channels
 def test_positions_outside_the_table(dev, heads, hq, dim, bs, calls, rot, which, fmt, dtype, pairs):  # noqa: F811
     print("case rope8 unstored", heads, hq, dim, bs, calls, rot, which, fmt, dtype, pairs, flush=True)
     _steps(dev, fmt, dtype, heads, hq, dim, bs, calls, rot, pairs, UNSTORED[which])
+
+
+@pytest.mark.parametrize("heads,hq,dim,bs,calls,rot", SHAPES + [
+    (16, 0, 128, 128, [[256, 100, 5], [128, 28, 250]], 128),                   # whole blocks whose octets take two rounds and more
+    (16, 2, 256, 256, [[256, 200, 1], [300, 56, 255]], 200)])
+@pytest.mark.parametrize("fmt,dtype,pairs", [(INT8, "bf16", False), (E4M3, "f32", False), (INT8, "f32", True), (E4M3, "bf16", True)])
+def test_every_dimension_and_round(dev, heads, hq, dim, bs, calls, rot, fmt, dtype, pairs):  # noqa: F811
+    """All positions in the table: runs of a wave and of a workgroup, windows of many, at every head dimension."""
+    print("case rope8", heads, hq, dim, bs, calls, rot, fmt, dtype, pairs, flush=True)
+    _steps(dev, fmt, dtype, heads, hq, dim, bs, calls, rot, pairs, lambda rng, i, p: False, seed=1)
