@@ -140,3 +140,12 @@ def test_large_scores_within_their_roundings(dev, dim, lens, new, hkv, group, wi
     assert (over <= 0).all(), "worst %.3g over, of |o| %.3g and weight %.3g" % (
         over.max(), np.abs(ref).flat[over.argmax()], weight.flat[over.argmax()])
     assert (np.abs(lse - ref_lse) <= du + sums + 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("last", [1, 15, 16, 17, 31, 32])
+def test_rows_of_the_last_row_tile(dev, dim, last):  # noqa: F811
+    """Prompts whose query rows leave 1 to 32 in the last tile of 32, whole, and cut behind 3000 tokens."""
+    test_outputs_are_off_by_their_own_rounding(dev, dim, [32 + last, 3000 + last], [32 + last, last if last > 16 else 32 + last], 2, 1, None, {})
+    if (64 + last) % 3 == 0:
+        test_outputs_are_off_by_their_own_rounding(dev, dim, [2100, 22], [(64 + last) // 3, 1], 1, 3, None, dict(softcap=4.0, window=1700))
