@@ -59,14 +59,6 @@ __device__ __forceinline__ bf16x8 operand(uint32_t w0, uint32_t w1) {
     return __builtin_bit_cast(bf16x8, r);
 }
 
-// Workgroups a CU (waves a SIMD) that a variant's registers are held to: enough loads in
-// flight for the memory, and as many parts as there are places for them.  (With a second
-// buffer for a step's codes int8 at head_dim 128 took 213 registers, two waves, and 212 us
-// for the 1.08 GB of the largest decode step.  At head_dim 64 and one row tile the registers would let
-// in a fifth wave; counted as places they make shorter parts: 4 requests of 8000 tokens 18.1 us against
-// 15.7, a verify step of 8 x 5 15.4 against 13.9, 32 of up to 8192 32.4 against 32.3.)
-constexpr int per_cu(int dq, int nt) { return nt == 1 ? (dq <= 2 ? 4 : dq == 3 ? 3 : 2) : (dq == 1 ? 4 : dq == 2 ? 3 : 2); }
-
 // DQ = head_dim / 64, NT = tiles of 16 query rows, EXT: cap, window or distance bias, WAVES: four
 // to a part, or one, which waits for no other and finds its share alone, where the requests
 // outnumber the places that parts of four waves have.  Four waves against one there:
@@ -479,8 +471,7 @@ struct Plan {
 
 // Workgroups of a head that the chip holds.
 static int places_of(const mbd_kv_cache* c, int nt, int waves) {
-    const int dq = c->head_dim / 64, a_cu = c->fmt == MBD_KV_MXFP4 ? per_cu4(dq, nt) : per_cu(dq, nt);
-    return std::max(1, kCus * a_cu * kMaxWaves / waves / c->n_heads);
+    return std::max(1, kCus * per_cu(c->head_dim / 64, nt) * kMaxWaves / waves / c->n_heads);
 }
 
 // Tiles of a part at least: a step a wave (8 bits, with two, three: one request of 2048 tokens 11.4, 12.7 us against

@@ -24,8 +24,6 @@
 namespace mbd {
 namespace kv {
 
-constexpr int per_cu4(int dq, int nt) { return nt == 1 ? (dq <= 2 ? 4 : dq == 3 ? 3 : 2) : (dq == 1 ? 4 : dq == 2 ? 3 : 2); }
-
 // Channels 2 B and 2 B + 1 of a word of codes as bf16; of the scale its exponent bits alone count.
 template <int B>
 __device__ __forceinline__ uint32_t value_pair(uint32_t w, uint32_t scale) {
@@ -149,7 +147,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) { return __buil
 // near 0; WAVES: of a part (as attn_kernel).  DIRECT: a workgroup takes a whole request, its own number, of one row
 // tile: nothing to look for, nothing to join.
 template <int DQ, int NT, bool EXT, int WAVES, bool DIRECT>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVES == 16 ? 4 : per_cu4(DQ, NT)))) void attn4_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVES == 16 ? 4 : per_cu(DQ, NT)))) void attn4_kernel(AttnArgs a) {
     constexpr int D = 64 * DQ, ROWS = 16 * NT, F = DQ / 2, H = DQ % 2, S = F + H;   // slabs of 128 channels, of 64
     // The waves' sums are joined in LDS, of one row tile all at once, of two 64 channels at a time.  Pitch: rows 4 banks apart.
     constexpr int SLABS = NT == 1 ? DQ : 1, PITCH = 64 * SLABS + 4;

@@ -17,6 +17,15 @@ constexpr int kMaxWaves = 4;           // most waves of a workgroup; they take i
 constexpr int kCus = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// Workgroups a CU (waves a SIMD) that a variant's registers are held to, in either kernel: enough loads in
+// flight for the memory, and as many parts as there are places for them.  (With a second
+// buffer for a step's codes int8 at head_dim 128 took 213 registers, two waves, and 212 us
+// for the 1.08 GB of the largest decode step.  At head_dim 64 and one row tile the registers would let
+// in a fifth wave; counted as places they make shorter parts.  8 bits, five and four: 4 requests of 8000 tokens 18.1 and
+// 15.7 us, a verify step of 8 x 5 15.4 and 13.9, 32 of up to 8192 32.4 and 32.3; 4 bits: 4 of 8000 15.6 and 14.4, 16 of
+// 2500 17.1 and 14.4, one of 100001 24.0 and 23.3, 32 of up to 8192 27.0 and 26.7, of 16384 66 and 69.)
+constexpr int per_cu(int dq, int nt) { return nt == 1 ? (dq <= 2 ? 4 : dq == 3 ? 3 : 2) : (dq == 1 ? 4 : dq == 2 ? 3 : 2); }
+
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 template <int N> using Const = std::integral_constant<int, N>;
 
