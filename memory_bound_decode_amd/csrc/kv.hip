@@ -717,7 +717,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // in flight together; short ones (a wave's units at most) by one wave each.  13 prompts of
 // 19.5k tokens (8 heads x 128, bf16 to int8, 120 MB) take 33.6 us, 3.6 TB/s, from fp32 (200 MB) 48.6
 // us, 4.1 TB/s: the vector units work 42% of that, the rest is the chain of a workgroup's loads.
-// With TURN, and 32 heads of queries (bf16), 129 us for 450 MB, 3.5 TB/s.
+// With TURN, and 32 heads of queries (bf16), 128 us for 450 MB, 3.5 TB/s.
 template <bool E4M3, class T, bool TURN>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TURN ? 3 : sizeof(T) == 2 ? 6 : 4))) void append_window_kernel(AppendArgs a) {
     __shared__ uint32_t lds[4];

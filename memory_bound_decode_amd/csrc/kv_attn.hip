@@ -476,8 +476,8 @@ static int places_of(const mbd_kv_cache* c, int nt, int waves) {
 
 // Tiles of a part at least: a step a wave (8 bits, with two, three: one request of 2048 tokens 11.4, 12.7 us against
 // 10.2, a verify step of 8 x 5 13.5, 13.5 against 13.9, 8 of up to 4096 13.4, 13.7 against 13.9); of two row tiles in 4 bits
-// eight, since 32 rows are more to join (with one, and eight: a prompt of 250 tokens 18.6 and 8.8 us, 100 tokens behind 900 20.5
-// and 16.1, 50 behind 3950 31.5 and 26.8, one of 500 14.1 and 11.9; four 21.8 for 23.9 with 4 x 30 behind 1970).
+// eight, since 32 rows are more to join (with one, four and eight: a prompt of 250 tokens 18.7, 9.3, 9.3 us, 100 tokens behind 900
+// 20.4, 18.6, 17.3, 50 behind 3950 25.1, 23.1, 24.1, one of 500 14.9, 12.9, 12.9, 4 x 30 behind 1970 24.4, 23.1, 24.9).
 static int least_part(const mbd_kv_cache* c, const Plan& p) { return p.waves * kStep * (c->fmt == MBD_KV_MXFP4 && p.nt == 2 ? 8 : 1); }
 
 // The parts and their memory, for tiles of p->nt * 16 query rows and parts of p->waves waves.
@@ -493,8 +493,10 @@ static void lay_out(const mbd_kv_cache* c, int64_t tiles, int64_t seq_tiles, Pla
 
 // 4 bits: requests of which a query sees at most 2048 tokens are not cut, if there are workgroups for half the CUs, or
 // each has at most 64 KB to read: a CU alone reads about 45 GB/s.  (Cut and whole: a verify step of 8 x 5 tokens x 16
-// heads behind a window of 1024 14.1 and 10.7 us, 256 requests of up to 1000 45 and 34, 1000 of up to 600 89 and 46;
-// one request of 2048 x 8 heads 10.2 and 11.6.)
+// heads behind a window of 1024 13.5 and 11.2 us, 256 requests of up to 1000 47 and 38.5, 1000 of up to 600 91 and 50;
+// one request of 2048 x 8 heads 9.7 and 14.1, 8 of 1 to 2000 12.4 and 14.7, 16 of them 15.4 and 15.1.)
+// What a query may see comes from the table's width and the window, as lengths are known on the device alone: short
+// requests in a wide table are cut (the 1000 and the 256 in one of 32768 tokens take 91 and 47 us).
 static bool takes_whole(const mbd_kv_cache* c, int32_t n_seqs, int64_t seen) {
     return seen <= 128 && (int64_t(n_seqs) * c->n_heads >= kCus / 2 || seen * 17 * c->head_dim <= 65536);
 }
@@ -569,7 +571,7 @@ static void launch(const AttnArgs& a, const Plan& p, int64_t items, bool ext, hi
         // few row tiles can have many parts each: more waves over them (four against one, one request of
         // 131072 tokens 58.8 and 69.3 us, 8 of up to 4096 13.9 and 14.8, one of 500 10.0 and 8.9; with more row
         // tiles, 32 of up to 8192 54.9 and 53.7, a verify step of 8 x 5 15.3 and 14.2; 4 bits, two row tiles, sixteen against one,
-        // 50 tokens behind 3950 26.9 and 22.4, 2 x 9 behind 7990 24.6 and 22.8, 16 behind 32750 30.6 and 34.4)
+        // 50 tokens behind 3950 28.2 and 23.9, 2 x 9 behind 7990 25.4 and 23.8, 16 behind 32750 32.7 and 37.0)
         if (a.n_seqs * int64_t(p.row_tiles) * (FMT == MBD_KV_MXFP4 && NT == 2 ? 24 : 8) >= p.places) join(join_kernel<DQ, 1, 4>, 1, 4, 4);
         else if constexpr (FMT == MBD_KV_MXFP4) join(join_kernel<DQ, 16, 1>, 16, 1, 16);
         else join(join_kernel<DQ, 4, 4>, 4, 4, 4);

@@ -11,10 +11,10 @@
 // it cuts products some 17 bits below the largest of a sum, exponents of groups included: scores were off by
 // 1e-5 where these are by 1e-7, and that is what a log-sum-exp loses.)
 //
-// One query row tile and long contexts: bound by HBM, 32 requests of 32768 tokens (64 / 4 heads x 128, 572 MB) in 92 us,
-// 6.2 TB/s, and 5 of the join.  Short ones: by the way to the first product (4 us: share, block ids, codes) and the join's
-// launch (4 us).  Two row tiles (prompts): by the vector units, which unpack for 32 rows at a time what the matrix unit
-// then takes a fifth of the time for; 22.5 GFLOP of prompt slices in 46 us.
+// One query row tile and long contexts: bound by HBM, 32 requests of 32768 tokens (64 / 4 heads x 128, 572 MB) in 94 us,
+// 6.1 TB/s, and 5 of the join.  Short ones: by the way to the first product (4 us: share, block ids, codes) and the join's
+// launch (4 us).  Two row tiles (prompts): by the vector units, two thirds of the time busy, since they unpack for 32
+// rows at a time, and the matrix units, a third; 22.5 GFLOP of prompt slices in 55 us.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -207,8 +207,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVE
     int32_t next_id = look_up(0);
 
     // Lane (g, n) holds row n's channels 32 g .. +32 of a slab of 128, four operands; of one of 64 the 16 from 32 (g % 2) +
-    // 16 (g / 2) on, two.  Two row tiles' lie in LDS, in the lanes' order.  Rows past the last repeat it: they see nothing, and
-    // nothing of them is kept.
+    // 16 (g / 2) on, two.  Two row tiles' lie in LDS, in the lanes' order.  Rows past the last repeat its
+    // queries (where masks are applied they see nothing); nothing of them is kept.
     constexpr bool kQueryLds = NT > 1, kLean = EXT || DQ > 2;
     __shared__ u32x4 queries[kQueryLds ? NT * 2 * DQ : 1][64];
     u32x4 held[kQueryLds ? 1 : 2 * DQ];
@@ -469,8 +469,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(WAVE
     };
 
     // Of waves that wait alike the oldest goes first, and the youngest workgroup of a CU ended 16% after the oldest.
-    // So a wave's priority falls with what it has done: 32 requests of 32768 tokens 98.9 -> 97.0 us, 32 of up to 8192 34.4
-    // -> 33.9, one of 100001 29.1 -> 28.6.  (With two row tiles, which are not bound by loads, prompts 62 -> 65.)
+    // So a wave's priority falls with what it has done: 32 requests of 32768 tokens 107 -> 103.6 us, 32 of up to 8192 38.7
+    // -> 38.1, one of 100001 29.6 either way.  (With two row tiles, which are not bound by loads, prompts of an earlier form 62 -> 65.)
     constexpr bool kEven = NT == 1 && !DIRECT;
     const int quarter = max(mine / 4, 1);
     if (kEven) __builtin_amdgcn_s_setprio(3);

@@ -94,8 +94,9 @@ __device__ __forceinline__ int wave_scan(int v) {
     return plus_dpp<0x143, 0xc>(v);    // row_bcast 31 into rows 2 and 3
 }
 
-// The lengths are known on the device alone, so every wave cuts the work up itself.  The
-// work of a request is its tiles of tokens times its tiles of query rows; all of it over the
+// The lengths are known on the device alone, so the workgroups cut the work up themselves: in 8 bits every wave
+// for itself, by find_item; in 4 bits one wave for its workgroup, up to 64 requests by find_item_64, above by
+// find_item.  The work of a request is its tiles of tokens times its tiles of query rows; all of it over the
 // places that the chip has for a head's workgroups is a chunk of tokens, a request is cut into
 // ceil(tokens / chunk) even parts, and the workgroup's (request, part, row tile) follows from
 // the prefix sums of their counts.  One round of workgroups: two or four rounds of shorter
@@ -113,7 +114,7 @@ __device__ __forceinline__ int32_t even_part(int tiles, int parts) {     // tile
     return ((tiles - 1) / parts + kStep) / kStep * kStep;
 }
 
-// Item `want` (seq is -1 if there is none), its request, and how many row tiles are split.
+// Item `want` (seq is -1 if there is none), its request, and how many row tiles are split, for any number of requests.
 __device__ __forceinline__ Item find_item(const AttnArgs& a, int32_t want, Seq* sq, int* splits) {
     const int lane = threadIdx.x & 63;
     // Request 64 j + l is lane l's in turn j: a turn's loads are whole lines.  (With a run of
